@@ -32,7 +32,8 @@ EXPORTS = ("moe_capacity", "moe_workspace_bytes", "moe_max_kept_rows", "moe_stat
            "moe_layer_forward_dropless_gated", "moe_workspace_bytes_batches",
            "moe_schedule_batches", "moe_layer_forward_batches", "moe_packed_weights_bytes",
            "moe_pack_weights", "moe_set_gemm_timing", "moe_set_stage_timing",
-           "moe_layer_forward_noalloc")
+           "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
+           "moe_workspace_bytes_route_backward", "moe_route_backward")
 
 
 class MoeShape(ctypes.Structure):
@@ -114,7 +115,17 @@ def lib() -> ctypes.CDLL:
         L.moe_set_gemm_timing.restype = I32
         L.moe_set_stage_timing.argtypes = [P]
         L.moe_set_stage_timing.restype = I32
-        for name in ("moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
+        for name in ("moe_workspace_bytes_balance", "moe_workspace_bytes_route_backward"):
+            getattr(L, name).argtypes = [SP]
+            getattr(L, name).restype = SZ
+        # shape, logits, topk_ids, token_mask, coef, grad_scale, loss, counts, probs, dlogits, ws,
+        # ws_bytes, stream
+        L.moe_balance_loss.argtypes = ([SP, P, P, P, ctypes.c_float, ctypes.c_float] + [P] * 5 +
+                                       [SZ, P])
+        # shape, x, w_router, logits, topk_ids, dgates, dlogits, token_mask, dx_add, dx, dw, db,
+        # ws, ws_bytes, stream
+        L.moe_route_backward.argtypes = [SP] + [P] * 12 + [SZ, P]
+        for name in ("moe_balance_loss", "moe_route_backward", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
                      "moe_layer_forward", "moe_layer_forward_profiled", "moe_layer_forward_padded",
                      "moe_layer_forward_noalloc",
                      "moe_layer_forward_gated", "moe_dispatch_pairs", "moe_expert_ffn_pairs",
@@ -299,7 +310,8 @@ def moe_layer_forward_noalloc(shape, x, w_router, b_router, w1, b1, w2, b2, out,
     args = _forward_args(shape, x, w_router, b_router, w1, b1, w2, b2, out, topk_ids, topk_gates,
                          slot_of, drop_mask, expert_counts, None)
     _check(lib().moe_layer_forward_noalloc(*args[:-2], _stream(stream)),
-           "moe_layer_forward_noalloc")
+           "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
+           "moe_workspace_bytes_route_backward", "moe_route_backward")
 
 
 def moe_layer_forward_profiled(shape, x, w_router, b_router, w1, b1, w2, b2, out, events,
@@ -513,3 +525,56 @@ def moe_pack_weights(shape, w, w_packed, stream=None):
     _check(lib().moe_pack_weights(ctypes.byref(shape), _ptr(w, "w", torch.bfloat16), int(rows),
                                   int(cols), _ptr(w_packed, "w_packed"), _stream(stream)),
            "moe_pack_weights")
+
+
+def _cur(t, name: str, dtype=None, numel: int | None = None):
+    """_ptr, and the tensor has to be on the current device (the one whose stream the call takes)."""
+    p = _ptr(t, name, dtype, numel=numel)
+    if p is not None and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def workspace_bytes_balance(shape: MoeShape) -> int:
+    return int(lib().moe_workspace_bytes_balance(ctypes.byref(shape)))
+
+
+def workspace_bytes_route_backward(shape: MoeShape) -> int:
+    return int(lib().moe_workspace_bytes_route_backward(ctypes.byref(shape)))
+
+
+def moe_balance_loss(shape, logits, topk_ids, loss, expert_counts=None, expert_probs=None,
+                     dlogits=None, token_mask=None, coef=1.0, grad_scale=1.0, ws=None,
+                     stream=None):
+    """Balance loss [1] and, where given, the counts [E], mean probabilities [E] and gradient on
+    the logits [T, E]; token_mask [T] uint8, 0 for padding."""
+    n = _n(shape)
+    _check(lib().moe_balance_loss(
+        ctypes.byref(shape), _cur(logits, "logits", torch.float32, numel=n["TE"]),
+        _cur(topk_ids, "topk_ids", torch.int32, numel=n["Tk"]),
+        _cur(token_mask, "token_mask", torch.uint8, numel=n["T"]), float(coef), float(grad_scale),
+        _cur(loss, "loss", torch.float32, numel=1),
+        _cur(expert_counts, "expert_counts", torch.int32, numel=n["E"]),
+        _cur(expert_probs, "expert_probs", torch.float32, numel=n["E"]),
+        _cur(dlogits, "dlogits", torch.float32, numel=n["TE"]), _cur(ws, "ws", torch.uint8),
+        ws.numel() if ws is not None else 0, _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(shape, x, w_router, logits, topk_ids, dgates, dlogits, dx=None,
+                       dw_router=None, db_router=None, dx_add=None, token_mask=None, ws=None,
+                       stream=None):
+    """Gradients of the router: dx [T, d] in the shape's dtype, dw_router [E, d] and db_router [E]
+    in fp32, each optional; dgates [T, k] or dlogits [T, E] (or both) come in."""
+    dt, n = _dtype_of(shape), _n(shape)
+    f32 = torch.float32
+    _check(lib().moe_route_backward(
+        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
+        _cur(w_router, "w_router", dt, numel=n["wr"]), _cur(logits, "logits", f32, numel=n["TE"]),
+        _cur(topk_ids, "topk_ids", torch.int32, numel=n["Tk"]),
+        _cur(dgates, "dgates", f32, numel=n["Tk"]), _cur(dlogits, "dlogits", f32, numel=n["TE"]),
+        _cur(token_mask, "token_mask", torch.uint8, numel=n["T"]),
+        _cur(dx_add, "dx_add", dt, numel=n["x"]), _cur(dx, "dx", dt, numel=n["x"]),
+        _cur(dw_router, "dw_router", f32, numel=n["wr"]),
+        _cur(db_router, "db_router", f32, numel=n["E"]), _cur(ws, "ws", torch.uint8),
+        ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_backward")

@@ -146,14 +146,22 @@ moe_status check_ptr(const void* p, size_t a, const char* name) {
   return MOE_OK;
 }
 
-moe_status check_ws(const moe_shape& s, const void* ws, size_t ws_bytes,
-                    LayoutKind kind = kLayoutCompact) {
-  const size_t need = layout(s, kind).total;
+moe_status check_ws_bytes(size_t need, const void* ws, size_t ws_bytes) {
   if (ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   if (need && !ws) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(MOE_ERR_UNSUPPORTED, "workspace is not 256-byte aligned");
   return MOE_OK;
+}
+
+moe_status check_ws(const moe_shape& s, const void* ws, size_t ws_bytes,
+                    LayoutKind kind = kLayoutCompact) {
+  return check_ws_bytes(layout(s, kind).total, ws, ws_bytes);
+}
+
+bool overlap(const void* p, size_t p_bytes, const void* q, size_t q_bytes) {
+  const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(q);
+  return a && b && a < b + q_bytes && b < a + p_bytes;
 }
 
 #define MOE_TRY(expr)            \
@@ -1033,6 +1041,82 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
   return layer_forward_batches(batch_shape, n_batches, consolidate != 0, x, w_router, b_router,
                                w1, b1, w2, b2, out, topk_ids, topk_gates, order, batch_experts,
                                ws, ws_bytes, (hipStream_t)stream, events);
+}
+
+size_t moe_workspace_bytes_balance(const moe_shape* shape) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  return balance_ws_bytes(*shape);
+}
+
+moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, float coef, float grad_scale, float* loss,
+                            int32_t* expert_counts, float* expert_probs, float* dlogits, void* ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  if (!isfinite(coef) || !isfinite(grad_scale))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "coef = %g, grad_scale = %g must be finite", coef,
+                grad_scale);
+  if (s.T > 0) {
+    MOE_TRY(check_ptr(logits, 4, "logits"));
+    MOE_TRY(check_ptr(topk_ids, 4, "topk_ids"));
+    if (dlogits) MOE_TRY(check_ptr(dlogits, 4, "dlogits"));
+    const size_t bytes = (size_t)s.T * s.n_experts * 4;
+    if (overlap(logits, bytes, dlogits, bytes))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits overlaps logits");
+  }
+  MOE_TRY(check_ptr(loss, 4, "loss"));
+  if (expert_counts) MOE_TRY(check_ptr(expert_counts, 4, "expert_counts"));
+  if (expert_probs) MOE_TRY(check_ptr(expert_probs, 4, "expert_probs"));
+  MOE_TRY(check_ws_bytes(balance_ws_bytes(s), ws, ws_bytes));
+  hipError_t err = launch_balance(s, logits, topk_ids, token_mask, coef, grad_scale, loss,
+                                  expert_counts, expert_probs, dlogits, ws, (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "balance loss");
+}
+
+size_t moe_workspace_bytes_route_backward(const moe_shape* shape) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  return route_backward_ws_bytes(*shape);
+}
+
+moe_status moe_route_backward(const moe_shape* shape, const void* x, const void* w_router,
+                              const float* logits, const int32_t* topk_ids, const float* dgates,
+                              const float* dlogits, const uint8_t* token_mask, const void* dx_add,
+                              void* dx, float* dw_router, float* db_router, void* ws,
+                              size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  if (!dx && !dw_router && !db_router)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dx, dw_router and db_router are all NULL");
+  if (dx_add && !dx) return fail(MOE_ERR_INVALID_ARGUMENT, "dx_add without dx");
+  if (dw_router) MOE_TRY(check_data_ptr(s, dw_router, "dw_router"));
+  if (db_router) MOE_TRY(check_ptr(db_router, 4, "db_router"));
+  if (s.T > 0) {
+    if (!dgates && !dlogits)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates and dlogits are both NULL");
+    if (dgates) {
+      MOE_TRY(check_ptr(dgates, 4, "dgates"));
+      MOE_TRY(check_ptr(logits, 4, "logits"));
+      MOE_TRY(check_ptr(topk_ids, 4, "topk_ids"));
+    }
+    if (dlogits) MOE_TRY(check_ptr(dlogits, 4, "dlogits"));
+    if (dw_router) MOE_TRY(check_data_ptr(s, x, "x"));
+    if (dx) {
+      MOE_TRY(check_data_ptr(s, dx, "dx"));
+      MOE_TRY(check_data_ptr(s, w_router, "w_router"));
+      if (dx_add) MOE_TRY(check_data_ptr(s, dx_add, "dx_add"));
+      const size_t bytes = (size_t)s.T * s.d_model * elem_bytes(s);
+      if (dw_router && overlap(dx, bytes, x, bytes))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dx overlaps x");
+      if (dx_add != dx && overlap(dx, bytes, dx_add, bytes))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dx_add overlaps dx without being it");
+    }
+  }
+  MOE_TRY(check_ws_bytes(route_backward_ws_bytes(s), ws, ws_bytes));
+  hipError_t err = launch_route_backward(s, x, w_router, logits, topk_ids, dgates, dlogits,
+                                         token_mask, dx_add, dx, dw_router, db_router, ws,
+                                         (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "route backward");
 }
 
 }  // extern "C"

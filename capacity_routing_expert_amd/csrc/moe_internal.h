@@ -231,4 +231,20 @@ hipError_t launch_batch_experts(const int32_t* ids, const int32_t* order, int B,
 hipError_t launch_permute_rows(const void* src, const int32_t* idx, void* dst, int64_t n,
                                int row_bytes, bool scatter, hipStream_t st);
 
+// ---- balance loss, its gradient on the logits and the counts (balance.hip); mask, counts, probs
+// and dlogits may be NULL; T == 0 writes zeros
+size_t balance_ws_bytes(const moe_shape& s);
+hipError_t launch_balance(const moe_shape& s, const float* logits, const int32_t* ids,
+                          const uint8_t* mask, float coef, float grad_scale, float* loss,
+                          int32_t* counts, float* probs, float* dlogits, void* ws,
+                          hipStream_t st);
+
+// ---- router backward pass (route_backward.hip); dgates or dlogits, mask, dx_add and any output
+// may be NULL; T == 0 writes zeros to dw and db
+size_t route_backward_ws_bytes(const moe_shape& s);
+hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* w_router,
+                                 const float* logits, const int32_t* ids, const float* dgates,
+                                 const float* dlogits, const uint8_t* mask, const void* dx_add,
+                                 void* dx, float* dw, float* db, void* ws, hipStream_t st);
+
 }  // namespace moe

@@ -291,3 +291,51 @@ def schedule_batches(ids: torch.Tensor, batch_size: int, n_experts: int) -> dict
     B.moe_schedule_batches(shape, M, ids, res["order"], res["batch_experts"],
                            res["orig_batch_experts"])
     return res
+
+
+# ---------------------------------------------------------------- router training
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0,
+                 token_mask: torch.Tensor | None = None, grad_scale: float = 1.0,
+                 want_grad: bool = True, ws: torch.Tensor | None = None) -> dict:
+    """Balance loss of logits [T, E] and ids [T, k]: loss [1], counts [E], probs [E] and, when
+    want_grad, dlogits [T, E]."""
+    T, E = logits.shape
+    device = logits.device
+    shape = B.make_shape(T, 8, 8, E, ids.shape[1], 0, B.MOE_F32)
+    if ws is None:
+        ws = torch.empty(max(B.workspace_bytes_balance(shape), 256), dtype=torch.uint8,
+                         device=device)
+    res = {
+        "loss": torch.empty((1,), dtype=torch.float32, device=device),
+        "counts": torch.empty((E,), dtype=torch.int32, device=device),
+        "probs": torch.empty((E,), dtype=torch.float32, device=device),
+        "dlogits": torch.empty((T, E), dtype=torch.float32, device=device) if want_grad else None,
+    }
+    B.moe_balance_loss(shape, logits, ids, res["loss"], expert_counts=res["counts"],
+                       expert_probs=res["probs"], dlogits=res["dlogits"], token_mask=token_mask,
+                       coef=coef, grad_scale=grad_scale, ws=ws)
+    return res
+
+
+def route_backward(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tensor | None,
+                   ids: torch.Tensor | None, dgates: torch.Tensor | None = None,
+                   dlogits: torch.Tensor | None = None, dx_add: torch.Tensor | None = None,
+                   token_mask: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> dict:
+    """Router gradients of x [T, d] and w_router [E, d]: dx, dw_router and db_router."""
+    T, d = x.shape
+    E = w_router.shape[0]
+    dtype = B.MOE_BF16 if x.dtype == torch.bfloat16 else B.MOE_F32
+    shape = B.make_shape(T, d, 8, E, ids.shape[1] if ids is not None else 1, 0, dtype)
+    if ws is None:
+        ws = torch.empty(max(B.workspace_bytes_route_backward(shape), 256), dtype=torch.uint8,
+                         device=x.device)
+    res = {
+        "dx": torch.empty_like(x),
+        "dw_router": torch.empty((E, d), dtype=torch.float32, device=x.device),
+        "db_router": torch.empty((E,), dtype=torch.float32, device=x.device),
+    }
+    B.moe_route_backward(shape, x, w_router, logits, ids, dgates, dlogits, dx=res["dx"],
+                         dw_router=res["dw_router"], db_router=res["db_router"], dx_add=dx_add,
+                         token_mask=token_mask, ws=ws)
+    return res

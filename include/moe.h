@@ -27,7 +27,8 @@
  *     device fault shows up at the caller's next synchronisation.
  *   - Arguments are checked on the host before anything is enqueued; on any non-OK status
  *     no output has been touched.  moe_last_error() then gives a one-line reason.
- *   - T == 0 is valid and enqueues nothing.
+ *   - T == 0 is valid and enqueues nothing (moe_balance_loss and moe_route_backward write the
+ *     zeros that their sums over no tokens are).
  *   - Calls that share a workspace must not overlap (same stream, or ordered by events).
  *   - Layouts: W_r [E, d_model]; W1 [E, d_ff, d_model]; b1 [E, d_ff]; W2 [E, d_model, d_ff];
  *     b2 [E, d_model]; x and out [T, d_model]; per-assignment arrays [T, top_k], with
@@ -415,6 +416,66 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
                                      int32_t* topk_ids, float* topk_gates, int32_t* order,
                                      int32_t* batch_experts, void* ws, size_t ws_bytes,
                                      moe_stream_t stream, moe_event_t const* events);
+
+/* ---- Router training.  "Expert Networks": routing collapses onto few experts unless something
+ * spreads the tokens; these two calls give that something its gradient down to the router. */
+
+/* Workspace bytes for moe_balance_loss; 0 for an invalid shape. */
+size_t moe_workspace_bytes_balance(const moe_shape* shape);
+
+/* Balance loss, per-expert counts and the loss's gradient on the logits, in one call.  Over the
+ * n valid tokens, with c_e assignments to expert e and softmax probabilities p:
+ *   loss          = coef * E * sum_e (c_e / (n k)) * (sum_t p_te / n)
+ *   dlogits[t, e] = grad_scale * coef * E / (n k n) * p_te * (c_e - sum_j p_tj c_j)
+ * (the counts are constants of the gradient; grad_scale is the gradient arriving at the loss).
+ * Even routing gives loss = coef.
+ *   logits        [T, E] fp32 in (moe_route's logits)
+ *   topk_ids      [T, k] int32 in; an id outside [0, E) is not counted
+ *   token_mask    [T] uint8 or NULL: 0 marks a token that is not there (padding).  Its logits and
+ *                 ids are not read, its dlogits row is zero.  NULL: every token is valid
+ *   loss          [1] fp32 out
+ *   expert_counts [E] int32 out or NULL: c_e, before the capacity cut
+ *   expert_probs  [E] fp32 out or NULL: sum_t p_te / n
+ *   dlogits       [T, E] fp32 out or NULL (no gradient); must not overlap logits
+ * No valid token: all outputs are zero.  A row whose logits are all -inf has probabilities 0; NaN
+ * in a valid row reaches the outputs.  Sums over tokens are fp32 inside a workgroup and fp64
+ * across them, in a fixed order: equal calls give equal bits.  Reads shape->T, n_experts and
+ * top_k.  Errors: MOE_ERR_INVALID_ARGUMENT also for a coef or grad_scale that is not finite. */
+moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, float coef, float grad_scale, float* loss,
+                            int32_t* expert_counts, float* expert_probs, float* dlogits, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes for moe_route_backward; 0 for an invalid shape. */
+size_t moe_workspace_bytes_route_backward(const moe_shape* shape);
+
+/* Backward pass of moe_route.  With p the softmax of the logits, dp_te the sum of dgates[t, c]
+ * over the choices c with topk_ids[t, c] = e, and
+ *   dl_te = p_te * (dp_te - sum_j p_tj dp_tj) + dlogits_te:
+ *   dx = dx_add + dl W_r,   dw_router = dl^T x,   db_router = sum_t dl_t
+ *   x          [T, d_model] dtype in, or NULL when dw_router is
+ *   w_router   [E, d_model] dtype in, or NULL when dx is
+ *   logits     [T, E] fp32 in (moe_route's), or NULL when dgates is
+ *   topk_ids   [T, k] int32 in, or NULL when dgates is; an id outside [0, E) takes no gradient,
+ *              an id that a token holds twice takes both
+ *   dgates     [T, k] fp32 in or NULL: gradient on topk_gates (zero where the assignment dropped)
+ *   dlogits    [T, E] fp32 in or NULL: gradient on the logits from elsewhere (moe_balance_loss).
+ *              At least one of dgates and dlogits is given
+ *   token_mask [T] uint8 or NULL: 0 marks a token that is not there; nothing of its row is read
+ *              but dx_add, and it adds to no gradient (its dx row is dx_add's, or zero)
+ *   dx_add     [T, d_model] dtype in or NULL: a gradient that dx is added to (the residual's and
+ *              the experts'); may be dx itself, must not overlap it otherwise
+ *   dx         [T, d_model] dtype out or NULL; must not overlap x
+ *   dw_router  [E, d_model] fp32 out or NULL;  db_router [E] fp32 out or NULL
+ * At least one output is given.  Products of bf16 inputs are formed with dl in bf16 terms (three
+ * for dw_router: 24 bits; two for dx: 16 bits, against the 8 that dx keeps) and summed in fp32;
+ * f32: fp32 throughout.  Sums are in a fixed order: equal calls give equal bits.  In bf16,
+ * dw_router must be 16-byte aligned. */
+moe_status moe_route_backward(const moe_shape* shape, const void* x, const void* w_router,
+                              const float* logits, const int32_t* topk_ids, const float* dgates,
+                              const float* dlogits, const uint8_t* token_mask, const void* dx_add,
+                              void* dx, float* dw_router, float* db_router, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

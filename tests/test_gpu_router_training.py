@@ -1,0 +1,331 @@
+"""moe_balance_loss and moe_route_backward on the GPU against the 64-bit references, within the
+bounds that router_ref derives from the arithmetic."""
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import router_ref as R
+from capacity_routing_expert_amd import binding as B
+from capacity_routing_expert_amd import layer as L
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+GUARD = 64
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    B.lib()  # loud failure if the library is missing
+    yield
+    torch.cuda.synchronize()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+class Guarded:
+    """An output tensor with poisoned elements behind it, which must stay as they are."""
+
+    def __init__(self, shape, dtype):
+        n = int(np.prod(shape))
+        self.all = torch.full((n + GUARD,), 77, dtype=dtype, device=DEV)
+        self.t = self.all[:n].view(shape)
+
+    def get(self):
+        assert bool((self.all[self.t.numel():] == 77).all()), "written behind the output"
+        return self.t.double().cpu().numpy()
+
+
+def inputs(T, E, k, seed, masked, spread=1.0):
+    rng = np.random.default_rng(seed)
+    logits = (rng.standard_normal((T, E)) + spread * rng.standard_normal(E)).astype(np.float32)
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :k].astype(np.int32)
+    mask = (rng.random(T) < 0.8).astype(np.uint8) if masked else None
+    return rng, logits, ids, mask
+
+
+def run_balance(logits, ids, mask, coef=0.01, grad_scale=1.0, want_grad=True):
+    T, E = logits.shape
+    shape = B.make_shape(T, 8, 8, E, ids.shape[1], 0, B.MOE_F32)
+    out = {"loss": Guarded((1,), torch.float32), "counts": Guarded((E,), torch.int32),
+           "probs": Guarded((E,), torch.float32),
+           "dlogits": Guarded((T, E), torch.float32) if want_grad else None}
+    ws = torch.full((B.workspace_bytes_balance(shape),), 255, dtype=torch.uint8, device=DEV)
+    B.moe_balance_loss(shape, dev(logits), dev(ids), out["loss"].t, expert_counts=out["counts"].t,
+                       expert_probs=out["probs"].t,
+                       dlogits=out["dlogits"].t if want_grad else None,
+                       token_mask=None if mask is None else dev(mask), coef=coef,
+                       grad_scale=grad_scale, ws=ws)
+    return {n: o.get() for n, o in out.items() if o is not None}
+
+
+def check_balance(logits, ids, mask, got, coef=0.01, grad_scale=1.0):
+    T, E = logits.shape
+    loss, c, probs, grad = R.balance(logits, ids, mask, coef, grad_scale)
+    bl, bp, bg = R.balance_bounds(logits, ids, mask, coef, grad_scale)
+    assert np.array_equal(got["counts"], c)
+    assert abs(got["loss"][0] - loss) <= bl, (got["loss"][0], loss, bl)
+    assert np.all(np.abs(got["probs"] - probs) <= bp)
+    if "dlogits" in got:
+        bad = np.abs(got["dlogits"] - grad) > bg
+        assert not bad.any(), (np.argwhere(bad)[:4], got["dlogits"][bad][:4], grad[bad][:4])
+
+
+BALANCE = [(1, 1, 1), (1, 2, 1), (3, 4, 4), (64, 8, 2), (65, 5, 2), (700, 12, 3), (1023, 16, 1),
+           (130, 17, 3), (515, 32, 6), (333, 33, 2), (4097, 64, 6), (1000, 65, 4), (2049, 100, 8),
+           (777, 130, 8), (3000, 256, 8), (1025, 255, 3), (9000, 8, 2)]
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,E,k", BALANCE)
+def test_balance(T, E, k, masked):
+    say(f"[balance] T={T} E={E} k={k} masked={masked}")
+    _, logits, ids, mask = inputs(T, E, k, T + E, masked)
+    check_balance(logits, ids, mask, run_balance(logits, ids, mask))
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 8, 2), (3000, 64, 6), (2000, 30, 2)])
+def test_balance_edges(T, E, k):
+    """Padding that holds NaN and any id, ids outside the experts, a token with one expert twice,
+    rows of -inf, large logits, no valid token, equal counts, no gradient asked for."""
+    rng, logits, ids, _ = inputs(T, E, k, 5, False, spread=3.0)
+    mask = (rng.random(T) < 0.5).astype(np.uint8)
+    logits[mask == 0] = np.nan
+    ids[mask == 0] = 12345
+    logits[mask == 1] *= 20
+    first = np.nonzero(mask)[0]
+    ids[first[0]] = -1
+    ids[first[1]] = E
+    ids[first[2]] = 1
+    logits[first[3]] = -np.inf
+    logits[first[4], : E // 2] = -np.inf
+    mask[mask == 1] = rng.integers(1, 256, int(mask.sum()))
+    check_balance(logits, ids, mask, run_balance(logits, ids, mask, 0.5, -3.0), 0.5, -3.0)
+    assert "dlogits" not in run_balance(logits, ids, mask, want_grad=False)
+    none = run_balance(logits, ids, np.zeros(T, np.uint8))
+    assert all(not a.any() for a in none.values())
+    ids_all = np.tile(np.arange(E, dtype=np.int32), (T, 1))
+    clean = rng.standard_normal((T, E)).astype(np.float32)
+    got = run_balance(clean, ids_all, None, coef=0.25)
+    assert not got["dlogits"].any()
+    assert abs(got["loss"][0] - 0.25) <= 0.25 * (E + T + 40) * R.U
+
+
+def test_balance_nan_in_a_valid_row_is_seen():
+    _, logits, ids, _ = inputs(100, 8, 2, 3, False)
+    logits[50, 3] = np.nan
+    got = run_balance(logits, ids, None)
+    assert np.isnan(got["loss"][0]) and np.isnan(got["dlogits"][50]).all()
+    assert np.isfinite(np.delete(got["dlogits"], 50, 0)).all()
+
+
+def run_backward(x, w, logits, ids, dgates, dlogits, mask=None, add=None, bf16=False,
+                 want=("dx", "dw", "db"), in_place=False):
+    T, d = x.shape
+    E = w.shape[0]
+    dt = torch.bfloat16 if bf16 else torch.float32
+    shape = B.make_shape(T, d, 8, E, ids.shape[1] if ids is not None else 1, 0,
+                         B.MOE_BF16 if bf16 else B.MOE_F32)
+    out = {"dx": Guarded((T, d), dt), "dw": Guarded((E, d), torch.float32),
+           "db": Guarded((E,), torch.float32)}
+    ws = torch.full((B.workspace_bytes_route_backward(shape),), 255, dtype=torch.uint8, device=DEV)
+    o = lambda n: out[n].t if n in want else None
+    t = lambda a, dtype=None: None if a is None else (dev(a) if dtype is None else dev(a).to(dtype))
+    addt = t(add, dt)
+    if in_place:
+        out["dx"].t.copy_(addt)
+        addt = out["dx"].t
+    B.moe_route_backward(shape, t(x, dt) if "dw" in want else None,
+                         t(w, dt) if "dx" in want else None, t(logits), t(ids), t(dgates),
+                         t(dlogits), dx=o("dx"), dw_router=o("dw"), db_router=o("db"),
+                         dx_add=addt, token_mask=t(mask), ws=ws)
+    return {n: out[n].get() for n in want}
+
+
+def as_stored(a, bf16):
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32))
+    return t.to(torch.bfloat16).float().numpy() if bf16 else t.numpy()
+
+
+def backward_inputs(T, d, E, k, bf16, masked, seed):
+    rng, _, _, mask = inputs(T, E, k, seed, masked)
+    x = as_stored(rng.standard_normal((T, d)), bf16)
+    w = as_stored(rng.standard_normal((E, d)) / np.sqrt(d), bf16)
+    logits = (x.astype(np.float64) @ w.astype(np.float64).T).astype(np.float32)
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :k].astype(np.int32)
+    dgates = (rng.standard_normal((T, k)) * (rng.random((T, k)) < 0.9)).astype(np.float32)
+    dlogits = (0.1 * rng.standard_normal((T, E))).astype(np.float32)
+    add = as_stored(rng.standard_normal((T, d)), bf16)
+    return x, w, logits, ids, dgates, dlogits, mask, add
+
+
+def check_backward(x, w, logits, ids, dgates, dlogits, mask, add, bf16, got):
+    ref = R.route_backward(x, w, logits, ids, dgates, dlogits, mask, add)[:3]
+    bounds = R.route_backward_bounds(x, w, logits, ids, dgates, dlogits, mask, add, bf16)
+    for name, r, b in zip(("dx", "dw", "db"), ref, bounds):
+        if name in got:
+            bad = ~(np.abs(got[name] - r) <= b)
+            assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4], got[name][bad][:4],
+                                   r[bad][:4], b[bad][:4])
+
+
+BACKWARD = [(1, 8, 1, 1), (1, 64, 8, 2), (2, 136, 5, 2), (33, 8, 3, 3), (37, 136, 5, 2),
+            (64, 128, 8, 2), (129, 72, 16, 4), (127, 264, 17, 2), (300, 520, 33, 6),
+            (1000, 128, 64, 6), (513, 64, 65, 3), (200, 392, 130, 8), (257, 72, 256, 8),
+            (5000, 256, 8, 2), (2500, 1032, 4, 1)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,d,E,k", BACKWARD)
+def test_route_backward(T, d, E, k, masked, bf16):
+    say(f"[route backward] T={T} d={d} E={E} k={k} masked={masked} bf16={bf16}")
+    x, w, lg, ids, dg, dlg, mask, add = backward_inputs(T, d, E, k, bf16, masked, T + d + E)
+    add = add if masked else None
+    got = run_backward(x, w, lg, ids, dg, dlg, mask, add, bf16)
+    check_backward(x, w, lg, ids, dg, dlg, mask, add, bf16, got)
+
+
+@pytest.mark.parametrize("T,d,E,k", [(19, 7, 3, 2), (100, 33, 9, 1), (700, 130, 40, 2)])
+def test_route_backward_odd_widths_f32(T, d, E, k):
+    x, w, lg, ids, dg, dlg, _, add = backward_inputs(T, d, E, k, False, False, 4)
+    got = run_backward(x, w, lg, ids, dg, dlg, None, add)
+    check_backward(x, w, lg, ids, dg, dlg, None, add, False, got)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,d,E,k", [(70, 64, 8, 2), (600, 136, 24, 3)])
+def test_route_backward_edges(T, d, E, k, bf16):
+    """Padding that holds NaN everywhere, ids outside the experts and doubled, -inf rows; each
+    gradient alone; dgates or dlogits alone; dx added in place."""
+    x, w, lg, ids, dg, dlg, _, add = backward_inputs(T, d, E, k, bf16, False, 11)
+    rng = np.random.default_rng(2)
+    mask = (rng.random(T) < 0.6).astype(np.uint8)
+    mask[:6] = 1
+    ids[0] = -1
+    ids[1] = E + 5
+    ids[2] = 1
+    lg[3] = -np.inf
+    lg[4, :4] = -np.inf
+    pad = mask == 0
+    x[pad], lg[pad], dg[pad], dlg[pad], ids[pad] = np.nan, np.nan, np.nan, np.nan, 99999
+    full = run_backward(x, w, lg, ids, dg, dlg, mask, add, bf16)
+    check_backward(x, w, lg, ids, dg, dlg, mask, add, bf16, full)
+    if bf16:
+        assert np.array_equal(full["dx"][pad], add[pad])
+    for name in ("dx", "dw", "db"):
+        one = run_backward(x, w, lg, ids, dg, dlg, mask, add if name == "dx" else None, bf16, (name,))
+        assert np.array_equal(one[name], full[name]), name
+    same = run_backward(x, w, lg, ids, dg, dlg, mask, add, bf16, in_place=True)
+    assert all(np.array_equal(same[n], full[n]) for n in same)
+    check_backward(x, w, lg, ids, dg, None, mask, None, bf16,
+                   run_backward(x, w, lg, ids, dg, None, mask, None, bf16))
+    check_backward(x, w, None, None, None, dlg, mask, None, bf16,
+                   run_backward(x, w, None, None, None, dlg, mask, None, bf16))
+    none = run_backward(x, w, lg, ids, dg, dlg, np.zeros(T, np.uint8), None, bf16)
+    assert all(not a.any() for a in none.values())
+
+
+def test_empty_batch_writes_zero_sums():
+    shape = B.make_shape(0, 64, 8, 8, 2, 0, B.MOE_BF16)
+    loss, counts, probs = (Guarded((1,), torch.float32), Guarded((8,), torch.int32),
+                           Guarded((8,), torch.float32))
+    ws = torch.empty(max(B.workspace_bytes_balance(shape), 256), dtype=torch.uint8, device=DEV)
+    B.moe_balance_loss(shape, None, None, loss.t, expert_counts=counts.t, expert_probs=probs.t, ws=ws)
+    assert not loss.get().any() and not counts.get().any() and not probs.get().any()
+    dw, db = Guarded((8, 64), torch.float32), Guarded((8,), torch.float32)
+    ws = torch.empty(max(B.workspace_bytes_route_backward(shape), 256), dtype=torch.uint8, device=DEV)
+    B.moe_route_backward(shape, None, None, None, None, None, None, dw_router=dw.t,
+                         db_router=db.t, ws=ws)
+    assert not dw.get().any() and not db.get().any()
+
+
+@pytest.mark.parametrize("T,E", [(50, 8), (5000, 64)])
+def test_router_step_on_a_side_stream_and_in_a_graph(T, E):
+    """The router's training step as it would be used (logits and ids from moe_route, the loss's
+    gradient into the router's): the same bits on the current stream, on a side stream and from
+    graph replays with eager work between them and new inputs written into the same tensors."""
+    d, k = 256, 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn(E, d, generator=g, device=DEV) / 16).to(torch.bfloat16)
+    dg = torch.randn(T, k, generator=g, device=DEV)
+    shape = B.make_shape(T, d, 8, E, k, 0, B.MOE_BF16)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    gates = torch.empty(T, k, device=DEV)
+    logits = torch.empty(T, E, device=DEV)
+    ws = torch.empty(max(B.workspace_bytes(shape), B.workspace_bytes_balance(shape),
+                         B.workspace_bytes_route_backward(shape)), dtype=torch.uint8, device=DEV)
+
+    def step(stream=None):
+        out = [torch.empty(1, device=DEV), torch.empty(T, E, device=DEV), torch.empty_like(x),
+               torch.empty(E, d, device=DEV), torch.empty(E, device=DEV)]
+        B.moe_route(shape, x, w, None, ids, gates, logits, ws, stream=stream)
+        B.moe_balance_loss(shape, logits, ids, out[0], dlogits=out[1], coef=0.01, ws=ws,
+                           stream=stream)
+        B.moe_route_backward(shape, x, w, logits, ids, dg, out[1], dx=out[2], dw_router=out[3],
+                             db_router=out[4], ws=ws, stream=stream)
+        return out
+
+    eager = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    on_side = step(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, on_side))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for turn in range(4):
+        x.copy_(torch.randn(T, d, generator=g, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [h.clone() for h in held]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, want)), turn
+
+
+def test_router_gradient_lowers_the_loss_it_is_of():
+    """Against differences, end to end: the loss of moe_route + moe_balance_loss at W + h D and
+    W - h D (the choices held) differs by 2 h <dW, D>."""
+    T, d, E, k = 256, 64, 8, 2
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.randn(T, d, generator=g, device=DEV)
+    w = torch.randn(E, d, generator=g, device=DEV) / 8
+    shape = B.make_shape(T, d, 8, E, k, 0, B.MOE_F32)
+    ws = torch.empty(max(B.workspace_bytes(shape), 256), dtype=torch.uint8, device=DEV)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    gates, logits = torch.empty(T, k, device=DEV), torch.empty(T, E, device=DEV)
+    B.moe_route(shape, x, w, None, ids, gates, logits, ws)
+    bal = L.balance_loss(logits, ids, coef=1.0)
+    res = L.route_backward(x, w, logits, ids, dlogits=bal["dlogits"])
+    D = torch.randn(E, d, generator=g, device=DEV)
+    D /= D.norm()
+    h = 2.0 ** -6
+    held = ids.cpu().numpy()
+
+    def loss(wt):
+        lg = (x.double() @ wt.double().T).cpu().numpy()
+        return R.balance(lg, held, counts=bal["counts"].cpu().numpy().astype(np.int64))[0]
+
+    diff = (loss(w.double() + h * D.double()) - loss(w.double() - h * D.double())) / (2 * h)
+    slope = float((res["dw_router"].double() * D.double()).sum())
+    # the difference is off by h^2 / 6 times the third derivative along D; |x . D| <= |x| (about 8)
+    # per logit and the loss is about 1: at most h^2 / 6 * 8^3 * |slope scale 1|, and in practice
+    # the average over tokens of random signs; a hundredth of that bound covers the fp32 gradient
+    assert abs(diff - slope) <= h * h / 6 * 512
+    assert abs(slope) > 0
