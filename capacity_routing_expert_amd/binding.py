@@ -33,7 +33,9 @@ EXPORTS = ("moe_capacity", "moe_workspace_bytes", "moe_max_kept_rows", "moe_stat
            "moe_schedule_batches", "moe_layer_forward_batches", "moe_packed_weights_bytes",
            "moe_pack_weights", "moe_set_gemm_timing", "moe_set_stage_timing",
            "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
-           "moe_workspace_bytes_route_backward", "moe_route_backward")
+           "moe_workspace_bytes_route_backward", "moe_route_backward", "moe_quantized_codes_bytes",
+           "moe_quantized_scales_bytes", "moe_quantize_weights", "moe_dequantize_weights",
+           "moe_expert_ffn_quantized", "moe_layer_forward_quantized")
 
 
 class MoeShape(ctypes.Structure):
@@ -41,6 +43,14 @@ class MoeShape(ctypes.Structure):
                 ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("capacity", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("weight_layout", ctypes.c_int32)]
+
+
+class MoeQuantizedExperts(ctypes.Structure):
+    """moe_quantized_experts; QuantizedExperts fills it and keeps the tensors."""
+    _fields_ = [("w1_codes", ctypes.c_void_p), ("w1_scales", ctypes.c_void_p),
+                ("b1", ctypes.c_void_p), ("w2_codes", ctypes.c_void_p),
+                ("w2_scales", ctypes.c_void_p), ("b2", ctypes.c_void_p),
+                ("group", ctypes.c_int32), ("gated", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -125,7 +135,19 @@ def lib() -> ctypes.CDLL:
         # shape, x, w_router, logits, topk_ids, dgates, dlogits, token_mask, dx_add, dx, dw, db,
         # ws, ws_bytes, stream
         L.moe_route_backward.argtypes = [SP] + [P] * 12 + [SZ, P]
-        for name in ("moe_balance_loss", "moe_route_backward", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
+        L.moe_quantized_codes_bytes.argtypes = [SP, I32, I32]
+        L.moe_quantized_codes_bytes.restype = SZ
+        L.moe_quantized_scales_bytes.argtypes = [SP, I32, I32, I32]
+        L.moe_quantized_scales_bytes.restype = SZ
+        L.moe_quantize_weights.argtypes = [SP, P, I32, I32, I32, P, P, P]
+        L.moe_dequantize_weights.argtypes = [SP, P, P, I32, I32, I32, P, P]
+        QP = ctypes.POINTER(MoeQuantizedExperts)
+        L.moe_expert_ffn_quantized.argtypes = [SP, P, P, P, QP, P, P, SZ, P]
+        # shape, x, w_router, b_router, experts, out, ids, gates, slot_of, drop, counts, ws,
+        # ws_bytes, stream, events
+        L.moe_layer_forward_quantized.argtypes = [SP, P, P, P, QP] + [P] * 7 + [SZ, P, P]
+        for name in ("moe_quantize_weights", "moe_dequantize_weights", "moe_expert_ffn_quantized",
+                     "moe_layer_forward_quantized", "moe_balance_loss", "moe_route_backward", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
                      "moe_layer_forward", "moe_layer_forward_profiled", "moe_layer_forward_padded",
                      "moe_layer_forward_noalloc",
                      "moe_layer_forward_gated", "moe_dispatch_pairs", "moe_expert_ffn_pairs",
@@ -311,7 +333,9 @@ def moe_layer_forward_noalloc(shape, x, w_router, b_router, w1, b1, w2, b2, out,
                          slot_of, drop_mask, expert_counts, None)
     _check(lib().moe_layer_forward_noalloc(*args[:-2], _stream(stream)),
            "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
-           "moe_workspace_bytes_route_backward", "moe_route_backward")
+           "moe_workspace_bytes_route_backward", "moe_route_backward", "moe_quantized_codes_bytes",
+           "moe_quantized_scales_bytes", "moe_quantize_weights", "moe_dequantize_weights",
+           "moe_expert_ffn_quantized", "moe_layer_forward_quantized")
 
 
 def moe_layer_forward_profiled(shape, x, w_router, b_router, w1, b1, w2, b2, out, events,
@@ -578,3 +602,110 @@ def moe_route_backward(shape, x, w_router, logits, topk_ids, dgates, dlogits, dx
         _cur(dw_router, "dw_router", f32, numel=n["wr"]),
         _cur(db_router, "db_router", f32, numel=n["E"]), _cur(ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_backward")
+
+
+def quantized_codes_bytes(shape: MoeShape, rows: int, cols: int) -> int:
+    return int(lib().moe_quantized_codes_bytes(ctypes.byref(shape), int(rows), int(cols)))
+
+
+def quantized_scales_bytes(shape: MoeShape, rows: int, cols: int, group: int) -> int:
+    return int(lib().moe_quantized_scales_bytes(ctypes.byref(shape), int(rows), int(cols),
+                                                int(group)))
+
+
+def moe_quantize_weights(shape, w, group, codes, scales, stream=None):
+    """w [E, rows, cols] in the shape's dtype -> codes (uint8) and scales (bf16)."""
+    E, rows, cols = w.shape
+    if E != shape.n_experts:
+        raise ValueError(f"w has {E} experts, the shape {shape.n_experts}")
+    _check(lib().moe_quantize_weights(
+        ctypes.byref(shape), _cur(w, "w", _dtype_of(shape)), int(rows), int(cols), int(group),
+        _cur(codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
+        _cur(scales, "scales", torch.bfloat16,
+             numel=quantized_scales_bytes(shape, rows, cols, group) // 2), _stream(stream)),
+        "moe_quantize_weights")
+
+
+def moe_dequantize_weights(shape, codes, scales, group, w, stream=None):
+    """The values of codes and scales -> w [E, rows, cols] fp32."""
+    E, rows, cols = w.shape
+    if E != shape.n_experts:
+        raise ValueError(f"w has {E} experts, the shape {shape.n_experts}")
+    _check(lib().moe_dequantize_weights(
+        ctypes.byref(shape),
+        _cur(codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
+        _cur(scales, "scales", torch.bfloat16,
+             numel=quantized_scales_bytes(shape, rows, cols, group) // 2),
+        int(rows), int(cols), int(group), _cur(w, "w", torch.float32), _stream(stream)),
+        "moe_dequantize_weights")
+
+
+class QuantizedExperts:
+    """The 4-bit experts of one layer: the tensors of moe_quantized_experts, checked once against
+    the layer's E, d_model and d_ff."""
+
+    def __init__(self, E, d_model, d_ff, group, gated, w1_codes, w1_scales, b1, w2_codes,
+                 w2_scales, b2):
+        self.E, self.d_model, self.d_ff = int(E), int(d_model), int(d_ff)
+        self.group, self.gated = int(group), bool(gated)
+        shape = make_shape(0, d_model, d_ff, E, 1, 0, MOE_BF16)
+        rows1 = (2 if gated else 1) * self.d_ff
+        u8, bf = torch.uint8, torch.bfloat16
+        sizes = {n: quantized_codes_bytes(shape, r, c)
+                 for n, r, c in (("w1", rows1, d_model), ("w2", d_model, d_ff))}
+        scales = {n: quantized_scales_bytes(shape, r, c, group) // 2
+                  for n, r, c in (("w1", rows1, d_model), ("w2", d_model, d_ff))}
+        if not sizes["w1"] or not sizes["w2"] or not scales["w1"]:
+            raise MoeError(2, "QuantizedExperts", last_error())
+        if gated and (b1 is not None or b2 is not None):
+            raise ValueError("gated experts have no biases")
+        self.tensors = (w1_codes, w1_scales, b1, w2_codes, w2_scales, b2)
+        self.struct = MoeQuantizedExperts(
+            _ptr(w1_codes, "w1_codes", u8, numel=sizes["w1"]),
+            _ptr(w1_scales, "w1_scales", bf, numel=scales["w1"]),
+            _ptr(b1, "b1", bf, numel=self.E * self.d_ff),
+            _ptr(w2_codes, "w2_codes", u8, numel=sizes["w2"]),
+            _ptr(w2_scales, "w2_scales", bf, numel=scales["w2"]),
+            _ptr(b2, "b2", bf, numel=self.E * self.d_model), self.group, int(self.gated))
+
+    def of(self, shape):
+        """The struct, for a call of this shape on the current device."""
+        if (shape.n_experts, shape.d_model, shape.d_ff) != (self.E, self.d_model, self.d_ff):
+            raise ValueError(f"experts of E {self.E}, d_model {self.d_model}, d_ff {self.d_ff}; the "
+                             f"shape has {shape.n_experts}, {shape.d_model}, {shape.d_ff}")
+        if self.tensors[0].get_device() != torch.cuda.current_device():
+            raise ValueError(f"experts are on {self.tensors[0].device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return ctypes.byref(self.struct)
+
+
+def moe_expert_ffn_quantized(shape, x, row_token, expert_offsets, experts, y_rows, ws,
+                             stream=None):
+    """moe_expert_ffn with QuantizedExperts."""
+    dt, n = _dtype_of(shape), _n(shape)
+    _check(lib().moe_expert_ffn_quantized(
+        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
+        _cur(row_token, "row_token", torch.int32, numel=n["rows"]) if row_token.numel() else None,
+        _cur(expert_offsets, "expert_offsets", torch.int32, numel=n["E1"]), experts.of(shape),
+        _cur(y_rows, "y_rows", dt, numel=n["yrows"]) if y_rows.numel() else None,
+        _cur(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "moe_expert_ffn_quantized")
+
+
+def moe_layer_forward_quantized(shape, x, w_router, b_router, experts, out, topk_ids=None,
+                                topk_gates=None, slot_of=None, drop_mask=None,
+                                expert_counts=None, ws=None, events=None, stream=None):
+    """moe_layer_forward (or _gated) with QuantizedExperts; `events` None or 6 recorded
+    torch.cuda.Event(enable_timing=True)."""
+    dt, n = _dtype_of(shape), _n(shape)
+    i32 = torch.int32
+    _check(lib().moe_layer_forward_quantized(
+        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
+        _cur(w_router, "w_router", dt, numel=n["wr"]),
+        _cur(b_router, "b_router", torch.float32, numel=n["E"]), experts.of(shape),
+        _cur(out, "out", dt, numel=n["x"]), _cur(topk_ids, "topk_ids", i32, numel=n["Tk"]),
+        _cur(topk_gates, "topk_gates", torch.float32, numel=n["Tk"]),
+        _cur(slot_of, "slot_of", i32, numel=n["Tk"]),
+        _cur(drop_mask, "drop_mask", torch.uint8, numel=n["Tk"]),
+        _cur(expert_counts, "expert_counts", i32, numel=n["E"]), _cur(ws, "ws", torch.uint8),
+        ws.numel() if ws is not None else 0, _stream(stream), _events(events)),
+        "moe_layer_forward_quantized")

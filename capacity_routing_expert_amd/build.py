@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "dispatch.hip", "gemm_bf16.hip", "ffn_f32.hip", "combine.hip",
-           "schedule.hip", "balance.hip", "route_backward.hip"]
+           "schedule.hip", "balance.hip", "route_backward.hip", "quantize.hip",
+           "ffn_quant.hip"]
 ARCH = "gfx950"
 
 

@@ -235,6 +235,41 @@ moe_status do_dispatch(const moe_shape& s, const int32_t* ids, const float* gate
   return err == hipSuccess ? MOE_OK : device_error(err, "dispatch");
 }
 
+// 4-bit experts: the shape's limits and every pointer of the struct.
+moe_status check_quantized(const moe_shape& s, const moe_quantized_experts& q) {
+  if (s.dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "4-bit experts are bf16 only");
+  if (s.weight_layout != MOE_WEIGHTS_ROW_MAJOR)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "4-bit experts have their own storage: weight_layout %d",
+                s.weight_layout);
+  if (q.group != 32 && q.group != 64 && q.group != 128)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", q.group);
+  if (q.gated != 0 && q.gated != 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "gated = %d is not 0 or 1", q.gated);
+  MOE_TRY(check_data_ptr(s, q.w1_codes, "w1_codes"));
+  MOE_TRY(check_data_ptr(s, q.w1_scales, "w1_scales"));
+  MOE_TRY(check_data_ptr(s, q.w2_codes, "w2_codes"));
+  MOE_TRY(check_data_ptr(s, q.w2_scales, "w2_scales"));
+  if (q.gated) {
+    if (q.b1 || q.b2) return fail(MOE_ERR_INVALID_ARGUMENT, "gated experts have no biases");
+  } else {
+    MOE_TRY(check_data_ptr(s, q.b1, "b1"));
+    MOE_TRY(check_data_ptr(s, q.b2, "b2"));
+  }
+  return MOE_OK;
+}
+
+// rows x cols expert matrices at 4 bits
+moe_status check_quantize(const moe_shape* shape, int32_t rows, int32_t cols, int32_t group) {
+  MOE_TRY(check_shape(shape));
+  if (rows < 1 || cols < 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "rows = %d, cols = %d must be >= 1", rows, cols);
+  if (rows % 8 != 0 || cols % 8 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "rows = %d, cols = %d must be multiples of 8", rows, cols);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", group);
+  return MOE_OK;
+}
+
 moe_status check_forward_args(const moe_shape* shape, const void* x, const void* w_router,
                               const float* b_router, const void* w1, const void* b1,
                               const void* w2, const void* b2, void* out, void* ws,
@@ -262,7 +297,8 @@ moe_status layer_forward(const moe_shape* shape, const void* x, const void* w_ro
                          const void* b2, void* out, int32_t* topk_ids, float* topk_gates,
                          int32_t* slot_of, uint8_t* drop_mask, int32_t* expert_counts, void* ws,
                          size_t ws_bytes, hipStream_t st, moe_event_t const* events,
-                         bool padded = false, void* y_rows = nullptr, bool gated = false) {
+                         bool padded = false, void* y_rows = nullptr, bool gated = false,
+                         const moe_quantized_experts* quant = nullptr) {
   hipEvent_t tev[4], sev[4];
   const bool timed = take_timing(tev);  // both consumed by this call even if it fails
   const bool stimed = take_stage_timing(sev);
@@ -278,7 +314,9 @@ moe_status layer_forward(const moe_shape* shape, const void* x, const void* w_ro
     if (stimed) MOE_TRY(record_now(sev, 4, st));
     return timed ? record_now(tev, 4, st) : MOE_OK;
   }
-  if (gated) {
+  if (quant) {
+    MOE_TRY(check_quantized(s, *quant));
+  } else if (gated) {
     if (s.dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "the gated expert is bf16 only");
     if ((int64_t)4 * s.d_ff * s.d_model >= ((int64_t)1 << 31))
       return fail(MOE_ERR_UNSUPPORTED, "2 * d_ff * d_model bf16 weights per expert: >= 2 GiB");
@@ -319,13 +357,15 @@ moe_status layer_forward(const moe_shape* shape, const void* x, const void* w_ro
   }
   MOE_TRY(rec(2));
   MOE_TRY(run_timed_stage(timing_pair(timed, tev, 0), st, "expert up-projection", [&] {
-    return gated ? launch_ffn_up_gated(s, x, row_token, offsets, w1, h, rows, st)
-                 : launch_ffn_up(s, x, row_token, offsets, w1, b1, h, rows, st);
+    return quant   ? launch_quant_up(s, *quant, x, row_token, offsets, h, rows, st)
+           : gated ? launch_ffn_up_gated(s, x, row_token, offsets, w1, h, rows, st)
+                   : launch_ffn_up(s, x, row_token, offsets, w1, b1, h, rows, st);
   }));
   MOE_TRY(rec(3));
   MOE_TRY(run_timed_stage(timing_pair(timed, tev, 1), st, "expert down-projection", [&] {
-    return gated ? launch_ffn_down_nobias(s, h, offsets, w2, y, rows, st)
-                 : launch_ffn_down(s, h, offsets, w2, b2, y, rows, st);
+    return quant   ? launch_quant_down(s, *quant, h, offsets, y, rows, st)
+           : gated ? launch_ffn_down_nobias(s, h, offsets, w2, y, rows, st)
+                   : launch_ffn_down(s, h, offsets, w2, b2, y, rows, st);
   }));
   MOE_TRY(rec(4));
   MOE_TRY(run_timed_stage(timing_pair(stimed, sev, 1), st, "combine",
@@ -1117,6 +1157,98 @@ moe_status moe_route_backward(const moe_shape* shape, const void* x, const void*
                                          token_mask, dx_add, dx, dw_router, db_router, ws,
                                          (hipStream_t)stream);
   return err == hipSuccess ? MOE_OK : device_error(err, "route backward");
+}
+
+size_t moe_quantized_codes_bytes(const moe_shape* shape, int32_t rows, int32_t cols) {
+  if (check_quantize(shape, rows, cols, 32) != MOE_OK) return 0;
+  return (size_t)quantized_codes_bytes(shape->n_experts, rows, cols);
+}
+
+size_t moe_quantized_scales_bytes(const moe_shape* shape, int32_t rows, int32_t cols,
+                                  int32_t group) {
+  if (check_quantize(shape, rows, cols, group) != MOE_OK) return 0;
+  return (size_t)quantized_scales_count(shape->n_experts, rows, cols, group) * 2;
+}
+
+moe_status moe_quantize_weights(const moe_shape* shape, const void* w, int32_t rows, int32_t cols,
+                                int32_t group, void* codes, void* scales, moe_stream_t stream) {
+  MOE_TRY(check_quantize(shape, rows, cols, group));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_data_ptr(s, w, "w"));
+  MOE_TRY(check_ptr(codes, 16, "codes"));
+  MOE_TRY(check_ptr(scales, 16, "scales"));
+  const size_t in = (size_t)s.n_experts * rows * cols * elem_bytes(s);
+  const size_t cb = (size_t)quantized_codes_bytes(s.n_experts, rows, cols);
+  const size_t sb = (size_t)quantized_scales_count(s.n_experts, rows, cols, group) * 2;
+  if (overlap(codes, cb, w, in) || overlap(scales, sb, w, in) || overlap(codes, cb, scales, sb))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "w, codes and scales overlap");
+  hipError_t err = launch_quantize(w, s.dtype == MOE_BF16, s.n_experts, rows, cols, group, codes,
+                                   scales, (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "quantize weights");
+}
+
+moe_status moe_dequantize_weights(const moe_shape* shape, const void* codes, const void* scales,
+                                  int32_t rows, int32_t cols, int32_t group, float* w,
+                                  moe_stream_t stream) {
+  MOE_TRY(check_quantize(shape, rows, cols, group));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_ptr(codes, 16, "codes"));
+  MOE_TRY(check_ptr(scales, 16, "scales"));
+  MOE_TRY(check_ptr(w, 4, "w"));
+  const size_t out = (size_t)s.n_experts * rows * cols * 4;
+  if (overlap(codes, (size_t)quantized_codes_bytes(s.n_experts, rows, cols), w, out) ||
+      overlap(scales, (size_t)quantized_scales_count(s.n_experts, rows, cols, group) * 2, w, out))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "w overlaps codes or scales");
+  hipError_t err = launch_dequantize(codes, scales, s.n_experts, rows, cols, group, w,
+                                     (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "dequantize weights");
+}
+
+moe_status moe_expert_ffn_quantized(const moe_shape* shape, const void* x,
+                                    const int32_t* row_token, const int32_t* expert_offsets,
+                                    const moe_quantized_experts* experts, void* y_rows, void* ws,
+                                    size_t ws_bytes, moe_stream_t stream) {
+  hipEvent_t tev[4];
+  const bool timed = take_timing(tev);  // consumed by this call even if it fails
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  hipStream_t st = (hipStream_t)stream;
+  if (!experts) return fail(MOE_ERR_INVALID_ARGUMENT, "experts is NULL");
+  if (s.T == 0) return timed ? record_now(tev, 4, st) : MOE_OK;  // empty batch
+  const moe_quantized_experts& q = *experts;
+  MOE_TRY(check_quantized(s, q));
+  MOE_TRY(check_data_ptr(s, x, "x"));
+  if (max_rows(s) > 0) {
+    MOE_TRY(check_ptr(row_token, 4, "row_token"));
+    MOE_TRY(check_data_ptr(s, y_rows, "y_rows"));
+  }
+  MOE_TRY(check_ptr(expert_offsets, 4, "expert_offsets"));
+  MOE_TRY(check_ws(s, ws, ws_bytes));
+  if (max_rows(s) == 0) return timed ? record_now(tev, 4, st) : MOE_OK;
+  void* h = at<void>(ws, layout(s).h);
+  MOE_TRY(run_timed_stage(timing_pair(timed, tev, 0), st, "expert up-projection (4 bits)", [&] {
+    return launch_quant_up(s, q, x, row_token, expert_offsets, h, max_rows(s), st);
+  }));
+  return run_timed_stage(timing_pair(timed, tev, 1), st, "expert down-projection (4 bits)", [&] {
+    return launch_quant_down(s, q, h, expert_offsets, y_rows, max_rows(s), st);
+  });
+}
+
+moe_status moe_layer_forward_quantized(const moe_shape* shape, const void* x, const void* w_router,
+                                       const float* b_router,
+                                       const moe_quantized_experts* experts, void* out,
+                                       int32_t* topk_ids, float* topk_gates, int32_t* slot_of,
+                                       uint8_t* drop_mask, int32_t* expert_counts, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream,
+                                       moe_event_t const* events) {
+  if (!experts) return fail(MOE_ERR_INVALID_ARGUMENT, "experts is NULL");
+  if (events)
+    for (int i = 0; i < 6; ++i)
+      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
+  return layer_forward(shape, x, w_router, b_router, experts->w1_codes, experts->b1,
+                       experts->w2_codes, experts->b2, out, topk_ids, topk_gates, slot_of,
+                       drop_mask, expert_counts, ws, ws_bytes, (hipStream_t)stream, events, false,
+                       nullptr, experts->gated != 0, experts);
 }
 
 }  // extern "C"

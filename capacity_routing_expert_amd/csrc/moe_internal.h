@@ -247,4 +247,18 @@ hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* 
                                  const float* dlogits, const uint8_t* mask, const void* dx_add,
                                  void* dx, float* dw, float* db, void* ws, hipStream_t st);
 
+// ---- 4-bit expert weights (quantize.hip, ffn_quant.hip); rows and cols multiples of 8, group 32,
+// 64 or 128
+int64_t quantized_codes_bytes(int64_t E, int rows, int cols);
+int64_t quantized_scales_count(int64_t E, int rows, int cols, int group);
+hipError_t launch_quantize(const void* w, bool bf16, int64_t E, int rows, int cols, int group,
+                           void* codes, void* scales, hipStream_t st);
+hipError_t launch_dequantize(const void* codes, const void* scales, int64_t E, int rows, int cols,
+                             int group, float* w, hipStream_t st);
+hipError_t launch_quant_up(const moe_shape& s, const moe_quantized_experts& q, const void* x,
+                           const int32_t* row_token, const int32_t* offsets, void* h,
+                           int64_t rows_ub, hipStream_t st);
+hipError_t launch_quant_down(const moe_shape& s, const moe_quantized_experts& q, const void* h,
+                             const int32_t* offsets, void* y, int64_t rows_ub, hipStream_t st);
+
 }  // namespace moe

@@ -339,3 +339,70 @@ def route_backward(x: torch.Tensor, w_router: torch.Tensor, logits: torch.Tensor
                          dw_router=res["dw_router"], db_router=res["db_router"], dx_add=dx_add,
                          token_mask=token_mask, ws=ws)
     return res
+
+
+# ---------------------------------------------------------------- experts at 4 bits
+def quantize_weights(w: torch.Tensor, group: int = 32) -> tuple:
+    """Codes (uint8) and scales (bf16) of an expert array [E, rows, cols], bf16 or fp32."""
+    E, rows, cols = w.shape
+    shape = B.make_shape(1, 8, 8, E, 1, 0,
+                         B.MOE_BF16 if w.dtype == torch.bfloat16 else B.MOE_F32)
+    codes = torch.empty(B.quantized_codes_bytes(shape, rows, cols), dtype=torch.uint8,
+                        device=w.device)
+    scales = torch.empty(B.quantized_scales_bytes(shape, rows, cols, group) // 2,
+                         dtype=torch.bfloat16, device=w.device)
+    B.moe_quantize_weights(shape, w, group, codes, scales)
+    return codes, scales
+
+
+def dequantize_weights(codes: torch.Tensor, scales: torch.Tensor, E: int, rows: int, cols: int,
+                       group: int) -> torch.Tensor:
+    """The fp32 values [E, rows, cols] of codes and scales."""
+    shape = B.make_shape(1, 8, 8, E, 1, 0, B.MOE_F32)
+    w = torch.empty((E, rows, cols), dtype=torch.float32, device=codes.device)
+    B.moe_dequantize_weights(shape, codes, scales, group, w)
+    return w
+
+
+def quantize_experts(w1: torch.Tensor, b1: torch.Tensor | None, w2: torch.Tensor,
+                     b2: torch.Tensor | None, group: int = 32,
+                     gated: bool = False) -> B.QuantizedExperts:
+    """The experts of a layer at 4 bits: w1 [E, d_ff, d_model] (gated: W13 [E, 2 d_ff, d_model], no
+    biases) and w2 [E, d_model, d_ff], bf16 or fp32; biases bf16.  A one-time preparation."""
+    E, d, f = w2.shape
+    return B.QuantizedExperts(E, d, f, group, gated, *quantize_weights(w1, group),
+                              None if gated else b1, *quantize_weights(w2, group),
+                              None if gated else b2)
+
+
+def expert_ffn_quantized(shape: B.MoeShape, x: torch.Tensor, experts: B.QuantizedExperts,
+                         row_token, offsets, ws=None) -> torch.Tensor:
+    ws = workspace(shape, x.device) if ws is None else ws
+    y = torch.empty((max(B.max_kept_rows(shape), 0), shape.d_model), dtype=x.dtype,
+                    device=x.device)
+    B.moe_expert_ffn_quantized(shape, x, row_token, offsets, experts, y, ws)
+    return y
+
+
+def layer_forward_quantized(dev: dict, experts: B.QuantizedExperts, top_k: int, capacity: int,
+                            ws: torch.Tensor | None = None, events=None) -> dict:
+    """Whole layer with 4-bit experts (dev holds x, w_router and b_router); as layer_forward."""
+    x = dev["x"]
+    device = x.device
+    T, E = x.shape[0], experts.E
+    shape = B.make_shape(T, x.shape[1], experts.d_ff, E, top_k, capacity,
+                         B.MOE_BF16 if x.dtype == torch.bfloat16 else B.MOE_F32)
+    ws = workspace(shape, device) if ws is None else ws
+    res = {
+        "out": torch.empty_like(x),
+        "ids": torch.empty((T, top_k), dtype=torch.int32, device=device),
+        "gates": torch.empty((T, top_k), dtype=torch.float32, device=device),
+        "slot_of": torch.empty((T, top_k), dtype=torch.int32, device=device),
+        "drop_mask": torch.empty((T, top_k), dtype=torch.uint8, device=device),
+        "counts": torch.empty((E,), dtype=torch.int32, device=device),
+    }
+    B.moe_layer_forward_quantized(shape, x, dev["w_router"], dev["b_router"], experts, res["out"],
+                                  topk_ids=res["ids"], topk_gates=res["gates"],
+                                  slot_of=res["slot_of"], drop_mask=res["drop_mask"],
+                                  expert_counts=res["counts"], ws=ws, events=events)
+    return res

@@ -417,6 +417,70 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
                                      int32_t* batch_experts, void* ws, size_t ws_bytes,
                                      moe_stream_t stream, moe_event_t const* events);
 
+/* ---- Experts at 4 bits.  For decode-sized batches the expert products stream every active
+ * expert's weights once per batch, so the bytes of a weight are their time: 0.5 + 2 / group bytes
+ * here against bf16's 2.  A weight is value(code) * scale: the code is a sign and one of the
+ * magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; one bf16 scale serves `group` (32, 64 or 128) consecutive
+ * columns of a row.  Storage of an [E, rows, cols] array (rows and cols multiples of 8), with
+ * KC = ceil(cols / 128):
+ *   codes  [E][rows / 8][KC] blocks of 512 bytes, 8 rows x 128 columns: column c of row r of a
+ *          block is in the dword ((c % 32 / 8 * 8 + r) * 4 + c / 32), bits 4 (c % 8) and up, sign
+ *          highest; columns past cols are zero
+ *   scales [E][rows][KC * 128 / group] bf16, zero past cols */
+
+/* Bytes of the two arrays; 0 for an invalid shape, rows or cols not multiples of 8, or a group
+ * that is not 32, 64 or 128. */
+size_t moe_quantized_codes_bytes(const moe_shape* shape, int32_t rows, int32_t cols);
+size_t moe_quantized_scales_bytes(const moe_shape* shape, int32_t rows, int32_t cols,
+                                  int32_t group);
+
+/* Quantise an expert weight array (a one-time preparation of the weights).  Of each group:
+ * scale = max |w| * fp32(1 / 6) rounded to bf16, code = the magnitude nearest to |w| / scale
+ * (ties to the even code, 6 for anything above) with w's sign; a group of zeros has scale 0.
+ *   w      [E, rows, cols] in, shape->dtype (bf16 or fp32), finite; W13 of a gated expert: rows =
+ *          2 d_ff
+ *   codes, scales out, 16-byte aligned; must not overlap w */
+moe_status moe_quantize_weights(const moe_shape* shape, const void* w, int32_t rows, int32_t cols,
+                                int32_t group, void* codes, void* scales, moe_stream_t stream);
+
+/* The values that codes and scales stand for, exact: w [E, rows, cols] fp32 out. */
+moe_status moe_dequantize_weights(const moe_shape* shape, const void* codes, const void* scales,
+                                  int32_t rows, int32_t cols, int32_t group, float* w,
+                                  moe_stream_t stream);
+
+/* The experts of a layer at 4 bits: device pointers, all 16-byte aligned. */
+typedef struct {
+  const void* w1_codes;  /* [E, d_ff, d_model], gated: W13 [E, 2 d_ff, d_model], gate rows first */
+  const void* w1_scales;
+  const void* b1;        /* [E, d_ff] bf16; gated: NULL */
+  const void* w2_codes;  /* [E, d_model, d_ff] */
+  const void* w2_scales;
+  const void* b2;        /* [E, d_model] bf16; gated: NULL */
+  int32_t group;         /* 32, 64 or 128, of both arrays */
+  int32_t gated;         /* 0: W2 SiLU(W1 x + b1) + b2; 1: W2 (SiLU(W_gate x) * (W_up x)) */
+} moe_quantized_experts;
+
+/* moe_expert_ffn with 4-bit experts.  bf16 only, shape->weight_layout row-major (the default);
+ * workspace moe_workspace_bytes(shape).  Of each group the products of x and the codes' values are
+ * exact and summed in fp32, and the scale multiplies that sum: no weight is rounded.  The
+ * activation between the products is stored as bf16, as moe_expert_ffn stores it.  Rows past the
+ * last kept one are not written. */
+moe_status moe_expert_ffn_quantized(const moe_shape* shape, const void* x,
+                                    const int32_t* row_token, const int32_t* expert_offsets,
+                                    const moe_quantized_experts* experts, void* y_rows, void* ws,
+                                    size_t ws_bytes, moe_stream_t stream);
+
+/* moe_layer_forward (gated: moe_layer_forward_gated) with 4-bit experts; router, dispatch and
+ * combine as there.  events NULL or 6 hipEvent_t as in moe_layer_forward_profiled;
+ * moe_set_gemm_timing and moe_set_stage_timing arm it too. */
+moe_status moe_layer_forward_quantized(const moe_shape* shape, const void* x, const void* w_router,
+                                       const float* b_router,
+                                       const moe_quantized_experts* experts, void* out,
+                                       int32_t* topk_ids, float* topk_gates, int32_t* slot_of,
+                                       uint8_t* drop_mask, int32_t* expert_counts, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream,
+                                       moe_event_t const* events);
+
 /* ---- Router training.  "Expert Networks": routing collapses onto few experts unless something
  * spreads the tokens; these two calls give that something its gradient down to the router. */
 
