@@ -245,6 +245,12 @@ moe_status check_quantized(const moe_shape& s, const moe_quantized_experts& q) {
     return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", q.group);
   if (q.gated != 0 && q.gated != 1)
     return fail(MOE_ERR_INVALID_ARGUMENT, "gated = %d is not 0 or 1", q.gated);
+  // codes and scales of an expert are addressed with 32-bit byte offsets
+  const int64_t lim = (int64_t)1 << 31;
+  if (quantized_codes_bytes(1, s.d_ff, s.d_model) * (q.gated ? 2 : 1) >= lim ||
+      quantized_codes_bytes(1, s.d_model, s.d_ff) >= lim)
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit expert of %d x %d: 2 GiB or more per expert", s.d_ff,
+                s.d_model);
   MOE_TRY(check_data_ptr(s, q.w1_codes, "w1_codes"));
   MOE_TRY(check_data_ptr(s, q.w1_scales, "w1_scales"));
   MOE_TRY(check_data_ptr(s, q.w2_codes, "w2_codes"));

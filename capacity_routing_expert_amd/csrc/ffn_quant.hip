@@ -1,6 +1,7 @@
 // Expert FFN on 4-bit weights: the two grouped products over the routed rows.
 //
-//   H[s, n] = act(sum_k x[row_token[s], k] W1[e, n, k] + b1[e, n]),  Y[s, n] = sum_k H[s, k] W2[e, n, k] + b2[e, n]
+//   H[s, n] = act(sum_k x[row_token[s], k] W1[e, n, k] + b1[e, n])
+//   Y[s, n] = sum_k H[s, k] W2[e, n, k] + b2[e, n]
 // with W[n, k] = scale[n, k / group] value(code[n, k]) (quantize.hip has the storage).  For every
 // group, v_mfma_f32_16x16x32_bf16 sums x value(code), both exact in bf16, in fp32, and the scale
 // multiplies that sum once, in fp32: no weight is rounded.  H is stored as bf16, as the bf16
@@ -8,7 +9,13 @@
 //
 // Roles: token rows are the A operand (lane n: row n of 16, 8 K values from 8 (lane / 16)), weight
 // rows the B operand, so a lane holds one feature's results for four token rows and one scale
-// serves all four.
+// serves all four.  A 16-byte load of codes feeds a lane's part of four matrix instructions (128
+// columns), and the waves of a block read neighbouring rows of the same column block: runs of
+// 4 to 16 KiB.  The token rows go through LDS in fragment order (1 KiB a fragment, read without
+// conflicts), loaded once for all waves of a block.
+//
+// Everything that a buffer descriptor is made of is wave-uniform and kept scalar (readfirstlane):
+// the loads then need no loop over descriptor values.
 #include "moe_internal.h"
 
 namespace moe {
@@ -43,15 +50,16 @@ template <int GROUP>
 struct Scales {
   static constexpr int N = 128 / GROUP;
   uint32_t w[(N + 1) / 2];
-  __device__ __forceinline__ void load(const bf16_t* p) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     if constexpr (N == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+      w[0] = v[0];
+      w[1] = v[1];
     } else if constexpr (N == 2) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
     } else {
-      w[0] = *p;
+      w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
     }
   }
   __device__ __forceinline__ float get(int g) const {
@@ -69,285 +77,117 @@ struct QArgs {
   bf16_t* out;         // [slots, N]
   int E, N, K;         // N output features (a gated expert has 2 N weight rows)
   int64_t a_rows;
+  int xcds;      // XCDs that share one row tile's feature tiles: 2 or 8
   int out_rows;  // rows of out: no slot at or past it is computed
 };
 
-// Expert number `want` (from 0) among those with rows, or -1; wave-uniform, all lanes call.
-__device__ __forceinline__ int nth_active(const int32_t* __restrict__ offsets, int E, int want) {
+// Row tile `want` of TM rows, counted over the experts: its expert and rows; false past the last.
+// Lane l adds up the tiles of experts 4 l .. 4 l + 3, a prefix sum over the lanes finds the owner.
+// The results are scalars.
+template <int TM>
+__device__ __forceinline__ bool row_tile(const QArgs& a, int want, int& e, int& row0, int& rows) {
   const int lane = threadIdx.x & 63;
-  int seen = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    uint64_t m = __ballot(e < E && offsets[e + 1] > offsets[e]);
-    const int here = __popcll(m);
-    if (want < seen + here) {
-      for (int i = want - seen; i > 0; --i) m &= m - 1;
-      return e0 + __ffsll((long long)m) - 1;
-    }
-    seen += here;
+  int te[4], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = lane * 4 + j;
+    const int n = i < a.E ? min(a.offsets[i + 1], a.out_rows) - a.offsets[i] : 0;
+    te[j] = n > 0 ? (n + TM - 1) / TM : 0;
+    sum += te[j];
   }
-  return -1;
+  int inc = sum;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += v;
+  }
+  if (want >= __builtin_amdgcn_readfirstlane(__shfl(inc, 63, 64))) return false;
+  const int owner = __builtin_amdgcn_readfirstlane(__ffsll((long long)__ballot(want < inc)) - 1);
+  int run = inc - sum, ex = lane * 4, at = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (want >= run && want < run + te[j]) {
+      ex = lane * 4 + j;
+      at = want - run;
+    }
+    run += te[j];
+  }
+  e = __builtin_amdgcn_readfirstlane(__shfl(ex, owner, 64));
+  at = __builtin_amdgcn_readfirstlane(__shfl(at, owner, 64));
+  row0 = __builtin_amdgcn_readfirstlane(a.offsets[e] + at * TM);
+  rows = __builtin_amdgcn_readfirstlane(min(min(a.offsets[e + 1], a.out_rows) - row0, TM));
+  return true;
 }
 
-// ---------------------------------------------------------------- few rows an expert
-// A block takes 16 FT weight rows of one expert and all of its token rows, 16 RT at a time; its WK
-// waves take the 128-column blocks of K in turn, and their sums are added in LDS, in wave order.
-// Weights go from HBM to registers, PF blocks ahead, each 16-byte load feeding four matrix
-// instructions; the token rows come from L2.
-template <int RT, int FT, int WK, int GROUP, int ACT>
-__global__ __launch_bounds__(64 * WK) void k_quant_rows(QArgs a) {
-  constexpr int PF = 2;
-  constexpr bool GATED = ACT == kQGated;
-  constexpr int FO = GATED ? FT / 2 : FT;  // output tiles
+// Block -> (row tile, feature tile) with NT feature tiles a row tile.  Workgroups go round-robin
+// over the 8 XCDs; the feature tiles of one row tile stay on `xcds` of them, so their shared token
+// rows are fetched by that many L2s.
+__device__ __forceinline__ bool tile_of(const QArgs& a, int NT, int& mt, int& nt) {
+  const int ntx = (NT + a.xcds - 1) / a.xcds, groups = 8 / a.xcds;
+  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+  nt = slot % ntx * a.xcds + xcd % a.xcds;
+  mt = slot / ntx * groups + xcd / a.xcds;
+  return nt < NT;
+}
+int64_t tile_grid(int64_t tiles, int64_t NT, int xcds) {
+  return 8 * ((NT + xcds - 1) / xcds) * ((tiles + 8 / xcds - 1) / (8 / xcds));
+}
+
+constexpr uint32_t kOut = 0x80000000u;  // past every range, whatever offset is added to it
+
+// A wave's weights: FT tiles of 16 rows of expert e from output feature f0 on (gated: FT / 2 gate
+// tiles, then the up tiles of the same features).
+template <int FT, int GROUP, bool GATED>
+struct Weights {
+  static constexpr int FO = GATED ? FT / 2 : FT, S = 128 / GROUP;
   static_assert(!GATED || FT % 2 == 0, "gate and up tiles in pairs");
-  __shared__ f32x4_t red[WK][RT * FT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, kg = lane >> 4;
-  const int e = nth_active(a.offsets, a.E, blockIdx.y);
-  if (e < 0) return;  // block-uniform
-  const int row0 = a.offsets[e], rows = min(a.offsets[e + 1], a.out_rows) - row0;
-  const int KC = (a.K + 127) / 128;
-  const int wrows = GATED ? 2 * a.N : a.N;  // weight rows of the expert (a multiple of 8)
-  const int f0 = blockIdx.x * FO * 16;
-  // weight row of lane n in tile f, clamped (the results of clamped lanes are not stored)
-  const uint4* cp[FT];
-  const bf16_t* sp[FT];
+  __amdgpu_buffer_rsrc_t cr, sr;
+  uint32_t cstep, sstep;  // bytes from a column block to the next
+  uint32_t co[FT], so[FT];
+  int KC;
+  __device__ __forceinline__ Weights(const QArgs& a, int e, int f0, int n, int kg) {
+    const int wrows = GATED ? 2 * a.N : a.N;
+    KC = (a.K + 127) / 128;
+    cstep = wrows * 64;
+    sstep = wrows * S * 2;
+    cr = buffer_rsrc(a.codes + (int64_t)e * KC * wrows * 4, KC * cstep);
+    sr = buffer_rsrc(a.scales + (int64_t)e * KC * wrows * S, KC * sstep);
 #pragma unroll
-  for (int f = 0; f < FT; ++f) {
-    int r = f0 + (f % FO) * 16 + n;
-    r = r < a.N ? r : a.N - 8 + (n & 7);
-    if (GATED && f >= FO) r += a.N;
-    const int64_t row = (int64_t)e * wrows + r;
-    cp[f] = a.codes + row / 8 * KC * 32 + kg * 8 + r % 8;
-    sp[f] = a.scales + row * KC * (128 / GROUP);
+    for (int f = 0; f < FT; ++f) {
+      uint32_t r = f0 + f % FO * 16 + n;
+      const bool in = (int)r < a.N;
+      if (GATED && f >= FO) r += a.N;
+      co[f] = in ? (r / 8 * 32 + kg * 8 + r % 8) * 16 : kOut;
+      so[f] = in ? r * S * 2 : kOut;
+    }
   }
-  for (int r0 = 0; r0 < rows; r0 += 16 * RT) {
-    const bf16_t* xp[RT];
-    bool in[RT];
+  // column block kc; past the last: zeros, without traffic
+  __device__ __forceinline__ void load(int kc, uint4 (&cw)[FT], Scales<GROUP> (&sc)[FT]) const {
+    const bool in = kc < KC;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = r0 + rt * 16 + n;
-      int64_t at = -1;
-      if (r < rows) at = a.row_token ? a.row_token[row0 + r] : row0 + r;
-      in[rt] = at >= 0 && at < a.a_rows;
-      xp[rt] = a.A + (in[rt] ? at : 0) * a.K + kg * 8;
+    for (int f = 0; f < FT; ++f) {
+      cw[f] = buffer_load16(cr, in ? co[f] + kc * cstep : kOut);
+      sc[f].load(sr, in ? so[f] + kc * sstep : kOut);
     }
-    f32x4_t acc[RT][FT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int f = 0; f < FT; ++f) acc[rt][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    uint4 cw[PF][FT], xw[PF][RT][4];
-    Scales<GROUP> sc[PF][FT];
-    auto load = [&](int p, int kc) {
-      if (kc >= KC) return;
-#pragma unroll
-      for (int f = 0; f < FT; ++f) {
-        cw[p][f] = cp[f][(int64_t)kc * 32];
-        sc[p][f].load(sp[f] + kc * (128 / GROUP));
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = kc * 128 + j * 32;
-          xw[p][rt][j] = make_uint4(0, 0, 0, 0);
-          if (in[rt] && k + kg * 8 < a.K) xw[p][rt][j] = *reinterpret_cast<const uint4*>(xp[rt] + k);
-        }
-    };
-#pragma unroll
-    for (int p = 0; p < PF; ++p) load(p, wave + p * WK);
-    for (int kc = wave; kc < KC; kc += PF * WK) {
-#pragma unroll
-      for (int p = 0; p < PF; ++p) {
-        if (kc + p * WK >= KC) break;
-#pragma unroll
-        for (int f = 0; f < FT; ++f) {
-          const uint32_t c[4] = {cw[p][f].x, cw[p][f].y, cw[p][f].z, cw[p][f].w};
-#pragma unroll
-          for (int g = 0; g < 128 / GROUP; ++g) {
-            const float s = sc[p][f].get(g);
-            f32x4_t t[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) t[rt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j) {
-              const bf16x8_t B = values_of(c[j]);
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt)
-                t[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qfrag(xw[p][rt][j]), B, t[rt], 0, 0, 0);
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[rt][f][i] = fmaf(s, t[rt][i], acc[rt][f][i]);
-          }
-        }
-        load(p, kc + (p + PF) * WK);
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int f = 0; f < FT; ++f) red[wave][rt * FT + f][lane] = acc[rt][f];
-    __syncthreads();
-    for (int i = threadIdx.x; i < RT * FO * 64; i += 64 * WK) {
-      const int rt = i / (FO * 64), f = i / 64 % FO, ln = i % 64;
-      f32x4_t v = red[0][rt * FT + f][ln];
-      for (int w = 1; w < WK; ++w) v += red[w][rt * FT + f][ln];
-      const int feat = f0 + f * 16 + ln % 16;
-      if (feat >= a.N) continue;
-      if constexpr (GATED) {
-        f32x4_t u = red[0][rt * FT + FO + f][ln];
-        for (int w = 1; w < WK; ++w) u += red[w][rt * FT + FO + f][ln];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = silu(v[j]) * u[j];
-      } else {
-        const float b = a.bias ? bf16_to_f32(a.bias[(int64_t)e * a.N + feat]) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ACT == kQSilu ? silu(v[j] + b) : v[j] + b;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = r0 + rt * 16 + ln / 16 * 4 + j;
-        if (r < rows) a.out[(int64_t)(row0 + r) * a.N + feat] = (bf16_t)pack_bf16x2(v[j], 0.0f);
-      }
-    }
-    __syncthreads();  // red is written again by the next rows
   }
+};
+
+// The token rows of a tile: gathered through row_token, or rows row0 .. of A.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t token_rsrc(const QArgs& a, int row0, int rows) {
+  return a.row_token ? buffer_rsrc(a.A, (uint32_t)(a.a_rows * a.K * 2))
+                     : buffer_rsrc(a.A + (int64_t)row0 * a.K, (uint32_t)rows * a.K * 2);
+}
+__device__ __forceinline__ uint32_t token_offset(const QArgs& a, int row0, int rows, int r) {
+  if (r >= rows) return kOut;
+  const int t = a.row_token ? a.row_token[row0 + r] : r;
+  return t >= 0 ? (uint32_t)t * a.K * 2 : kOut;
 }
 
-// ---------------------------------------------------------------- many rows an expert
-// A block takes 16 RT token rows x 256 weight rows (four waves of 64).  A block of 128 columns of
-// the token rows goes through LDS in fragment order (16 lanes a row group, 1 KiB a fragment), so
-// the four waves read it without conflicts; each wave converts its own weights, once for all
-// token rows.
-template <int RT, int GROUP, int ACT>
-__global__ __launch_bounds__(256) void k_quant_tiles(QArgs a) {
+// Bias, activation, bf16 and store of a wave's results: rows r0 + 16 rt + 4 kg + j of the tile.
+template <int RT, int FT, int ACT>
+__device__ __forceinline__ void store_tile(const QArgs& a, const f32x4_t (&acc)[RT][FT], int e,
+                                           int row0, int rows, int r0, int f0, int n, int kg) {
   constexpr bool GATED = ACT == kQGated;
-  constexpr int FT = 4, FO = GATED ? 2 : 4;
-  constexpr int TM = 16 * RT;
-  __shared__ uint4 xs[2][RT * 4][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, kg = lane >> 4;
-  // token tile `mt` of all experts' tiles
-  constexpr int NB = GATED ? 128 : 256;
-  const int NT = (a.N + NB - 1) / NB;
-  const int mt = blockIdx.x / NT, nt = blockIdx.x % NT;
-  int e = -1, row0 = 0, rows = 0;
-  {
-    int seen = 0;
-    for (int i = 0; i < a.E; ++i) {
-      const int lo = a.offsets[i], hi = min(a.offsets[i + 1], a.out_rows);
-      const int t = (hi - lo + TM - 1) / TM;
-      if (mt < seen + t) {
-        e = i;
-        row0 = lo + (mt - seen) * TM;
-        rows = hi - row0 < TM ? hi - row0 : TM;
-        break;
-      }
-      seen += t;
-    }
-  }
-  if (e < 0) return;  // block-uniform
-  const int KC = (a.K + 127) / 128;
-  const int wrows = GATED ? 2 * a.N : a.N;
-  const int f0 = (nt * 4 + wave) * FO * 16;
-  const uint4* cp[FT];
-  const bf16_t* sp[FT];
-#pragma unroll
-  for (int f = 0; f < FT; ++f) {
-    int r = f0 + (f % FO) * 16 + n;
-    r = r < a.N ? r : a.N - 8 + (n & 7);
-    if (GATED && f >= FO) r += a.N;
-    const int64_t row = (int64_t)e * wrows + r;
-    cp[f] = a.codes + row / 8 * KC * 32 + kg * 8 + r % 8;
-    sp[f] = a.scales + row * KC * (128 / GROUP);
-  }
-  // this thread's share of the staging: fragments (rt, j = wave), lane (n, kg)
-  const bf16_t* xp[RT];
-  bool in[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = rt * 16 + n;
-    int64_t at = -1;
-    if (r < rows) at = a.row_token ? a.row_token[row0 + r] : row0 + r;
-    in[rt] = at >= 0 && at < a.a_rows;
-    xp[rt] = a.A + (in[rt] ? at : 0) * a.K + wave * 32 + kg * 8;
-  }
-  uint4 xr[RT], cw[FT];
-  Scales<GROUP> sc[FT];
-  auto load_x = [&](int kc) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      xr[rt] = make_uint4(0, 0, 0, 0);
-      if (in[rt] && kc * 128 + wave * 32 + kg * 8 < a.K)
-        xr[rt] = *reinterpret_cast<const uint4*>(xp[rt] + kc * 128);
-    }
-  };
-  auto load_w = [&](int kc) {
-#pragma unroll
-    for (int f = 0; f < FT; ++f) {
-      cw[f] = cp[f][(int64_t)kc * 32];
-      sc[f].load(sp[f] + kc * (128 / GROUP));
-    }
-  };
-  f32x4_t acc[RT][FT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int f = 0; f < FT; ++f) acc[rt][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  load_x(0);
-  load_w(0);
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) xs[0][rt * 4 + wave][lane] = xr[rt];
-  __syncthreads();
-  for (int kc = 0; kc < KC; ++kc) {
-    bf16x8_t B[FT][4];
-    float s[FT][128 / GROUP];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) {
-      B[f][0] = values_of(cw[f].x);
-      B[f][1] = values_of(cw[f].y);
-      B[f][2] = values_of(cw[f].z);
-      B[f][3] = values_of(cw[f].w);
-#pragma unroll
-      for (int g = 0; g < 128 / GROUP; ++g) s[f][g] = sc[f].get(g);
-    }
-    const bool more = kc + 1 < KC;
-    if (more) {
-      load_x(kc + 1);
-      load_w(kc + 1);
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      bf16x8_t A[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) A[j] = qfrag(xs[kc & 1][rt * 4 + j][lane]);
-#pragma unroll
-      for (int g = 0; g < 128 / GROUP; ++g) {
-        f32x4_t t[FT];
-#pragma unroll
-        for (int f = 0; f < FT; ++f) t[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = g * (GROUP / 32); j < (g + 1) * (GROUP / 32); ++j)
-#pragma unroll
-          for (int f = 0; f < FT; ++f)
-            t[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j], B[f][j], t[f], 0, 0, 0);
-#pragma unroll
-        for (int f = 0; f < FT; ++f)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[rt][f][i] = fmaf(s[f][g], t[f][i], acc[rt][f][i]);
-      }
-    }
-    if (more) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) xs[(kc + 1) & 1][rt * 4 + wave][lane] = xr[rt];
-    }
-    __syncthreads();
-  }
+  constexpr int FO = GATED ? FT / 2 : FT;
 #pragma unroll
   for (int f = 0; f < FO; ++f) {
     const int feat = f0 + f * 16 + n;
@@ -357,7 +197,7 @@ __global__ __launch_bounds__(256) void k_quant_tiles(QArgs a) {
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = rt * 16 + kg * 4 + j;
+        const int r = r0 + rt * 16 + kg * 4 + j;
         float v = acc[rt][f][j];
         if constexpr (GATED)
           v = silu(v) * acc[rt][FO + f][j];
@@ -368,34 +208,317 @@ __global__ __launch_bounds__(256) void k_quant_tiles(QArgs a) {
   }
 }
 
-template <int GROUP, int ACT>
-hipError_t run_quant(const QArgs& a, int64_t rows_ub, int64_t mean_rows, hipStream_t st) {
+// ---------------------------------------------------------------- few rows an expert
+// A block takes 16 RT token rows of one expert and 16 FT WF of its weight rows; WF waves stand side
+// by side on the features, WK share the column blocks (step s: blocks WK s .. WK s + WK - 1), and
+// their sums are added in LDS, in wave order.  Weights go from HBM to registers, D steps in
+// flight.  STAGED: a step's token rows are loaded into registers two steps ahead and into one of
+// two LDS buffers one step ahead, one barrier a step; otherwise (one or two tokens, where the
+// barriers cost more than the loads) every wave loads its own.
+//
+// Bound: the weight stream.  E 8, d 2048, f 8192, 64 tokens, group 32 (75 MB a product): 19.3 us
+// up, 22.9 us down, 3.9 and 3.3 TB/s; loading the same codes without products or token rows: 16.8
+// and 18.3 us, and 2.3 us of it are an empty launch.  Column blocks outermost in the storage (runs of
+// 8 KiB a block of waves) instead of rows outermost: 24.2 -> 20.0 us up, 26.3 -> 22.2 us down.
+template <int RT, int FT, int WF, int WK, int D, bool STAGED, int GROUP, int ACT>
+__global__ __launch_bounds__(64 * WF * WK) void k_quant_rows(QArgs a) {
+  constexpr int S = 128 / GROUP, J = GROUP / 32, W = WF * WK, XL = STAGED ? RT * 4 / WF : RT;
   constexpr bool GATED = ACT == kQGated;
-  const int64_t active = rows_ub < a.E ? rows_ub : a.E;
-  if (mean_rows > 64) {
-    constexpr int NB = GATED ? 128 : 256;
-    const int64_t tiles = (rows_ub + 127) / 128 + a.E;
-    return launch_timed(k_quant_tiles<8, GROUP, ACT>,
-                        dim3((unsigned)((a.N + NB - 1) / NB * tiles)), dim3(256), 0, st, a);
-  }
-  auto grid = [&](int FT) {
-    const int cols = 16 * (GATED ? FT / 2 : FT);
-    return dim3((unsigned)((a.N + cols - 1) / cols), (unsigned)active);
+  constexpr int FO = GATED ? FT / 2 : FT;  // output tiles of a wave
+  static_assert(!STAGED || RT * 4 % WF == 0, "whole fragments a wave");
+  extern __shared__ uint4 smem[];
+  auto xs = reinterpret_cast<uint4(*)[WK][RT * 4][64]>(smem);          // [2]
+  auto red = reinterpret_cast<f32x4_t(*)[WF][RT * FT][64]>(smem);      // [WK - 1]
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wf = wave % WF, wk = wave / WF;
+  const int n = lane & 15, kg = lane >> 4;
+  int mt, nt, e, row0, rows;
+  if (!tile_of(a, (a.N + 16 * FO * WF - 1) / (16 * FO * WF), mt, nt)) return;  // block-uniform
+  if (!row_tile<16 * RT>(a, mt, e, row0, rows)) return;                         // block-uniform
+  const int f0 = (nt * WF + wf) * FO * 16;
+  const Weights<FT, GROUP, GATED> w(a, e, f0, n, kg);
+  const int KC = w.KC, steps = (KC + WK - 1) / WK;
+  const __amdgpu_buffer_rsrc_t xr = token_rsrc(a, row0, rows);
+  // STAGED: fragment i W + wave of a step (its column block, row group and 32 columns); else row
+  // group i
+  uint32_t xo[XL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i)
+    xo[i] = token_offset(a, row0, rows, (STAGED ? (i * W + wave) / 4 % RT : i) * 16 + n);
+  uint4 cw[D][FT], xw[STAGED ? 1 : D][STAGED ? XL : RT * 4];
+  Scales<GROUP> sc[D][FT];
+  auto load_own = [&](int p, int s) {  // not STAGED: the wave's own column block
+#pragma unroll
+    for (int i = 0; i < RT * 4; ++i) {
+      const int k = (s * WK + wk) * 128 + i % 4 * 32 + kg * 8;
+      xw[STAGED ? 0 : p][STAGED ? 0 : i] = buffer_load16(xr, k < a.K ? xo[STAGED ? 0 : i / 4] + k * 2 : kOut);
+    }
   };
-  if (mean_rows > 24)
-    return launch_timed(k_quant_rows<4, 2, 8, GROUP, ACT>, grid(2), dim3(512), 0, st, a);
-  if (mean_rows > 8)
-    return launch_timed(k_quant_rows<2, 4, 8, GROUP, ACT>, grid(4), dim3(512), 0, st, a);
-  return launch_timed(k_quant_rows<1, 4, 8, GROUP, ACT>, grid(4), dim3(512), 0, st, a);
+  auto load_step = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int id = i * W + wave;
+      const int k = (s * WK + id / (RT * 4)) * 128 + id % 4 * 32 + kg * 8;
+      xw[0][i] = buffer_load16(xr, k < a.K ? xo[i] + k * 2 : kOut);
+    }
+  };
+  auto store_step = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int id = i * W + wave;
+      xs[s & 1][id / (RT * 4)][id % (RT * 4)][lane] = xw[0][i];
+    }
+  };
+  f32x4_t acc[RT][FT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int f = 0; f < FT; ++f) acc[rt][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto compute = [&](int p, int s) {
+    if (s * WK + wk >= KC) return;  // wave-uniform
+#pragma unroll
+    for (int g = 0; g < S; ++g) {
+      bf16x8_t A[J][RT];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          A[j][rt] = qfrag(STAGED ? xs[s & 1][wk][rt * 4 + g * J + j][lane]
+                                  : xw[STAGED ? 0 : p][STAGED ? 0 : rt * 4 + g * J + j]);
+#pragma unroll
+      for (int f = 0; f < FT; ++f) {
+        const uint32_t c[4] = {cw[p][f].x, cw[p][f].y, cw[p][f].z, cw[p][f].w};
+        const float sv = sc[p][f].get(g);
+        f32x4_t t[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) t[rt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const bf16x8_t B = values_of(c[g * J + j]);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            t[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[j][rt], B, t[rt], 0, 0, 0);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[rt][f][i] = fmaf(sv, t[rt][i], acc[rt][f][i]);
+        // one tile's conversions at a time: hoisted together they take twice the registers
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  if constexpr (STAGED) load_step(0);
+#pragma unroll
+  for (int p = 0; p < D - 1; ++p) {
+    w.load(p * WK + wk, cw[p], sc[p]);
+    if constexpr (!STAGED) load_own(p, p);
+  }
+  if constexpr (STAGED) {
+    store_step(0);
+    load_step(1);
+    __syncthreads();
+  }
+  for (int s0 = 0; s0 < steps; s0 += D) {
+#pragma unroll
+    for (int p = 0; p < D; ++p) {
+      const int s = s0 + p;
+      if (s >= steps) break;
+      w.load((s + D - 1) * WK + wk, cw[(p + D - 1) % D], sc[(p + D - 1) % D]);
+      if constexpr (!STAGED) load_own((p + D - 1) % D, s + D - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(p, s);
+      if constexpr (STAGED) {
+        store_step(s + 1);
+        load_step(s + 2);
+        __syncthreads();
+      }
+    }
+  }
+  if constexpr (WK > 1) {
+    if (wk > 0) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int f = 0; f < FT; ++f) red[wk - 1][wf][rt * FT + f][lane] = acc[rt][f];
+    }
+    __syncthreads();
+    if (wk > 0) return;
+    for (int i = 0; i < WK - 1; ++i)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int f = 0; f < FT; ++f) acc[rt][f] += red[i][wf][rt * FT + f][lane];
+  }
+  store_tile<RT, FT, ACT>(a, acc, e, row0, rows, 0, f0, n, kg);
+}
+
+// ---------------------------------------------------------------- many rows an expert
+// A block takes 16 RT token rows and 16 FT WF weight rows, a wave 16 FT of them and all token rows:
+// each weight is converted once for 16 RT rows.  The fragments of the next (row group, scale
+// group) are read from LDS, and the sums of the last one scaled, between the matrix instructions
+// of the present one; the scheduling barriers keep the compiler from gathering either at one end
+// (gathered: 1.22 ms instead of 0.62 ms on the layer below).
+//
+// Bound: the matrix instructions and their interleaved conversions and scale products (4 fp32
+// products for every GROUP / 32 matrix instructions).  E 8, d 2048, f 8192, 4096 tokens, top-2, group
+// 128: 309 us a product, 890 TFLOP/s; group 32: 433 and 449 us.
+template <int WF, int RT, int FT, int GROUP, int ACT>
+__global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
+  constexpr bool GATED = ACT == kQGated;
+  constexpr int FO = GATED ? FT / 2 : FT, S = 128 / GROUP, J = GROUP / 32;
+  constexpr int XL = RT * 4 / WF, NI = RT * S;  // NI items of a column block: (row group, scale group)
+  static_assert(RT * 4 % WF == 0, "whole fragments a wave");
+  __shared__ uint4 xs[2][RT * 4][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, kg = lane >> 4;
+  int mt, nt, e, row0, rows;
+  if (!tile_of(a, (a.N + 16 * FO * WF - 1) / (16 * FO * WF), mt, nt)) return;  // block-uniform
+  if (!row_tile<16 * RT>(a, mt, e, row0, rows)) return;                         // block-uniform
+  const int f0 = (nt * WF + wave) * FO * 16;
+  const Weights<FT, GROUP, GATED> w(a, e, f0, n, kg);
+  const __amdgpu_buffer_rsrc_t xr = token_rsrc(a, row0, rows);
+  uint32_t xo[XL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) xo[i] = token_offset(a, row0, rows, (i * WF + wave) / 4 * 16 + n);
+  uint4 cw[FT], xw[XL];
+  Scales<GROUP> sc[FT];
+  auto load_x = [&](int kc) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      const int k = kc * 128 + (i * WF + wave) % 4 * 32 + kg * 8;
+      xw[i] = buffer_load16(xr, k < a.K ? xo[i] + k * 2 : kOut);
+    }
+  };
+  auto store_x = [&](int kc) {
+#pragma unroll
+    for (int i = 0; i < XL; ++i) xs[kc & 1][i * WF + wave][lane] = xw[i];
+  };
+  f32x4_t acc[RT][FT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int f = 0; f < FT; ++f) acc[rt][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  load_x(0);
+  w.load(0, cw, sc);
+  store_x(0);
+  load_x(1);
+  __syncthreads();
+  for (int kc = 0; kc < w.KC; ++kc) {
+    bf16x8_t B[FT][4];
+    float s[FT][S];
+#pragma unroll
+    for (int f = 0; f < FT; ++f) {
+      B[f][0] = values_of(cw[f].x);
+      B[f][1] = values_of(cw[f].y);
+      B[f][2] = values_of(cw[f].z);
+      B[f][3] = values_of(cw[f].w);
+#pragma unroll
+      for (int g = 0; g < S; ++g) s[f][g] = sc[f].get(g);
+    }
+    w.load(kc + 1, cw, sc);
+    bf16x8_t A[2][J];
+    f32x4_t t[2][FT];
+    auto frags = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) A[i & 1][j] = qfrag(xs[kc & 1][i / S * 4 + i % S * J + j][lane]);
+    };
+    auto scale = [&](int i) {
+#pragma unroll
+      for (int f = 0; f < FT; ++f)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          acc[i / S][f][u] = fmaf(s[f][i % S], t[i & 1][f][u], acc[i / S][f][u]);
+    };
+    frags(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (i + 1 < NI) frags(i + 1);
+#pragma unroll
+      for (int f = 0; f < FT; ++f) t[i & 1][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int f = 0; f < FT; ++f)
+          t[i & 1][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[i & 1][j], B[f][i % S * J + j],
+                                                                t[i & 1][f], 0, 0, 0);
+      if (i > 0) scale(i - 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    scale(NI - 1);
+    store_x(kc + 1);
+    load_x(kc + 2);
+    __syncthreads();
+  }
+  store_tile<RT, FT, ACT>(a, acc, e, row0, rows, 0, f0, n, kg);
+}
+
+// ---------------------------------------------------------------- choice of the kernel
+template <int RT, int FT, int WF, int WK, int D, bool STAGED, int GROUP, int ACT>
+hipError_t run_rows(const QArgs& a, int64_t tiles, int64_t NT, hipStream_t st) {
+  constexpr size_t x = STAGED ? (size_t)2 * WK * RT * 4096 : 0;
+  constexpr size_t r = (size_t)(WK - 1) * WF * RT * FT * 1024;
+  constexpr size_t lds = x > r ? x : r;
+  static_assert(lds <= 64 * 1024, "LDS without an attribute");
+  return launch_timed(k_quant_rows<RT, FT, WF, WK, D, STAGED, GROUP, ACT>,
+                      dim3((unsigned)tile_grid(tiles, NT, a.xcds)), dim3(64 * WF * WK), lds, st, a);
+}
+
+// Rows an expert on average, and blocks a variant would launch, decide (d 2048, f 8192, 8 experts unless
+// said otherwise, us up / down):
+//  - many rows: 64 x 256 tiles of 8 waves, once they are 160 blocks (64 experts of f 1408, 96 rows each:
+//    60 / 58 against 77 / 75 for the next); 64 rows each: 39 up as the next's, down only 96 blocks
+//    and the next is ahead, 47 against 54;
+//  - else 32 rows x 256 weight rows, from 160 blocks on (64 experts, 24 rows each: 29 / 31 against 33
+//    / 29 for the next);
+//  - else 32 x 128, from 256 blocks on (16 rows each, up: 19.3 against 37 for the next);
+//  - else K shared by 4 groups of waves, 64 weight rows a block: 32 token rows (16 rows each, down:
+//    22.9 against 38 for the last), or 16 where experts have at most 8 (2 rows each, down: 18.4
+//    against 19.9);
+//  - one or two tokens, with fewer blocks than that: 16 weight rows a block, K shared by 8 waves
+//    that load their own token rows (1 token, down: 7.1 against 14).
+// A gated tile holds a gate and an up row per feature: half the features a block.
+template <int GROUP, int ACT>
+hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
+  constexpr bool GATED = ACT == kQGated;
+  constexpr int F1 = GATED ? 2 : 1;  // the narrowest wave: one feature tile, or a gate and an up tile
+  const int64_t active = rows_ub < a.E ? rows_ub : a.E, mean = (rows_ub + a.E - 1) / a.E;
+  auto NT = [&](int wrows) {  // feature tiles of blocks of that many weight rows
+    const int64_t f = GATED ? wrows / 2 : wrows;
+    return (a.N + f - 1) / f;
+  };
+  auto likely = [&](int TM) {  // row tiles: a whole and half a tile an expert
+    const int64_t t = rows_ub / TM + active / 2;
+    return t > active ? t : active;
+  };
+  auto most = [&](int TM) {  // row tiles, at most
+    const int64_t t = rows_ub / TM + a.E;
+    return t < rows_ub ? t : rows_ub;
+  };
+  // few row tiles go over all XCDs; more are dealt to pairs of them
+  a.xcds = active < 8 ? 8 : 2;
+  if (mean > 24 && NT(256) * likely(64) >= 160)
+    return launch_timed(k_quant_tiles<8, 4, 2, GROUP, ACT>,
+                        dim3((unsigned)tile_grid(most(64), NT(256), a.xcds)), dim3(512), 0, st, a);
+  if (NT(256) * likely(32) >= 160)
+    return run_rows<2, 2, 8, 1, 3, true, GROUP, ACT>(a, most(32), NT(256), st);
+  if (!GATED && NT(128) * likely(32) >= 256)
+    return run_rows<2, F1, 8, 1, 2, true, GROUP, ACT>(a, most(32), NT(128 * F1), st);
+  if (mean > 8) return run_rows<2, F1, 4, 4, 2, true, GROUP, ACT>(a, most(32), NT(64 * F1), st);
+  if (NT(64 * F1) * likely(16) >= 192)
+    return run_rows<1, F1, 4, 4, 2, true, GROUP, ACT>(a, most(16), NT(64 * F1), st);
+  return run_rows<1, F1, 1, 8, 2, false, GROUP, ACT>(a, most(16), NT(16 * F1), st);
 }
 
 template <int ACT>
-hipError_t run_quant(int group, const QArgs& a, int64_t rows_ub, int64_t mean_rows,
-                     hipStream_t st) {
+hipError_t run_quant(int group, const QArgs& a, int64_t rows_ub, hipStream_t st) {
   if (rows_ub <= 0) return hipSuccess;
-  if (group == 32) return run_quant<32, ACT>(a, rows_ub, mean_rows, st);
-  if (group == 64) return run_quant<64, ACT>(a, rows_ub, mean_rows, st);
-  return run_quant<128, ACT>(a, rows_ub, mean_rows, st);
+  if (group == 32) return run_quant<32, ACT>(a, rows_ub, st);
+  if (group == 64) return run_quant<64, ACT>(a, rows_ub, st);
+  return run_quant<128, ACT>(a, rows_ub, st);
 }
 
 }  // namespace
@@ -403,39 +526,38 @@ hipError_t run_quant(int group, const QArgs& a, int64_t rows_ub, int64_t mean_ro
 hipError_t launch_quant_up(const moe_shape& s, const moe_quantized_experts& q, const void* x,
                            const int32_t* row_token, const int32_t* offsets, void* h,
                            int64_t rows_ub, hipStream_t st) {
-  QArgs a = {(const bf16_t*)x,
-             row_token,
-             offsets,
-             (const uint4*)q.w1_codes,
-             (const bf16_t*)q.w1_scales,
-             q.gated ? nullptr : (const bf16_t*)q.b1,
-             (bf16_t*)h,
-             s.n_experts,
-             s.d_ff,
-             s.d_model,
-             s.T,
-             (int)rows_ub};
-  const int64_t mean = (rows_ub + s.n_experts - 1) / s.n_experts;
-  return q.gated ? run_quant<kQGated>(q.group, a, rows_ub, mean, st)
-                 : run_quant<kQSilu>(q.group, a, rows_ub, mean, st);
+  QArgs a = {};
+  a.A = (const bf16_t*)x;
+  a.row_token = row_token;
+  a.offsets = offsets;
+  a.codes = (const uint4*)q.w1_codes;
+  a.scales = (const bf16_t*)q.w1_scales;
+  a.bias = (const bf16_t*)q.b1;
+  a.out = (bf16_t*)h;
+  a.E = s.n_experts;
+  a.N = s.d_ff;
+  a.K = s.d_model;
+  a.a_rows = s.T;
+  a.out_rows = (int)rows_ub;
+  return q.gated ? run_quant<kQGated>(q.group, a, rows_ub, st)
+                 : run_quant<kQSilu>(q.group, a, rows_ub, st);
 }
 
 hipError_t launch_quant_down(const moe_shape& s, const moe_quantized_experts& q, const void* h,
                              const int32_t* offsets, void* y, int64_t rows_ub, hipStream_t st) {
-  QArgs a = {(const bf16_t*)h,
-             nullptr,
-             offsets,
-             (const uint4*)q.w2_codes,
-             (const bf16_t*)q.w2_scales,
-             q.gated ? nullptr : (const bf16_t*)q.b2,
-             (bf16_t*)y,
-             s.n_experts,
-             s.d_model,
-             s.d_ff,
-             rows_ub,
-             (int)rows_ub};
-  const int64_t mean = (rows_ub + s.n_experts - 1) / s.n_experts;
-  return run_quant<kQNone>(q.group, a, rows_ub, mean, st);
+  QArgs a = {};
+  a.A = (const bf16_t*)h;
+  a.offsets = offsets;
+  a.codes = (const uint4*)q.w2_codes;
+  a.scales = (const bf16_t*)q.w2_scales;
+  a.bias = (const bf16_t*)q.b2;
+  a.out = (bf16_t*)y;
+  a.E = s.n_experts;
+  a.N = s.d_model;
+  a.K = s.d_ff;
+  a.a_rows = rows_ub;
+  a.out_rows = (int)rows_ub;
+  return run_quant<kQNone>(q.group, a, rows_ub, st);
 }
 
 }  // namespace moe

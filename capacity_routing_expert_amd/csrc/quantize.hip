@@ -7,11 +7,12 @@
 // w ~ s * value(code).
 //
 // Codes are stored in the order that the products read: blocks of 8 rows x 128 columns, 512
-// bytes each, [E][rows / 8][ceil(cols / 128)]; in a block, 16 bytes belong to row r and the
+// bytes each, [E][ceil(cols / 128)][rows / 8]; in a block, 16 bytes belong to row r and the
 // column octets o, o + 4, o + 8, o + 12 (o = 0 .. 3), at (8 o + r) 16, a dword an octet, its
 // first column in the lowest 4 bits.  So the 64 lanes of a wave that feed 16 rows x 32 columns
-// per matrix instruction read two whole blocks, 16 bytes a lane, for four instructions.  Scales:
-// [E][rows][ceil(cols / 128) 128 / group], the ones past cols zero.
+// per matrix instruction read two whole blocks, 16 bytes a lane, for four instructions, and the
+// waves of a workgroup, on neighbouring rows of the same columns, one run of memory.  Scales:
+// [E][ceil(cols / 128)][rows][128 / group], the ones past cols zero.
 //
 // Bound: HBM (2 or 4 bytes in, 0.5 + 2 / group out, a weight).  A wave takes one block; a lane
 // 16 columns of a row, so a group is 2, 4 or 8 lanes.
@@ -46,15 +47,14 @@ __device__ __forceinline__ void load8(const TIn* p, float* v) {
 template <typename TIn>
 __global__ __launch_bounds__(256) void k_quantize(const TIn* __restrict__ w,
                                                   uint32_t* __restrict__ codes,
-                                                  bf16_t* __restrict__ scales, int64_t row_tiles,
-                                                  int cols, int KC, int group) {
+                                                  bf16_t* __restrict__ scales, int64_t blocks,
+                                                  int rows, int cols, int KC, int group) {
   const int lane = threadIdx.x & 63, r = lane & 7, kg = lane >> 3;
   const int per = 128 / group;  // groups of a block of columns
-  const int64_t blocks = row_tiles * KC;
   for (int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); b < blocks;
        b += (int64_t)gridDim.x * 4) {
-    const int64_t row = b / KC * 8 + r;
-    const int kc = (int)(b % KC);
+    const int r8 = (int)(b % (rows / 8)), kc = (int)(b / (rows / 8) % KC);  // block [e][kc][r8]
+    const int64_t row = b / (rows / 8) / KC * rows + r8 * 8 + r;
     const int c0 = kc * 128 + kg * 16;
     float v[16];
 #pragma unroll
@@ -86,23 +86,23 @@ __global__ __launch_bounds__(256) void k_quantize(const TIn* __restrict__ w,
       const int oct = kg * 2 + h;
       codes[b * 128 + ((oct & 3) * 8 + r) * 4 + (oct >> 2)] = word;
     }
-    if (kg * 16 % group == 0)
-      scales[row * ((int64_t)KC * per) + kc * per + kg * 16 / group] = sb;
+    if (kg * 16 % group == 0) scales[(b * 8 + r) * per + kg * 16 / group] = sb;
   }
 }
 
 // One thread an octet of columns.
 __global__ __launch_bounds__(256) void k_dequantize(const uint32_t* __restrict__ codes,
                                                     const bf16_t* __restrict__ scales,
-                                                    float* __restrict__ w, int64_t rows, int cols,
-                                                    int KC, int group) {
+                                                    float* __restrict__ w, int64_t all_rows,
+                                                    int rows, int cols, int KC, int group) {
   const int per = 128 / group, octs = cols / 8;
-  const int64_t n = rows * octs;
+  const int64_t n = all_rows * octs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / octs;
     const int c = (int)(i % octs) * 8, kc = c / 128, oct = c % 128 / 8;
-    const uint32_t word = codes[(row / 8 * KC + kc) * 128 + ((oct & 3) * 8 + row % 8) * 4 + (oct >> 2)];
-    const float s = bf16_to_f32(scales[row * ((int64_t)KC * per) + kc * per + oct * 8 / group]);
+    const int64_t at = (row / rows * KC + kc) * rows + row % rows;  // [e][kc][row]
+    const uint32_t word = codes[at / 8 * 128 + ((oct & 3) * 8 + at % 8) * 4 + (oct >> 2)];
+    const float s = bf16_to_f32(scales[at * per + oct * 8 / group]);
     float* o = w + row * cols + c;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -126,14 +126,14 @@ int64_t quantized_scales_count(int64_t E, int rows, int cols, int group) {
 hipError_t launch_quantize(const void* w, bool bf16, int64_t E, int rows, int cols, int group,
                            void* codes, void* scales, hipStream_t st) {
   const int KC = (cols + 127) / 128;
-  const int64_t tiles = E * rows / 8, blocks = (tiles * KC + 3) / 4;
-  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+  const int64_t blocks = E * (rows / 8) * KC, wg = (blocks + 3) / 4;
+  const dim3 grid((unsigned)(wg < 65536 ? wg : 65536));
   if (bf16)
     hipLaunchKernelGGL(k_quantize<bf16_t>, grid, dim3(256), 0, st, (const bf16_t*)w,
-                       (uint32_t*)codes, (bf16_t*)scales, tiles, cols, KC, group);
+                       (uint32_t*)codes, (bf16_t*)scales, blocks, rows, cols, KC, group);
   else
     hipLaunchKernelGGL(k_quantize<float>, grid, dim3(256), 0, st, (const float*)w,
-                       (uint32_t*)codes, (bf16_t*)scales, tiles, cols, KC, group);
+                       (uint32_t*)codes, (bf16_t*)scales, blocks, rows, cols, KC, group);
   return hipGetLastError();
 }
 
@@ -141,7 +141,7 @@ hipError_t launch_dequantize(const void* codes, const void* scales, int64_t E, i
                              int group, float* w, hipStream_t st) {
   const int64_t n = E * rows * (cols / 8), blocks = (n + 255) / 256;
   hipLaunchKernelGGL(k_dequantize, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
-                     st, (const uint32_t*)codes, (const bf16_t*)scales, w, E * rows, cols,
+                     st, (const uint32_t*)codes, (const bf16_t*)scales, w, E * rows, rows, cols,
                      (cols + 127) / 128, group);
   return hipGetLastError();
 }

@@ -423,10 +423,10 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
  * magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; one bf16 scale serves `group` (32, 64 or 128) consecutive
  * columns of a row.  Storage of an [E, rows, cols] array (rows and cols multiples of 8), with
  * KC = ceil(cols / 128):
- *   codes  [E][rows / 8][KC] blocks of 512 bytes, 8 rows x 128 columns: column c of row r of a
+ *   codes  [E][KC][rows / 8] blocks of 512 bytes, 8 rows x 128 columns: column c of row r of a
  *          block is in the dword ((c % 32 / 8 * 8 + r) * 4 + c / 32), bits 4 (c % 8) and up, sign
  *          highest; columns past cols are zero
- *   scales [E][rows][KC * 128 / group] bf16, zero past cols */
+ *   scales [E][KC][rows][128 / group] bf16, zero past cols */
 
 /* Bytes of the two arrays; 0 for an invalid shape, rows or cols not multiples of 8, or a group
  * that is not 32, 64 or 128. */
@@ -464,7 +464,8 @@ typedef struct {
  * workspace moe_workspace_bytes(shape).  Of each group the products of x and the codes' values are
  * exact and summed in fp32, and the scale multiplies that sum: no weight is rounded.  The
  * activation between the products is stored as bf16, as moe_expert_ffn stores it.  Rows past the
- * last kept one are not written. */
+ * last kept one are not written.  MOE_ERR_UNSUPPORTED when the codes of one expert's W1 (W13) or
+ * W2 reach 2 GiB. */
 moe_status moe_expert_ffn_quantized(const moe_shape* shape, const void* x,
                                     const int32_t* row_token, const int32_t* expert_offsets,
                                     const moe_quantized_experts* experts, void* y_rows, void* ws,

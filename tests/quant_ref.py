@@ -45,19 +45,21 @@ def pack(codes):
     KC = -(-cols // 128)
     c = np.zeros((E, rows, KC * 128), np.uint32)
     c[:, :, :cols] = codes
-    words = np.zeros((E, rows // 8, KC, 128), np.uint32)
+    words = np.zeros((E, KC, rows // 8, 128), np.uint32)
     for r in range(8):
         for col in range(128):
             words[:, :, :, (col % 32 // 8 * 8 + r) * 4 + col // 32] |= (
-                c[:, r::8, col::128] << np.uint32(4 * (col % 8)))
+                c[:, r::8, col::128].transpose(0, 2, 1) << np.uint32(4 * (col % 8)))
     return words.reshape(-1).view(np.uint8)
 
 
-def pad_scales(scales, cols, group):
+def pack_scales(scales, cols, group):
+    """The storage of include/moe.h: [E][KC][rows][128 / group]."""
     E, rows, G = scales.shape
-    out = np.zeros((E, rows, -(-cols // 128) * (128 // group)), np.float32)
+    KC, per = -(-cols // 128), 128 // group
+    out = np.zeros((E, rows, KC * per), np.float32)
     out[:, :, :G] = scales
-    return out
+    return out.reshape(E, rows, KC, per).transpose(0, 2, 1, 3)
 
 
 def silu(v):

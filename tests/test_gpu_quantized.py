@@ -55,7 +55,7 @@ def test_quantize(E, rows, cols, group, dtype):
     codes, scales = L.quantize_weights(
         torch.from_numpy(w).to(DEV).to(torch.bfloat16 if dtype == "bf16" else torch.float32), group)
     want_c, want_s = Q.quantize(w, group)
-    assert np.array_equal(scales.float().cpu().numpy(), Q.pad_scales(want_s, cols, group).reshape(-1))
+    assert np.array_equal(scales.float().cpu().numpy(), Q.pack_scales(want_s, cols, group).reshape(-1))
     assert np.array_equal(codes.cpu().numpy(), Q.pack(want_c))
     back = L.dequantize_weights(codes, scales, E, rows, cols, group).cpu().numpy()
     assert np.array_equal(back.astype(np.float64), Q.dequantize(want_c, want_s, group))

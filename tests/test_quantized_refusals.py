@@ -39,7 +39,7 @@ def test_reference_storage_is_the_header_formula():
     KC = 2
     for _ in range(500):
         e, r, c = rng.integers(E), rng.integers(rows), rng.integers(cols)
-        block = (e * (rows // 8) + r // 8) * KC + c // 128
+        block = (e * KC + c // 128) * (rows // 8) + r // 8
         cb = c % 128
         word = words[block * 128 + (cb % 32 // 8 * 8 + r % 8) * 4 + cb // 32]
         assert word >> (4 * (cb % 8)) & 15 == codes[e, r, c]
@@ -103,6 +103,8 @@ GATED = dict(gated=1, b1=None, b2=None)
     (dict(dtype=B.MOE_F32), {}, 2, "bf16 only"),
     (dict(weight_layout=B.MOE_WEIGHTS_PACKED), {}, 1, "own storage"),
     ({}, dict(GATED, w2_codes=P(4)), 2, "w2_codes"), (dict(top_k=99), {}, 1, "top_k"),
+    (dict(d_model=1 << 16, d_ff=1 << 16), {}, 2, "2 GiB"),
+    (dict(d_model=1 << 16, d_ff=1 << 15), GATED, 2, "2 GiB"),
 ])
 def test_expert_refusals(lib, shape_kw, kw, status, text):
     s, q = shape(**shape_kw), experts(**kw)
