@@ -551,13 +551,18 @@ def moe_pack_weights(shape, w, w_packed, stream=None):
            "moe_pack_weights")
 
 
-def _cur(t, name: str, dtype=None, numel: int | None = None):
-    """_ptr, and the tensor has to be on the current device (the one whose stream the call takes)."""
-    p = _ptr(t, name, dtype, numel=numel)
-    if p is not None and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return p
+def _cur(t, name: str, dtype=None, numel: int = 0):
+    """_ptr, and the tensor has to be on the current device (the one whose stream the call takes).
+    Everything is looked at once; only a tensor that something is wrong with takes the long way."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and
+            t.numel() >= numel and t.is_cuda and t.is_contiguous() and
+            t.get_device() == torch.cuda.current_device()):
+        return t.data_ptr()
+    _ptr(t, name, dtype, numel=numel)
+    raise ValueError(f"{name} is on {t.device}, the current device is "
+                     f"cuda:{torch.cuda.current_device()}")
 
 
 def workspace_bytes_balance(shape: MoeShape) -> int:
@@ -573,15 +578,15 @@ def moe_balance_loss(shape, logits, topk_ids, loss, expert_counts=None, expert_p
                      stream=None):
     """Balance loss [1] and, where given, the counts [E], mean probabilities [E] and gradient on
     the logits [T, E]; token_mask [T] uint8, 0 for padding."""
-    n = _n(shape)
+    T, E, k = shape.T, shape.n_experts, shape.top_k
     _check(lib().moe_balance_loss(
-        ctypes.byref(shape), _cur(logits, "logits", torch.float32, numel=n["TE"]),
-        _cur(topk_ids, "topk_ids", torch.int32, numel=n["Tk"]),
-        _cur(token_mask, "token_mask", torch.uint8, numel=n["T"]), float(coef), float(grad_scale),
+        ctypes.byref(shape), _cur(logits, "logits", torch.float32, numel=T * E),
+        _cur(topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(token_mask, "token_mask", torch.uint8, numel=T), float(coef), float(grad_scale),
         _cur(loss, "loss", torch.float32, numel=1),
-        _cur(expert_counts, "expert_counts", torch.int32, numel=n["E"]),
-        _cur(expert_probs, "expert_probs", torch.float32, numel=n["E"]),
-        _cur(dlogits, "dlogits", torch.float32, numel=n["TE"]), _cur(ws, "ws", torch.uint8),
+        _cur(expert_counts, "expert_counts", torch.int32, numel=E),
+        _cur(expert_probs, "expert_probs", torch.float32, numel=E),
+        _cur(dlogits, "dlogits", torch.float32, numel=T * E), _cur(ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream)), "moe_balance_loss")
 
 
@@ -590,17 +595,17 @@ def moe_route_backward(shape, x, w_router, logits, topk_ids, dgates, dlogits, dx
                        stream=None):
     """Gradients of the router: dx [T, d] in the shape's dtype, dw_router [E, d] and db_router [E]
     in fp32, each optional; dgates [T, k] or dlogits [T, E] (or both) come in."""
-    dt, n = _dtype_of(shape), _n(shape)
-    f32 = torch.float32
+    dt, f32 = _dtype_of(shape), torch.float32
+    T, d, E, k = shape.T, shape.d_model, shape.n_experts, shape.top_k
     _check(lib().moe_route_backward(
-        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
-        _cur(w_router, "w_router", dt, numel=n["wr"]), _cur(logits, "logits", f32, numel=n["TE"]),
-        _cur(topk_ids, "topk_ids", torch.int32, numel=n["Tk"]),
-        _cur(dgates, "dgates", f32, numel=n["Tk"]), _cur(dlogits, "dlogits", f32, numel=n["TE"]),
-        _cur(token_mask, "token_mask", torch.uint8, numel=n["T"]),
-        _cur(dx_add, "dx_add", dt, numel=n["x"]), _cur(dx, "dx", dt, numel=n["x"]),
-        _cur(dw_router, "dw_router", f32, numel=n["wr"]),
-        _cur(db_router, "db_router", f32, numel=n["E"]), _cur(ws, "ws", torch.uint8),
+        ctypes.byref(shape), _cur(x, "x", dt, numel=T * d),
+        _cur(w_router, "w_router", dt, numel=E * d), _cur(logits, "logits", f32, numel=T * E),
+        _cur(topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(dgates, "dgates", f32, numel=T * k), _cur(dlogits, "dlogits", f32, numel=T * E),
+        _cur(token_mask, "token_mask", torch.uint8, numel=T),
+        _cur(dx_add, "dx_add", dt, numel=T * d), _cur(dx, "dx", dt, numel=T * d),
+        _cur(dw_router, "dw_router", f32, numel=E * d),
+        _cur(db_router, "db_router", f32, numel=E), _cur(ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_backward")
 
 
@@ -682,12 +687,13 @@ class QuantizedExperts:
 def moe_expert_ffn_quantized(shape, x, row_token, expert_offsets, experts, y_rows, ws,
                              stream=None):
     """moe_expert_ffn with QuantizedExperts."""
-    dt, n = _dtype_of(shape), _n(shape)
+    dt, T, d = _dtype_of(shape), shape.T, shape.d_model
+    rows = min(T * shape.top_k, shape.n_experts * shape.capacity)  # moe_max_kept_rows
     _check(lib().moe_expert_ffn_quantized(
-        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
-        _cur(row_token, "row_token", torch.int32, numel=n["rows"]) if row_token.numel() else None,
-        _cur(expert_offsets, "expert_offsets", torch.int32, numel=n["E1"]), experts.of(shape),
-        _cur(y_rows, "y_rows", dt, numel=n["yrows"]) if y_rows.numel() else None,
+        ctypes.byref(shape), _cur(x, "x", dt, T * d),
+        _cur(row_token, "row_token", torch.int32, rows) if row_token.numel() else None,
+        _cur(expert_offsets, "expert_offsets", torch.int32, shape.n_experts + 1),
+        experts.of(shape), _cur(y_rows, "y_rows", dt, rows * d) if y_rows.numel() else None,
         _cur(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "moe_expert_ffn_quantized")
 
 

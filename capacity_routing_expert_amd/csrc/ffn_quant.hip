@@ -367,8 +367,11 @@ __global__ __launch_bounds__(64 * WF * WK) void k_quant_rows(QArgs a) {
 template <int WF, int RT, int FT, int GROUP, int ACT>
 __global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
   constexpr bool GATED = ACT == kQGated;
-  constexpr int FO = GATED ? FT / 2 : FT, S = 128 / GROUP, J = GROUP / 32;
-  constexpr int XL = RT * 4 / WF, NI = RT * S;  // NI items of a column block: (row group, scale group)
+  // columns whose sum is scaled at once: groups of 128 in halves, as chains of four dependent matrix
+  // instructions leave gaps (group 128 in one: 385 / 344 us, in halves as group 64)
+  constexpr int CG = GROUP == 128 ? 64 : GROUP;
+  constexpr int FO = GATED ? FT / 2 : FT, S = 128 / CG, J = CG / 32;
+  constexpr int XL = RT * 4 / WF, NI = RT * S;  // NI items of a column block: (row group, columns)
   static_assert(RT * 4 % WF == 0, "whole fragments a wave");
   __shared__ uint4 xs[2][RT * 4][64];
   const int lane = threadIdx.x & 63;
@@ -416,7 +419,7 @@ __global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
       B[f][2] = values_of(cw[f].z);
       B[f][3] = values_of(cw[f].w);
 #pragma unroll
-      for (int g = 0; g < S; ++g) s[f][g] = sc[f].get(g);
+      for (int g = 0; g < S; ++g) s[f][g] = sc[f].get(g * CG / GROUP);
     }
     w.load(kc + 1, cw, sc);
     bf16x8_t A[2][J];

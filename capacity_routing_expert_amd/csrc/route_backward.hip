@@ -52,11 +52,12 @@ BackwardLayout backward_layout(const moe_shape& s) {
   L.EK = bf ? (E + 7) / 8 * 8 : (E + 3) / 4 * 4;
   const int64_t tiles = L.Tp / kTT;
   L.dl_blocks = tiles < kMaxDlBlocks ? tiles : kMaxDlBlocks;
-  // blocks of dW_r: column tiles x groups of 64 experts x token ranges; about two a compute
-  // unit, and at least 128 tokens a range
+  // blocks of dW_r: column tiles x groups of 64 experts x token ranges; about one a compute
+  // unit, and at least 128 tokens a range (T 16384, E 64, d 2048: 25 us, with twice the blocks 33,
+  // as each writes a partial dW_r of its own)
   const int64_t cols = bf ? kCols : kColsF32;
   const int64_t base = (d + cols - 1) / cols * ((E + 63) / 64);
-  int64_t splits = (512 + base - 1) / base;
+  int64_t splits = (256 + base - 1) / base;
   const int64_t most = (s.T + 127) / 128;
   if (splits > most) splits = most;
   L.splits = splits < 1 ? 1 : splits;
@@ -86,47 +87,85 @@ struct DlArgs {
   int E, EK, k;
   void* dl_x;      // or NULL
   void* dl_w;      // or NULL
-  uint8_t* valid;
+  uint8_t* valid;  // or NULL
   float* db_part;  // or NULL
 };
 
+// Block -> (column tile, token range) with `cols` column tiles a range.  Workgroups go round-robin
+// over the 8 XCDs; the column tiles of one range stay on one XCD, so dl, which all of them read,
+// comes through one L2.
+__device__ __forceinline__ bool range_of(int cols, int64_t ranges, int& col, int64_t& range) {
+  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+  col = slot % cols;
+  range = (int64_t)(slot / cols) * 8 + xcd;
+  return range < ranges;
+}
+int64_t range_grid(int64_t cols, int64_t ranges) { return 8 * cols * ((ranges + 7) / 8); }
+
+constexpr int kDlThreads = 512;
+constexpr int kDlChoices = 8;  // choices staged at a time
+
 // One block takes tiles of 64 tokens: softmax gradients of the tile's rows into LDS, [expert]
 // [token] with a pitch of 65 words, then both layouts from there.  Rows past T and masked rows
-// are zero, so the product kernels need no guards on dl.
+// are zero, so the product kernels need no guards on dl.  Latency-bound: 64 tokens a block are
+// few loads, so the logits of the first rows and the choices are asked for before anything waits.
 template <typename Row, bool BF>
-__global__ __launch_bounds__(256) void k_route_dlogits(DlArgs a) {
-  constexpr int LPT = Row::LPT, NV = Row::NV, TPW = Row::TPW, P = kTT + 1;
-  extern __shared__ float tile[];  // [E][P]
+__global__ __launch_bounds__(kDlThreads) void k_route_dlogits(DlArgs a) {
+  constexpr int LPT = Row::LPT, NV = Row::NV, TPW = Row::TPW, P = kTT + 1, NW = kDlThreads / 64;
+  extern __shared__ float tile[];  // [E][P], then [E][8] partial sums of db
+  __shared__ int sid[kTT * kDlChoices];
+  __shared__ float sgate[kTT * kDlChoices];
   const int E = a.E, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane % LPT;
+  float* dbs = tile + E * P;
   float db = 0.0f;
   for (int64_t tb = (int64_t)blockIdx.x * kTT; tb < a.Tp; tb += (int64_t)gridDim.x * kTT) {
-    // gate gradients scattered to their experts: one thread a token, choices in order
-    if (a.dgates) {
-      for (int i = tid; i < E * P; i += 256) tile[i] = 0.0f;
-      __syncthreads();
-      const int64_t t = tb + tid;
-      if (tid < kTT && t < a.T && (!a.mask || a.mask[t]))
-        for (int c = 0; c < a.k; ++c) {
-          const int id = a.ids[t * a.k + c];
-          if ((unsigned)id < (unsigned)E) tile[id * P + tid] += a.dgates[t * a.k + c];
-        }
-      __syncthreads();
-    }
-    for (int g = wave * TPW; g < kTT; g += 4 * TPW) {
+    float p[NV], in[NV];
+    bool valid = false;
+    auto load = [&](int g) {  // rows g .. g + TPW - 1 of the tile
       const int tl = g + lane / LPT;
       const int64_t t = tb + tl;
-      const bool valid = tl < kTT && t < a.T && (!a.mask || a.mask[t]);
+      valid = tl < kTT && t < a.T && (!a.mask || a.mask[t]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        p[i] = -INFINITY;  // not valid: probabilities 0
+        in[i] = 0.0f;
+      }
+      if (valid && a.dgates) Row::load(a.logits + t * E, E, l, -INFINITY, p);
+      if (valid && a.dlogits) Row::load(a.dlogits + t * E, E, l, 0.0f, in);
+    };
+    load(wave * TPW);
+    // gate gradients scattered to their experts: one thread a token, choices in order
+    if (a.dgates) {
+      for (int i = tid; i < E * P; i += kDlThreads) tile[i] = 0.0f;
+      for (int c0 = 0; c0 < a.k; c0 += kDlChoices) {
+        const int tl = tid / kDlChoices, c = c0 + tid % kDlChoices;
+        const int64_t t = tb + tl;
+        int id = -1;
+        float gate = 0.0f;
+        if (c < a.k && t < a.T && (!a.mask || a.mask[t])) {
+          id = a.ids[t * a.k + c];
+          gate = a.dgates[t * a.k + c];
+        }
+        sid[tid] = id;
+        sgate[tid] = gate;
+        __syncthreads();
+        if (tid < kTT) {
+#pragma unroll
+          for (int j = 0; j < kDlChoices; ++j) {
+            const int e = sid[tid * kDlChoices + j];
+            if ((unsigned)e < (unsigned)E) tile[e * P + tid] += sgate[tid * kDlChoices + j];
+          }
+        }
+        __syncthreads();
+      }
+    }
+    for (int g = wave * TPW; g < kTT; g += NW * TPW) {
+      const int tl = g + lane / LPT;
       float dl[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) dl[i] = 0.0f;
       if (a.dgates) {
-        float p[NV], dot = 0.0f;
-        if (valid) {
-          Row::load(a.logits + t * E, E, l, -INFINITY, p);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) p[i] = -INFINITY;
-        }
+        float dot = 0.0f;
         Row::softmax(p);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -138,29 +177,24 @@ __global__ __launch_bounds__(256) void k_route_dlogits(DlArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) dl[i] = p[i] * (dl[i] - dot);
       }
-      if (a.dlogits && valid) {
-        float in[NV];
-        Row::load(a.dlogits + t * E, E, l, 0.0f, in);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dl[i] += in[i];
-      }
+      for (int i = 0; i < NV; ++i) dl[i] = valid ? dl[i] + in[i] : 0.0f;
       if (tl < kTT) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int e = Row::expert(l, i);
-          if (e < E) tile[e * P + tl] = valid ? dl[i] : 0.0f;
+          if (e < E) tile[e * P + tl] = dl[i];
         }
-        if (l == 0) a.valid[t] = valid;
+        if (l == 0 && a.valid) a.valid[tb + tl] = valid;
       }
+      load(g + NW * TPW);
     }
     __syncthreads();
-    if (a.db_part && tid < E)
-      for (int t = 0; t < kTT; ++t) db += tile[tid * P + t];
     if (a.dl_x) {
       constexpr int W = BF ? 8 : 4;  // experts of a 16-byte chunk
       const int chunks = a.EK / W;
-      for (int i = tid; i < kTT * chunks; i += 256) {
-        const int tl = i % kTT, e0 = i / kTT * W;
+      for (int i = tid; i < kTT * chunks; i += kDlThreads) {
+        const int tl = i / chunks, e0 = i % chunks * W;
         float v[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) v[j] = e0 + j < E ? tile[(e0 + j) * P + tl] : 0.0f;
@@ -182,12 +216,17 @@ __global__ __launch_bounds__(256) void k_route_dlogits(DlArgs a) {
         }
       }
     }
-    if (a.dl_w) {
-      for (int i = tid; i < E * (kTT / 8); i += 256) {
+    if (a.dl_w || a.db_part) {
+      for (int i = tid; i < E * (kTT / 8); i += kDlThreads) {
         const int e = i / (kTT / 8), t0 = i % (kTT / 8) * 8;
-        float v[8];
+        float v[8], sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = tile[e * P + t0 + j];
+        for (int j = 0; j < 8; ++j) {
+          v[j] = tile[e * P + t0 + j];
+          sum += v[j];
+        }
+        if (a.db_part) dbs[i] = sum;
+        if (!a.dl_w) continue;
         const int64_t at = (int64_t)e * a.Tp + tb + t0;
         if constexpr (BF) {
           bf16_t* o = static_cast<bf16_t*>(a.dl_w);
@@ -211,6 +250,8 @@ __global__ __launch_bounds__(256) void k_route_dlogits(DlArgs a) {
       }
     }
     __syncthreads();  // the tile is overwritten by the next one
+    if (a.db_part && tid < E)
+      for (int j = 0; j < kTT / 8; ++j) db += dbs[tid * (kTT / 8) + j];
   }
   if (a.db_part && tid < E) a.db_part[(int64_t)blockIdx.x * E + tid] = db;
 }
@@ -240,12 +281,16 @@ __device__ __forceinline__ void transpose8x8(const uint4 (&r)[8], uint4 (&out)[8
 __global__ __launch_bounds__(256) void k_route_dx_bf16(const bf16_t* __restrict__ dl,
                                                        const bf16_t* __restrict__ w,
                                                        const bf16_t* add, bf16_t* dx, int64_t T,
-                                                       int64_t Tp, int d, int E, int EK) {
+                                                       int64_t Tp, int d, int E, int EK,
+                                                       int64_t ranges) {
   extern __shared__ uint4 wfrag[];  // [KS][8][64]
+  int cb;
+  int64_t range;
+  if (!range_of((d + kCols - 1) / kCols, ranges, cb, range)) return;  // block-uniform
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, kg = lane >> 4;
   const int KS = (E + 31) / 32;
-  const int col = blockIdx.x * kCols + 8 * n;
+  const int col = cb * kCols + 8 * n;
   const bool incol = col < d;
   for (int ks = wave; ks < KS; ks += 4) {
     uint4 r[8], o[8];
@@ -260,35 +305,53 @@ __global__ __launch_bounds__(256) void k_route_dx_bf16(const bf16_t* __restrict_
     for (int i = 0; i < 8; ++i) wfrag[(ks * 8 + i) * 64 + lane] = o[i];
   }
   __syncthreads();
-  const int64_t step = (int64_t)gridDim.y * 128;
-  for (int64_t t0 = (int64_t)blockIdx.y * 128 + wave * 32; t0 < T; t0 += step) {
+  const int64_t step = ranges * 128;
+  // chunks of experts past EK repeat the last one's: they meet zero rows of W_r
+  uint4 A[2][2];
+  auto load = [&](int64_t t0, int ks) {
+    const int64_t tt = min(t0, Tp - 32);
+    const int e = min(ks * 32 + kg * 8, EK - 8);
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+        A[rt][term] = *reinterpret_cast<const uint4*>(
+            dl + ((int64_t)term * Tp + tt + rt * 16 + n) * EK + e);
+  };
+  uint4 next[2][4];
+  auto load_add = [&](int64_t t0) {
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t t = t0 + rt * 16 + kg * 4 + j;
+        next[rt][j] = make_uint4(0, 0, 0, 0);
+        if (add && t < T && incol) next[rt][j] = *reinterpret_cast<const uint4*>(add + t * d + col);
+      }
+  };
+  int64_t t0 = range * 128 + wave * 32;
+  load(t0, 0);
+  load_add(t0);
+  for (; t0 < T; t0 += step) {
     uint4 ad[2][4];
-    if (add) {
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
+    for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t t = t0 + rt * 16 + kg * 4 + j;
-          ad[rt][j] = make_uint4(0, 0, 0, 0);
-          if (t < T && incol) ad[rt][j] = *reinterpret_cast<const uint4*>(add + t * d + col);
-        }
-    }
+      for (int j = 0; j < 4; ++j) ad[rt][j] = next[rt][j];
+    load_add(t0 + step);
     f32x4_t acc[2][8];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[rt][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     for (int ks = 0; ks < KS; ++ks) {
-      uint4 A[2][2];
+      bf16x8_t C[2][2];
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const int e = ks * 32 + kg * 8;
-          A[rt][term] = make_uint4(0, 0, 0, 0);
-          if (e < EK)
-            A[rt][term] = *reinterpret_cast<const uint4*>(dl + ((int64_t)term * Tp + t0 + rt * 16 + n) * EK + e);
-        }
+        for (int term = 0; term < 2; ++term) C[rt][term] = frag(A[rt][term]);
+      const bool last = ks + 1 == KS;
+      load(last ? t0 + step : t0, last ? 0 : ks + 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bf16x8_t B = frag(wfrag[(ks * 8 + i) * 64 + lane]);
@@ -296,8 +359,8 @@ __global__ __launch_bounds__(256) void k_route_dx_bf16(const bf16_t* __restrict_
         for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
           for (int term = 1; term >= 0; --term)  // the small term first
-            acc[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(A[rt][term]), B, acc[rt][i],
-                                                                 0, 0, 0);
+            acc[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(C[rt][term], B, acc[rt][i], 0, 0,
+                                                                 0);
       }
     }
 #pragma unroll
@@ -326,55 +389,79 @@ __global__ __launch_bounds__(256) void k_route_dx_bf16(const bf16_t* __restrict_
 
 // ---------------------------------------------------------------- dW_r, bf16
 // A wave holds 16 MT experts x 128 columns of dW_r in accumulators and walks 32-token steps of
-// its block's range.  The token axis is the contraction, so x enters transposed: a lane loads 8
-// rows of 8 columns (16-byte loads, 256 contiguous bytes a row over 16 lanes) and 32 byte
-// permutations make its eight fragments, tile i holding columns 8 n + i.  The four waves take
-// the steps in turn and are added in wave order; token ranges are added by k_route_reduce.
+// its block's range, the next step's loads in flight during the present one's products.  The token
+// axis is the contraction, so x enters transposed: a lane loads 8 rows of 8 columns (16-byte
+// loads, 256 contiguous bytes a row over 16 lanes) and 32 byte permutations make its eight
+// fragments, tile i holding columns 8 n + i.  The four waves take the steps in turn and are added
+// in wave order; token ranges are added by k_route_reduce.  valid: NULL when no token is masked.
 template <int MT>
 __global__ __launch_bounds__(256) void k_route_dw_bf16(const bf16_t* __restrict__ dl,
                                                        const bf16_t* __restrict__ x,
                                                        const uint8_t* __restrict__ valid,
                                                        float* __restrict__ out, int64_t T,
-                                                       int64_t Tp, int d, int E, int64_t per) {
+                                                       int64_t Tp, int d, int E, int64_t per,
+                                                       int64_t ranges) {
   __shared__ float4 red[2][MT * 8][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int cb;
+  int64_t range;
+  if (!range_of((d + kCols - 1) / kCols, ranges, cb, range)) return;  // block-uniform
+  const int e0 = blockIdx.y * 64;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  const int col = blockIdx.x * kCols + 8 * n;
+  const int col = cb * kCols + 8 * n;
   const bool incol = col < d;
-  const int e0 = blockIdx.z * 64;
   f32x4_t acc[MT][8];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[m][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t ts = blockIdx.y * per, te = ts + per < T ? ts + per : T;
-  for (int64_t t0 = ts + wave * 32; t0 < te; t0 += 128) {
-    // a masked token's row is not read (whatever it holds counts as zeros)
-    const uint2 ok = *reinterpret_cast<const uint2*>(valid + t0 + kg * 8);
-    uint4 r[8], B[8], A[MT][3];
+  const int64_t ts = range * per, te = ts + per < T ? ts + per : T;
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(x, (uint32_t)(T * d * 2));  // below 2 GiB
+  const bf16_t* dp[MT];  // rows of experts past E repeat the last one's; they are not stored
+#pragma unroll
+  for (int m = 0; m < MT; ++m) dp[m] = dl + (int64_t)min(e0 + m * 16 + n, E - 1) * Tp + kg * 8;
+  uint4 r[8], A[MT][3];
+  // a masked token's row is not read (whatever it holds counts as zeros)
+  auto mask_of = [&](int64_t t0) -> uint2 {
+    if (valid) return *reinterpret_cast<const uint2*>(valid + min(t0, Tp - 32) + kg * 8);
+    return make_uint2(0x01010101u, 0x01010101u);
+  };
+  auto load = [&](int64_t t0, uint2 ok) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r[j] = make_uint4(0, 0, 0, 0);
-      const uint32_t b = ((j < 4 ? ok.x : ok.y) >> (8 * (j & 3))) & 1;
-      if (b && incol) r[j] = *reinterpret_cast<const uint4*>(x + (t0 + kg * 8 + j) * d + col);
+      const int64_t t = t0 + kg * 8 + j;
+      const bool in = incol && t < te && ((j < 4 ? ok.x : ok.y) >> (8 * (j & 3)) & 1);
+      r[j] = buffer_load16(xr, in ? (uint32_t)(t * d + col) * 2 : 0x80000000u);
     }
+    const int64_t td = min(t0, Tp - 32);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int term = 0; term < 3; ++term) {
-        const int e = e0 + m * 16 + n;
-        A[m][term] = make_uint4(0, 0, 0, 0);
-        if (e < E)
-          A[m][term] = *reinterpret_cast<const uint4*>(dl + ((int64_t)term * E + e) * Tp + t0 + kg * 8);
-      }
+      for (int term = 0; term < 3; ++term)
+        A[m][term] = *reinterpret_cast<const uint4*>(dp[m] + (int64_t)term * E * Tp + td);
+  };
+  int64_t t0 = ts + wave * 32;
+  uint2 ok = mask_of(t0);
+  load(t0, ok);
+  ok = mask_of(t0 + 128);
+  for (; t0 < te; t0 += 128) {
+    uint4 B[8], C[MT][3];
     transpose8x8(r, B);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int term = 2; term >= 0; --term)
+      for (int term = 0; term < 3; ++term) C[m][term] = A[m][term];
+    load(t0 + 128, ok);
+    ok = mask_of(t0 + 256);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int term = 2; term >= 0; --term)  // the small terms first
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(A[m][term]), frag(B[i]),
+          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(C[m][term]), frag(B[i]),
                                                               acc[m][i], 0, 0, 0);
   }
   // waves 2, 3 into 0, 1, then 1 into 0
@@ -403,7 +490,7 @@ __global__ __launch_bounds__(256) void k_route_dw_bf16(const bf16_t* __restrict_
     __syncthreads();
   }
   if (wave || !incol) return;
-  float* o = out + (int64_t)blockIdx.y * E * d;
+  float* o = out + range * E * d;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -472,7 +559,7 @@ __global__ __launch_bounds__(256) void k_route_dw_f32(const float* __restrict__ 
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int64_t t = t0 + q * 4 + kg;
-      const bool ok = valid[t];
+      const bool ok = t < T && (!valid || valid[t]);
       float A[MT], B[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -578,7 +665,7 @@ hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* 
   const int E = s.n_experts, d = s.d_model;
   const bool bf = s.dtype == MOE_BF16;
   float* dw_part = L.splits > 1 ? reinterpret_cast<float*>(b + L.dw_part) : dw;
-  float* db_part = reinterpret_cast<float*>(b + L.db_part);
+  float* db_part = L.dl_blocks > 1 ? reinterpret_cast<float*>(b + L.db_part) : db;
   hipError_t err;
   if (s.T > 0) {
     DlArgs a = {};
@@ -594,69 +681,74 @@ hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* 
     a.k = s.top_k;
     a.dl_x = dx ? b + L.dl_x : nullptr;
     a.dl_w = dw ? b + L.dl_w : nullptr;
-    a.valid = reinterpret_cast<uint8_t*>(b + L.valid);
+    a.valid = mask ? reinterpret_cast<uint8_t*>(b + L.valid) : nullptr;
     a.db_part = db ? db_part : nullptr;
     const bool vec = E % 4 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)dlogits % 16 == 0;
     err = with_router_row(E, vec, [&](auto row) -> hipError_t {
       using Row = decltype(row);
       auto kern = bf ? k_route_dlogits<Row, true> : k_route_dlogits<Row, false>;
-      const int lds = E * (kTT + 1) * 4;
-      if (lds > 64 * 1024) {
+      const int lds = E * (kTT + 1 + kTT / 8) * 4;
+      if (lds > 60 * 1024) {
         static std::atomic<bool> done_bf[kMaxDevices], done_f32[kMaxDevices];
-        if (hipError_t e = allow_dynamic_lds((const void*)kern, 256 * (kTT + 1) * 4, bf ? done_bf : done_f32);
+        if (hipError_t e = allow_dynamic_lds((const void*)kern, 256 * (kTT + 1 + kTT / 8) * 4, bf ? done_bf : done_f32);
             e != hipSuccess)
           return e;
       }
-      hipLaunchKernelGGL(kern, dim3((unsigned)L.dl_blocks), dim3(256), lds, st, a);
+      hipLaunchKernelGGL(kern, dim3((unsigned)L.dl_blocks), dim3(kDlThreads), lds, st, a);
       return hipGetLastError();
     });
     if (err != hipSuccess) return err;
-    if (dx) {
-      const int64_t cols = bf ? kCols : kColsF32, ct = (d + cols - 1) / cols;
-      const int64_t rows = bf ? 128 : 64;  // tokens of a block at a time
-      int64_t tb = (s.T + rows - 1) / rows, want = (1024 + ct - 1) / ct;
-      tb = tb < want ? tb : want;
-      const dim3 grid((unsigned)ct, (unsigned)tb);
-      if (bf)
-        hipLaunchKernelGGL(k_route_dx_bf16, grid, dim3(256), (size_t)(E + 31) / 32 * 8192, st,
-                           (const bf16_t*)(b + L.dl_x), (const bf16_t*)w, (const bf16_t*)dx_add,
-                           (bf16_t*)dx, s.T, L.Tp, d, E, (int)L.EK);
-      else
-        hipLaunchKernelGGL(k_route_dx_f32, grid, dim3(256), 0, st, (const float*)(b + L.dl_x),
-                           (const float*)w, (const float*)dx_add, (float*)dx, s.T, d, E,
-                           (int)L.EK);
+    const int64_t cols = bf ? kCols : kColsF32, ct = (d + cols - 1) / cols;
+    const int64_t rows = bf ? 128 : 64;  // tokens of a dx block at a time
+    int64_t tb = (s.T + rows - 1) / rows;
+    if (tb > (1024 + ct - 1) / ct) tb = (1024 + ct - 1) / ct;
+    int64_t per = (s.T + L.splits - 1) / L.splits;
+    per = (per + 127) / 128 * 128;
+    const uint8_t* valid = mask ? reinterpret_cast<const uint8_t*>(b + L.valid) : nullptr;
+    const int e_groups = (E + 63) / 64;
+    // one launch for both products was slower: reads alone and reads with writes mixed on the same
+    // channels (T 16384, E 64: 71 us against 33 + 25)
+    if (bf && dx) {
+      hipLaunchKernelGGL(k_route_dx_bf16, dim3((unsigned)range_grid(ct, tb)), dim3(256),
+                         (size_t)(E + 31) / 32 * 8192, st, (const bf16_t*)(b + L.dl_x),
+                         (const bf16_t*)w, (const bf16_t*)dx_add, (bf16_t*)dx, s.T, L.Tp, d, E,
+                         (int)L.EK, tb);
       if ((err = hipGetLastError()) != hipSuccess) return err;
     }
-    if (dw) {
-      const int64_t cols = bf ? kCols : kColsF32;
-      int64_t per = (s.T + L.splits - 1) / L.splits;
-      per = (per + 127) / 128 * 128;
-      const dim3 grid((unsigned)((d + cols - 1) / cols), (unsigned)L.splits,
-                      (unsigned)((E + 63) / 64));
-      const uint8_t* valid = reinterpret_cast<const uint8_t*>(b + L.valid);
-      auto run = [&](auto kb, auto kf) {
-        if (bf)
-          hipLaunchKernelGGL(kb, grid, dim3(256), 0, st, (const bf16_t*)(b + L.dl_w),
-                             (const bf16_t*)x, valid, dw_part, s.T, L.Tp, d, E, per);
-        else
-          hipLaunchKernelGGL(kf, grid, dim3(256), 0, st, (const float*)(b + L.dl_w),
-                             (const float*)x, valid, dw_part, s.T, L.Tp, d, E, per);
+    if (bf && dw) {
+      auto run = [&](auto kern) {
+        hipLaunchKernelGGL(kern, dim3((unsigned)range_grid(ct, L.splits), (unsigned)e_groups),
+                           dim3(256), 0, st, (const bf16_t*)(b + L.dl_w), (const bf16_t*)x, valid,
+                           dw_part, s.T, L.Tp, d, E, per, L.splits);
+        return hipGetLastError();
       };
-      if (E <= 16)
-        run(k_route_dw_bf16<1>, k_route_dw_f32<1>);
-      else if (E <= 32)
-        run(k_route_dw_bf16<2>, k_route_dw_f32<2>);
-      else
-        run(k_route_dw_bf16<4>, k_route_dw_f32<4>);
+      err = E <= 16 ? run(k_route_dw_bf16<1>) : E <= 32 ? run(k_route_dw_bf16<2>) : run(k_route_dw_bf16<4>);
+      if (err != hipSuccess) return err;
+    }
+    if (!bf && dx) {
+      hipLaunchKernelGGL(k_route_dx_f32, dim3((unsigned)ct, (unsigned)tb), dim3(256), 0, st,
+                         (const float*)(b + L.dl_x), (const float*)w, (const float*)dx_add,
+                         (float*)dx, s.T, d, E, (int)L.EK);
       if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    if (!bf && dw) {
+      auto run = [&](auto kern) {
+        hipLaunchKernelGGL(kern, dim3((unsigned)ct, (unsigned)L.splits, (unsigned)e_groups),
+                           dim3(256), 0, st, (const float*)(b + L.dl_w), (const float*)x, valid,
+                           dw_part, s.T, L.Tp, d, E, per);
+        return hipGetLastError();
+      };
+      err = E <= 16 ? run(k_route_dw_f32<1>) : E <= 32 ? run(k_route_dw_f32<2>) : run(k_route_dw_f32<4>);
+      if (err != hipSuccess) return err;
     }
   }
   const bool sum_dw = dw && (L.splits > 1 || s.T == 0);
-  if (!sum_dw && !db) return hipSuccess;
+  const bool sum_db = db && L.dl_blocks != 1;
+  if (!sum_dw && !sum_db) return hipSuccess;
   const int64_t n = (int64_t)E * d;
   int64_t blocks = sum_dw ? (n + 255) / 256 : 0;
   if (blocks > 4096) blocks = 4096;
-  hipLaunchKernelGGL(k_route_reduce, dim3((unsigned)(blocks + (db ? 1 : 0))), dim3(256), 0, st,
+  hipLaunchKernelGGL(k_route_reduce, dim3((unsigned)(blocks + (sum_db ? 1 : 0))), dim3(256), 0, st,
                      dw_part, s.T > 0 ? L.splits : 0, n, dw, (int)blocks, db_part,
                      s.T > 0 ? L.dl_blocks : 0, E, db);
   return hipGetLastError();
