@@ -362,8 +362,9 @@ __global__ __launch_bounds__(64 * WF * WK) void k_quant_rows(QArgs a) {
 // (gathered: 1.22 ms instead of 0.62 ms on the layer below).
 //
 // Bound: the matrix instructions and their interleaved conversions and scale products (4 fp32
-// products for every GROUP / 32 matrix instructions).  E 8, d 2048, f 8192, 4096 tokens, top-2, group
-// 128: 309 us a product, 890 TFLOP/s; group 32: 433 and 449 us.
+// products for every CG / 32 matrix instructions), then the latency of the token rows.  E 8, d 2048,
+// f 8192, 4096 tokens, top-2: group 64 and 128 296 us up and 280 us down, 929 and 981 TFLOP/s; group
+// 32 334 and 328 us.  Without the products the loads alone take about 170 us.
 template <int WF, int RT, int FT, int GROUP, int ACT>
 __global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
   constexpr bool GATED = ACT == kQGated;
@@ -470,19 +471,26 @@ hipError_t run_rows(const QArgs& a, int64_t tiles, int64_t NT, hipStream_t st) {
                       dim3((unsigned)tile_grid(tiles, NT, a.xcds)), dim3(64 * WF * WK), lds, st, a);
 }
 
-// Rows an expert on average, and blocks a variant would launch, decide (d 2048, f 8192, 8 experts unless
-// said otherwise, us up / down):
-//  - many rows: 64 x 256 tiles of 8 waves, once they are 160 blocks (64 experts of f 1408, 96 rows each:
-//    60 / 58 against 77 / 75 for the next); 64 rows each: 39 up as the next's, down only 96 blocks
-//    and the next is ahead, 47 against 54;
-//  - else 32 rows x 256 weight rows, from 160 blocks on (64 experts, 24 rows each: 29 / 31 against 33
-//    / 29 for the next);
-//  - else 32 x 128, from 256 blocks on (16 rows each, up: 19.3 against 37 for the next);
-//  - else K shared by 4 groups of waves, 64 weight rows a block: 32 token rows (16 rows each, down:
-//    22.9 against 38 for the last), or 16 where experts have at most 8 (2 rows each, down: 18.4
-//    against 19.9);
-//  - one or two tokens, with fewer blocks than that: 16 weight rows a block, K shared by 8 waves
-//    that load their own token rows (1 token, down: 7.1 against 14).
+// Rows an expert on average, and blocks a variant would launch, decide (us of both products, unless said
+// otherwise; random routing):
+//  - more than 48 rows: 64 x 256 tiles of 8 waves, once they are 160 blocks (8 experts, d 2048, f
+//    8192, 1024 rows each: 594 against 662 for 32 x 256; 64 gated experts, d 2048, f 1408, 72 rows
+//    each: 146 against 159; 38 rows each: 111 against 98);
+//  - at most 6 rows and 512 blocks: 16 token rows by 128 weight rows, waves of twice the width (64
+//    tokens, top-6, 64 gated experts of d 2048, f 1408: 57 against 63 for the next; 16 experts of
+//    4 rows, d 2048, f 4096, 44.5 against 43.2: about even at the limit);
+//  - else 32 rows x 256 weight rows, from 160 blocks on (64 experts, 24 rows each: 29 up / 31 down
+//    against 33 / 29 for the next);
+//  - else 32 x 128, from 256 blocks on (8 experts, f 8192, 16 rows each, up: 19.3 against 37);
+//  - else K is shared by groups of waves, 64 weight rows a block.  Four groups for long K: 32 token
+//    rows if the blocks, of 16 waves, are one a CU (d 2048, f 8192, 16 rows each: 41.8 against 46.0
+//    with 16 token rows; 20 rows each, where some CUs get two: 60.5 against 54.6).  Two groups
+//    for K below 4096 (8 gated experts, d 2048, f 768, 9 rows each: 12.2 against 14.6 with four), of 16
+//    token rows up to 24 rows an expert (24 rows each: 15.1 against 17.4 with 32 token rows; 64 rows
+//    each: 21.4 against 19.9);
+//  - few tokens with few such blocks: 16 weight rows a block, K shared by 8 waves that load their own
+//    token rows (1 token, f 8192: 14.8 against 23.0; 2 rows each, f 1408: 14.1 against 12.7, from 128
+//    blocks on therefore not).
 // A gated tile holds a gate and an up row per feature: half the features a block.
 template <int GROUP, int ACT>
 hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
@@ -503,16 +511,24 @@ hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
   };
   // few row tiles go over all XCDs; more are dealt to pairs of them
   a.xcds = active < 8 ? 8 : 2;
-  if (mean > 24 && NT(256) * likely(64) >= 160)
+  if (mean > 48 && NT(256) * likely(64) >= 160)
     return launch_timed(k_quant_tiles<8, 4, 2, GROUP, ACT>,
                         dim3((unsigned)tile_grid(most(64), NT(256), a.xcds)), dim3(512), 0, st, a);
+  if (mean <= 6 && NT(128) * likely(16) >= 512)
+    return run_rows<1, 2 * F1, 4, 1, GATED ? 2 : 4, true, GROUP, ACT>(a, most(16), NT(128 * F1), st);
   if (NT(256) * likely(32) >= 160)
     return run_rows<2, 2, 8, 1, 3, true, GROUP, ACT>(a, most(32), NT(256), st);
-  if (!GATED && NT(128) * likely(32) >= 256)
-    return run_rows<2, F1, 8, 1, 2, true, GROUP, ACT>(a, most(32), NT(128 * F1), st);
-  if (mean > 8) return run_rows<2, F1, 4, 4, 2, true, GROUP, ACT>(a, most(32), NT(64 * F1), st);
-  if (NT(64 * F1) * likely(16) >= 192)
-    return run_rows<1, F1, 4, 4, 2, true, GROUP, ACT>(a, most(16), NT(64 * F1), st);
+  if constexpr (!GATED)
+    if (NT(128) * likely(32) >= 256)
+      return run_rows<2, 1, 8, 1, 2, true, GROUP, ACT>(a, most(32), NT(128), st);
+  const bool long_k = a.K >= 4096;
+  if (long_k && mean > 8 && NT(64 * F1) * likely(32) <= 256)
+    return run_rows<2, F1, 4, 4, 2, true, GROUP, ACT>(a, most(32), NT(64 * F1), st);
+  if (mean > 24) return run_rows<2, F1, 4, 2, 2, true, GROUP, ACT>(a, most(32), NT(64 * F1), st);
+  if (mean > 8 || NT(64 * F1) * likely(16) >= (mean > 1 ? 128 : 192)) {
+    if (long_k) return run_rows<1, F1, 4, 4, 2, true, GROUP, ACT>(a, most(16), NT(64 * F1), st);
+    return run_rows<1, F1, 4, 2, 2, true, GROUP, ACT>(a, most(16), NT(64 * F1), st);
+  }
   return run_rows<1, F1, 1, 8, 2, false, GROUP, ACT>(a, most(16), NT(16 * F1), st);
 }
 

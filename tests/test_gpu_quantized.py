@@ -131,6 +131,28 @@ def test_expert_ffn(T, d, f, E, k, group, C, gated):
         assert np.linalg.norm(got - ref) <= 2 * Q.BF * np.linalg.norm(ref)
 
 
+# every kernel that the products choose from, by rows an expert, blocks and length, in both products
+VARIANT_SHAPES = [  # T, d, f, E, k, C
+    (200, 136, 264, 256, 3, 256.0),  # few rows, many blocks
+    (640, 264, 136, 160, 2, 160.0),  # 32 rows by 256 weight rows
+    (560, 248, 248, 140, 2, 140.0),  # 32 rows by 128
+    (40, 4104, 136, 2, 1, 2.0),      # K shared by four groups of waves: up, 32 rows
+    (40, 136, 4104, 2, 1, 2.0),      # down
+    (96, 4104, 72, 64, 2, 64.0),     # up, 16 rows
+    (96, 72, 4104, 64, 2, 64.0),     # down
+    (2600, 264, 520, 32, 4, 32.0),   # 64 by 256 tiles
+    (1000, 136, 72, 12, 2, 1.5),     # shared by two groups, 32 rows
+    (200, 200, 136, 24, 2, 24.0),    # 16 rows
+]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,d,f,E,k,C", VARIANT_SHAPES)
+def test_expert_ffn_variants(T, d, f, E, k, group, C, gated):
+    test_expert_ffn(T, d, f, E, k, group, C, gated)
+
+
 def test_expert_ffn_skewed_rows():
     """All tokens on one expert, then one token each on the rest: more rows than a tile in the
     kernels for few rows, and a slot count far from the mean."""
