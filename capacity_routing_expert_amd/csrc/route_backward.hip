@@ -52,12 +52,13 @@ BackwardLayout backward_layout(const moe_shape& s) {
   L.EK = bf ? (E + 7) / 8 * 8 : (E + 3) / 4 * 4;
   const int64_t tiles = L.Tp / kTT;
   L.dl_blocks = tiles < kMaxDlBlocks ? tiles : kMaxDlBlocks;
-  // blocks of dW_r: column tiles x groups of 64 experts x token ranges; about one a compute
-  // unit, and at least 128 tokens a range (T 16384, E 64, d 2048: 25 us, with twice the blocks 33,
-  // as each writes a partial dW_r of its own)
+  // blocks of dW_r: column tiles x groups of 64 experts x token ranges, and at least 128 tokens a
+  // range.  bf16: about one a compute unit (T 16384, E 64, d 2048: 25 us, with twice the blocks 33,
+  // as each writes a partial dW_r of its own); f32, whose waves have half the bytes on their
+  // way: three (the whole pass at T 8192, E 128, d 4096: 285 us, with two 343, with one 507)
   const int64_t cols = bf ? kCols : kColsF32;
   const int64_t base = (d + cols - 1) / cols * ((E + 63) / 64);
-  int64_t splits = (256 + base - 1) / base;
+  int64_t splits = ((bf ? 256 : 768) + base - 1) / base;
   const int64_t most = (s.T + 127) / 128;
   if (splits > most) splits = most;
   L.splits = splits < 1 ? 1 : splits;
@@ -504,77 +505,159 @@ __global__ __launch_bounds__(256) void k_route_dw_bf16(const bf16_t* __restrict_
 }
 
 // ---------------------------------------------------------------- fp32
-// dx: a wave takes 16 tokens x 64 columns (4 tiles), experts in steps of 4.
-__global__ __launch_bounds__(256) void k_route_dx_f32(const float* __restrict__ dl,
-                                                      const float* __restrict__ w,
-                                                      const float* add, float* dx, int64_t T,
-                                                      int d, int E, int EK) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n = lane & 15, kg = lane >> 4;
-  const int c0 = blockIdx.x * kColsF32;
-  const int64_t step = (int64_t)gridDim.y * 64;
-  for (int64_t t0 = (int64_t)blockIdx.y * 64 + wave * 16; t0 < T; t0 += step) {
-    f32x4_t acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int e0 = 0; e0 < EK; e0 += 4) {
-      const int e = e0 + kg;
-      const float A = dl[(t0 + n) * EK + e];  // rows up to Tp and experts up to EK are there
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + i * 16 + n;
-        const float B = e < E && c < d ? w[(int64_t)e * d + c] : 0.0f;
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(A, B, acc[i], 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + kg * 4 + j;
-        const int c = c0 + i * 16 + n;
-        if (t < T && c < d) dx[t * d + c] = acc[i][j] + (add ? add[t * d + c] : 0.0f);
-      }
+// The sum of a matrix instruction does not mind the order of its terms, so lane group kg takes experts
+// (dx) or tokens (dW_r) 4 kg .. 4 kg + 3 of 16, one 16-byte load, and tile i of four holds columns
+// 4 n + i: rows of x, W_r and dx move in 16-byte pieces, 256 B a row.  VEC: d is a multiple of 4.
+// T 1970, d 4024, E 11, with dx_add: dx 13.5 us (95 MB), dW_r 12.8 us (32 MB); with a dword a lane
+// and loads behind branches 57 us for the whole pass instead of 32.
+template <bool VEC>
+__device__ __forceinline__ float4 load_cols(const float* row, int c, int d) {
+  if constexpr (VEC) return c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0, 0, 0, 0);
+  return make_float4(c < d ? row[c] : 0.0f, c + 1 < d ? row[c + 1] : 0.0f,
+                     c + 2 < d ? row[c + 2] : 0.0f, c + 3 < d ? row[c + 3] : 0.0f);
+}
+template <bool VEC>
+__device__ __forceinline__ void store_cols(float* row, int c, int d, float4 v) {
+  if constexpr (VEC) {
+    if (c < d) *reinterpret_cast<float4*>(row + c) = v;
+  } else {
+    if (c < d) row[c] = v.x;
+    if (c + 1 < d) row[c + 1] = v.y;
+    if (c + 2 < d) row[c + 2] = v.z;
+    if (c + 3 < d) row[c + 3] = v.w;
   }
 }
 
-// dW_r: a wave takes 64 experts x 64 columns at most, tokens in steps of 4.
-template <int MT>
+// dx: a wave takes 16 tokens x 64 columns at a time; the block's columns of W_r stay in LDS.
+template <bool VEC>
+__global__ __launch_bounds__(256) void k_route_dx_f32(const float* __restrict__ dl,
+                                                      const float* __restrict__ w,
+                                                      const float* add, float* dx, int64_t T,
+                                                      int d, int E, int EK, int64_t ranges) {
+  extern __shared__ float4 wl[];  // [experts, up to whole 16][16]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = lane & 15, kg = lane >> 4;
+  int col;
+  int64_t range;
+  if (!range_of((d + kColsF32 - 1) / kColsF32, ranges, col, range)) return;  // block-uniform
+  const int c = col * kColsF32 + n * 4, EG = (E + 15) / 16;
+  for (int i = threadIdx.x; i < EG * 256; i += 256)  // i % 16 is this thread's n
+    wl[i] = i / 16 < E ? load_cols<VEC>(w + (int64_t)(i / 16) * d, c, d) : make_float4(0, 0, 0, 0);
+  __syncthreads();
+  for (int64_t t0 = range * 64 + wave * 16; t0 < T; t0 += ranges * 64) {
+    const float* row = dl + (t0 + n) * EK;  // rows up to Tp and experts up to EK are there
+    float4 in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = t0 + kg * 4 + j;
+      in[j] = add && t < T ? load_cols<VEC>(add + t * d, c, d) : make_float4(0, 0, 0, 0);
+    }
+    f32x4_t acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < EG; ++g) {
+      const int e = g * 16 + kg * 4;
+      const float4 a = e < EK ? *reinterpret_cast<const float4*>(row + e) : make_float4(0, 0, 0, 0);
+      const float A[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float4 b = wl[(e + s) * 16 + n];
+        acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[s], b.x, acc[0], 0, 0, 0);
+        acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[s], b.y, acc[1], 0, 0, 0);
+        acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[s], b.z, acc[2], 0, 0, 0);
+        acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[s], b.w, acc[3], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = t0 + kg * 4 + j;
+      if (t < T)
+        store_cols<VEC>(dx + t * d, c, d,
+                        make_float4(acc[0][j] + in[j].x, acc[1][j] + in[j].y, acc[2][j] + in[j].z,
+                                    acc[3][j] + in[j].w));
+    }
+  }
+}
+
+// dW_r: a wave takes 64 experts x 64 columns at most and 16 tokens at a time, the next 16 on their
+// way; no load stands behind a branch, as the waits at its end would be for every load before it.
+template <int MT, bool VEC>
 __global__ __launch_bounds__(256) void k_route_dw_f32(const float* __restrict__ dl,
                                                       const float* __restrict__ x,
                                                       const uint8_t* __restrict__ valid,
                                                       float* __restrict__ out, int64_t T,
-                                                      int64_t Tp, int d, int E, int64_t per) {
+                                                      int64_t Tp, int d, int E, int64_t per,
+                                                      int64_t ranges) {
   __shared__ float4 red[2][MT * 4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, kg = lane >> 4;
-  const int c0 = blockIdx.x * kColsF32, e0 = blockIdx.z * 64;
+  int col;
+  int64_t range;
+  if (!range_of((d + kColsF32 - 1) / kColsF32, ranges, col, range)) return;  // block-uniform
+  const int c = col * kColsF32 + n * 4, e0 = blockIdx.y * 64;
   f32x4_t acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[m][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t ts = blockIdx.y * per, te = ts + per < T ? ts + per : T;
-  for (int64_t t0 = ts + wave * 32; t0 < te; t0 += 128) {
+  const int64_t ts = range * per, te = ts + per < T ? ts + per : T;
+  const float* dp[MT];  // rows of experts past E repeat the last one's; they are not stored
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int64_t t = t0 + q * 4 + kg;
-      const bool ok = t < T && (!valid || valid[t]);
-      float A[MT], B[4];
+  for (int m = 0; m < MT; ++m) dp[m] = dl + (int64_t)min(e0 + m * 16 + n, E - 1) * Tp + kg * 4;
+  float4 r[4], A[MT];
+  // a masked token's row is not read (whatever it holds counts as zeros)
+  auto mask_of = [&](int64_t t0) -> uint32_t {
+    return valid ? *reinterpret_cast<const uint32_t*>(valid + min(t0, Tp - 16) + kg * 4) : 0x01010101u;
+  };
+  auto load = [&](int64_t t0, uint32_t ok) {
+    const int rows = t0 < te ? (int)min(te - t0, (int64_t)16) : 0;
+    const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(x + (rows ? t0 : 0) * d, (uint32_t)rows * d * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + i * 16 + n;
-        B[i] = ok && c < d ? x[t * d + c] : 0.0f;
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int e = e0 + m * 16 + n;
-        A[m] = e < E ? dl[(int64_t)e * Tp + t] : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      const bool in = kg * 4 + j < rows && (ok >> (8 * j) & 1);
+      const uint32_t at = (uint32_t)((kg * 4 + j) * d + c) * 4;
+      if constexpr (VEC) {
+        const uint4 v = buffer_load16(xr, in && c < d ? at : 0x80000000u);
+        r[j] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                           __uint_as_float(v.w));
+      } else {
+        float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(A[m], B[i], acc[m][i], 0, 0, 0);
+          v[i] = buffer_load_f32(xr, in && c + i < d ? at + i * 4 : 0x80000000u);
+        r[j] = make_float4(v[0], v[1], v[2], v[3]);
       }
     }
+    const int64_t td = min(t0, Tp - 16);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) A[m] = *reinterpret_cast<const float4*>(dp[m] + td);
+  };
+  int64_t t0 = ts + wave * 16;
+  uint32_t ok = mask_of(t0);
+  load(t0, ok);
+  ok = mask_of(t0 + 64);
+  for (; t0 < te; t0 += 64) {
+    float4 B[4], C[MT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) B[j] = r[j];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) C[m] = A[m];
+    const uint32_t now = ok;
+    ok = mask_of(t0 + 128);
+    __builtin_amdgcn_sched_barrier(0);
+    load(t0 + 64, now);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float a = j == 0 ? C[m].x : j == 1 ? C[m].y : j == 2 ? C[m].z : C[m].w;
+        acc[m][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, B[j].x, acc[m][0], 0, 0, 0);
+        acc[m][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, B[j].y, acc[m][1], 0, 0, 0);
+        acc[m][2] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, B[j].z, acc[m][2], 0, 0, 0);
+        acc[m][3] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, B[j].w, acc[m][3], 0, 0, 0);
+      }
   }
   for (int half = 2; half >= 1; half >>= 1) {
     if (wave >= half && wave < 2 * half) {
@@ -601,18 +684,15 @@ __global__ __launch_bounds__(256) void k_route_dw_f32(const float* __restrict__ 
     __syncthreads();
   }
   if (wave) return;
-  float* o = out + (int64_t)blockIdx.y * E * d;
+  float* o = out + range * E * d;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int e = e0 + m * 16 + kg * 4 + j;
-      if (e >= E) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + i * 16 + n;
-        if (c < d) o[(int64_t)e * d + c] = acc[m][i][j];
-      }
+      if (e < E)
+        store_cols<VEC>(o + (int64_t)e * d, c, d,
+                        make_float4(acc[m][0][j], acc[m][1][j], acc[m][2][j], acc[m][3][j]));
     }
 }
 
@@ -725,20 +805,28 @@ hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* 
       err = E <= 16 ? run(k_route_dw_bf16<1>) : E <= 32 ? run(k_route_dw_bf16<2>) : run(k_route_dw_bf16<4>);
       if (err != hipSuccess) return err;
     }
-    if (!bf && dx) {
-      hipLaunchKernelGGL(k_route_dx_f32, dim3((unsigned)ct, (unsigned)tb), dim3(256), 0, st,
-                         (const float*)(b + L.dl_x), (const float*)w, (const float*)dx_add,
-                         (float*)dx, s.T, d, E, (int)L.EK);
-      if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
-    if (!bf && dw) {
-      auto run = [&](auto kern) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)ct, (unsigned)L.splits, (unsigned)e_groups),
-                           dim3(256), 0, st, (const float*)(b + L.dl_w), (const float*)x, valid,
-                           dw_part, s.T, L.Tp, d, E, per);
-        return hipGetLastError();
+    if (!bf) {
+      auto run = [&](auto vec) {
+        constexpr bool VEC = decltype(vec)::value;
+        if (dx) {
+          hipLaunchKernelGGL(k_route_dx_f32<VEC>, dim3((unsigned)range_grid(ct, tb)), dim3(256),
+                             (size_t)(E + 15) / 16 * 4096, st, (const float*)(b + L.dl_x),
+                             (const float*)w, (const float*)dx_add, (float*)dx, s.T, d, E,
+                             (int)L.EK, tb);
+          if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        }
+        if (!dw) return hipSuccess;
+        auto dw_run = [&](auto kern) {
+          hipLaunchKernelGGL(kern, dim3((unsigned)range_grid(ct, L.splits), (unsigned)e_groups),
+                             dim3(256), 0, st, (const float*)(b + L.dl_w), (const float*)x, valid,
+                             dw_part, s.T, L.Tp, d, E, per, L.splits);
+          return hipGetLastError();
+        };
+        return E <= 16   ? dw_run(k_route_dw_f32<1, VEC>)
+               : E <= 32 ? dw_run(k_route_dw_f32<2, VEC>)
+                         : dw_run(k_route_dw_f32<4, VEC>);
       };
-      err = E <= 16 ? run(k_route_dw_f32<1>) : E <= 32 ? run(k_route_dw_f32<2>) : run(k_route_dw_f32<4>);
+      err = d % 4 == 0 ? run(std::true_type()) : run(std::false_type());
       if (err != hipSuccess) return err;
     }
   }
