@@ -665,6 +665,8 @@ class QuantizedExperts:
         if gated and (b1 is not None or b2 is not None):
             raise ValueError("gated experts have no biases")
         self.tensors = (w1_codes, w1_scales, b1, w2_codes, w2_scales, b2)
+        if len({t.device for t in self.tensors if t is not None}) > 1:
+            raise ValueError("the experts' tensors are on different devices")
         self.struct = MoeQuantizedExperts(
             _ptr(w1_codes, "w1_codes", u8, numel=sizes["w1"]),
             _ptr(w1_scales, "w1_scales", bf, numel=scales["w1"]),

@@ -235,6 +235,9 @@ moe_status do_dispatch(const moe_shape& s, const int32_t* ids, const float* gate
   return err == hipSuccess ? MOE_OK : device_error(err, "dispatch");
 }
 
+// codes and scales of an expert are addressed with 32-bit byte offsets
+constexpr int64_t kMaxQuantizedBytes = (int64_t)1 << 31;
+
 // 4-bit experts: the shape's limits and every pointer of the struct.
 moe_status check_quantized(const moe_shape& s, const moe_quantized_experts& q) {
   if (s.dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "4-bit experts are bf16 only");
@@ -245,10 +248,8 @@ moe_status check_quantized(const moe_shape& s, const moe_quantized_experts& q) {
     return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", q.group);
   if (q.gated != 0 && q.gated != 1)
     return fail(MOE_ERR_INVALID_ARGUMENT, "gated = %d is not 0 or 1", q.gated);
-  // codes and scales of an expert are addressed with 32-bit byte offsets
-  const int64_t lim = (int64_t)1 << 31;
-  if (quantized_codes_bytes(1, s.d_ff, s.d_model) * (q.gated ? 2 : 1) >= lim ||
-      quantized_codes_bytes(1, s.d_model, s.d_ff) >= lim)
+  if (quantized_codes_bytes(1, s.d_ff, s.d_model) * (q.gated ? 2 : 1) >= kMaxQuantizedBytes ||
+      quantized_codes_bytes(1, s.d_model, s.d_ff) >= kMaxQuantizedBytes)
     return fail(MOE_ERR_UNSUPPORTED, "4-bit expert of %d x %d: 2 GiB or more per expert", s.d_ff,
                 s.d_model);
   MOE_TRY(check_data_ptr(s, q.w1_codes, "w1_codes"));
@@ -273,6 +274,8 @@ moe_status check_quantize(const moe_shape* shape, int32_t rows, int32_t cols, in
     return fail(MOE_ERR_UNSUPPORTED, "rows = %d, cols = %d must be multiples of 8", rows, cols);
   if (group != 32 && group != 64 && group != 128)
     return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", group);
+  if (quantized_codes_bytes(1, rows, cols) >= kMaxQuantizedBytes)
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit matrix of %d x %d: 2 GiB or more per expert", rows, cols);
   return MOE_OK;
 }
 
@@ -1247,7 +1250,12 @@ moe_status moe_layer_forward_quantized(const moe_shape* shape, const void* x, co
                                        uint8_t* drop_mask, int32_t* expert_counts, void* ws,
                                        size_t ws_bytes, moe_stream_t stream,
                                        moe_event_t const* events) {
-  if (!experts) return fail(MOE_ERR_INVALID_ARGUMENT, "experts is NULL");
+  if (!experts) {
+    hipEvent_t armed[4];  // consumed by this call even if it fails
+    take_timing(armed);
+    take_stage_timing(armed);
+    return fail(MOE_ERR_INVALID_ARGUMENT, "experts is NULL");
+  }
   if (events)
     for (int i = 0; i < 6; ++i)
       if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);

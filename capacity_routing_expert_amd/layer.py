@@ -370,6 +370,9 @@ def quantize_experts(w1: torch.Tensor, b1: torch.Tensor | None, w2: torch.Tensor
     """The experts of a layer at 4 bits: w1 [E, d_ff, d_model] (gated: W13 [E, 2 d_ff, d_model], no
     biases) and w2 [E, d_model, d_ff], bf16 or fp32; biases bf16.  A one-time preparation."""
     E, d, f = w2.shape
+    if tuple(w1.shape) != (E, 2 * f if gated else f, d):
+        raise ValueError(f"w1 is {tuple(w1.shape)}, w2 {tuple(w2.shape)}: w1 has to be "
+                         f"{(E, 2 * f if gated else f, d)}")
     return B.QuantizedExperts(E, d, f, group, gated, *quantize_weights(w1, group),
                               None if gated else b1, *quantize_weights(w2, group),
                               None if gated else b2)

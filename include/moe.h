@@ -225,8 +225,8 @@ moe_status moe_layer_forward_profiled(const moe_shape* shape, const void* x,
 /* Kernel timing of the two expert GEMMs (the layer's expert-FFN stage, Worked Example: the
  * expert computations whose slowest expert sets the wall-clock time), with nothing inserted
  * between launches.  Arms the NEXT call on this thread of moe_layer_forward (or its _profiled,
- * _padded or _gated form), moe_layer_forward_dropless(_gated), moe_expert_ffn or
- * moe_expert_ffn_pairs:
+ * _padded, _gated or _quantized form), moe_layer_forward_dropless(_gated), moe_expert_ffn(_quantized)
+ * or moe_expert_ffn_pairs:
  *   events[0], [1]  start and end of the up-projection's kernel
  *   events[2], [3]  start and end of the down-projection's kernel
  * recorded by the kernel launches themselves (hipExtLaunchKernel).  The events are the
@@ -241,7 +241,7 @@ moe_status moe_set_gemm_timing(const moe_event_t* events);
  * softmax and top-k: "Dynamic Token Routing AI", "How it works") and of step 4 (the
  * gate-weighted combine and residual: Worked Example, trace of token 0), without the launch
  * gaps that events recorded between stages include.  Arms the NEXT call on this thread of
- * moe_layer_forward (or its _profiled, _padded, _gated or _noalloc form):
+ * moe_layer_forward (or its _profiled, _padded, _gated, _quantized or _noalloc form):
  *   events[0], [1]  start and end of the router's kernel
  *   events[2], [3]  start and end of the combine's kernel
  * recorded by those launches themselves (hipExtLaunchKernel).  The events are the caller's
@@ -428,8 +428,8 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
  *          highest; columns past cols are zero
  *   scales [E][KC][rows][128 / group] bf16, zero past cols */
 
-/* Bytes of the two arrays; 0 for an invalid shape, rows or cols not multiples of 8, or a group
- * that is not 32, 64 or 128. */
+/* Bytes of the two arrays; 0 for an invalid shape, rows or cols not multiples of 8, a group that
+ * is not 32, 64 or 128, or codes of 2 GiB or more per expert (MOE_ERR_UNSUPPORTED below). */
 size_t moe_quantized_codes_bytes(const moe_shape* shape, int32_t rows, int32_t cols);
 size_t moe_quantized_scales_bytes(const moe_shape* shape, int32_t rows, int32_t cols,
                                   int32_t group);

@@ -156,3 +156,46 @@ def test_binding_checks(lib):
         B.QuantizedExperts(8, 60, 96, 32, False, **args)
     with pytest.raises(ValueError, match="experts"):
         B.moe_quantize_weights(shape(), torch.zeros(3, 8, 8, dtype=bf), 32, None, None)
+
+
+def test_matrices_of_2_gib_are_refused(lib):
+    """Also where E x rows x cols would leave 64 bits."""
+    s = shape(n_experts=256)
+    assert B.quantized_codes_bytes(s, 1 << 16, (1 << 16) - 128) == 256 * (2 ** 31 - 2 ** 22)
+    for rows, cols in ((1 << 16, 1 << 16), (1 << 30, 1 << 30), (8, (1 << 31) - 8), ((1 << 31) - 8, 8)):
+        big = -(-cols // 128) * 64 * rows >= 1 << 31
+        assert big == (B.quantized_codes_bytes(s, rows, cols) == 0)
+        assert big == (B.quantized_scales_bytes(s, rows, cols, 32) == 0)
+        if big:
+            assert lib.moe_quantize_weights(ctypes.byref(s), at(0), rows, cols, 32, at(1), at(2),
+                                            None) == 2
+            assert "2 GiB" in B.last_error()
+
+
+def test_experts_have_to_fit_together(lib):
+    from capacity_routing_expert_amd import layer as L
+    w = lambda *n: torch.zeros(n, dtype=torch.bfloat16)
+    for w1, w2, gated in ((w(2, 64, 96), w(2, 64, 96), False),   # W1 as [E, d, f]
+                          (w(2, 96, 64), w(2, 64, 96), True),    # W1 for a W13
+                          (w(2, 192, 64), w(2, 64, 96), False), (w(3, 96, 64), w(2, 64, 96), False)):
+        with pytest.raises(ValueError, match="w1 has to be"):
+            L.quantize_experts(w1, None, w2, None, 32, gated)
+    with pytest.raises(ValueError, match="different devices"):
+        B.QuantizedExperts(1, 8, 8, 32, True, torch.zeros(512, dtype=torch.uint8, device="meta"),
+                           w(32), None, torch.zeros(512, dtype=torch.uint8), w(32), None)
+
+
+def test_a_refused_call_consumes_the_timing_arm(lib):
+    """A second set of handles may then be armed and disarmed; the refused call left nothing that
+    a later call would record into."""
+    events = (ctypes.c_void_p * 4)(1, 2, 3, 4)
+    s = shape(T=0)
+    assert lib.moe_set_gemm_timing(events) == 0
+    assert lib.moe_set_stage_timing(events) == 0
+    none = [None] * 7
+    assert lib.moe_layer_forward_quantized(ctypes.byref(s), None, None, None, None, *none, 0, None,
+                                           None) == 1
+    ok = B.MoeQuantizedExperts()
+    # an empty batch records what is armed: nothing is
+    assert lib.moe_layer_forward_quantized(ctypes.byref(s), None, None, None, ctypes.byref(ok), *none,
+                                           0, None, None) == 0
