@@ -332,10 +332,7 @@ def moe_layer_forward_noalloc(shape, x, w_router, b_router, w1, b1, w2, b2, out,
     args = _forward_args(shape, x, w_router, b_router, w1, b1, w2, b2, out, topk_ids, topk_gates,
                          slot_of, drop_mask, expert_counts, None)
     _check(lib().moe_layer_forward_noalloc(*args[:-2], _stream(stream)),
-           "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
-           "moe_workspace_bytes_route_backward", "moe_route_backward", "moe_quantized_codes_bytes",
-           "moe_quantized_scales_bytes", "moe_quantize_weights", "moe_dequantize_weights",
-           "moe_expert_ffn_quantized", "moe_layer_forward_quantized")
+           "moe_layer_forward_noalloc")
 
 
 def moe_layer_forward_profiled(shape, x, w_router, b_router, w1, b1, w2, b2, out, events,
