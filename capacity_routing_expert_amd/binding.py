@@ -225,7 +225,14 @@ def _w(shape: MoeShape, rows: int, cols: int) -> int:
     return E * rows * cols  # row-major (other layouts and dtypes are refused by the library)
 
 
+# the handle alone: torch.cuda.current_stream() makes an object around it, 3 us of the 10 us that a
+# small call takes on the host
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -548,18 +555,25 @@ def moe_pack_weights(shape, w, w_packed, stream=None):
            "moe_pack_weights")
 
 
-def _cur(t, name: str, dtype=None, numel: int = 0):
-    """_ptr, and the tensor has to be on the current device (the one whose stream the call takes).
-    Everything is looked at once; only a tensor that something is wrong with takes the long way."""
+def _device() -> int:
+    """The current device (-1 without one): looked up once a call."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -1
+
+
+def _cur(dev: int, t, name: str, dtype=None, numel: int = 0):
+    """_ptr, and the tensor has to be on device `dev`, the current one (whose stream the call
+    takes).  Everything is looked at once; only a tensor that something is wrong with takes the
+    long way."""
     if t is None:
         return None
     if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and
-            t.numel() >= numel and t.is_cuda and t.is_contiguous() and
-            t.get_device() == torch.cuda.current_device()):
+            t.numel() >= numel and t.is_cuda and t.is_contiguous() and t.get_device() == dev):
         return t.data_ptr()
     _ptr(t, name, dtype, numel=numel)
-    raise ValueError(f"{name} is on {t.device}, the current device is "
-                     f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def workspace_bytes_balance(shape: MoeShape) -> int:
@@ -576,14 +590,15 @@ def moe_balance_loss(shape, logits, topk_ids, loss, expert_counts=None, expert_p
     """Balance loss [1] and, where given, the counts [E], mean probabilities [E] and gradient on
     the logits [T, E]; token_mask [T] uint8, 0 for padding."""
     T, E, k = shape.T, shape.n_experts, shape.top_k
+    dev = _device()
     _check(lib().moe_balance_loss(
-        ctypes.byref(shape), _cur(logits, "logits", torch.float32, numel=T * E),
-        _cur(topk_ids, "topk_ids", torch.int32, numel=T * k),
-        _cur(token_mask, "token_mask", torch.uint8, numel=T), float(coef), float(grad_scale),
-        _cur(loss, "loss", torch.float32, numel=1),
-        _cur(expert_counts, "expert_counts", torch.int32, numel=E),
-        _cur(expert_probs, "expert_probs", torch.float32, numel=E),
-        _cur(dlogits, "dlogits", torch.float32, numel=T * E), _cur(ws, "ws", torch.uint8),
+        ctypes.byref(shape), _cur(dev, logits, "logits", torch.float32, numel=T * E),
+        _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(dev, token_mask, "token_mask", torch.uint8, numel=T), float(coef), float(grad_scale),
+        _cur(dev, loss, "loss", torch.float32, numel=1),
+        _cur(dev, expert_counts, "expert_counts", torch.int32, numel=E),
+        _cur(dev, expert_probs, "expert_probs", torch.float32, numel=E),
+        _cur(dev, dlogits, "dlogits", torch.float32, numel=T * E), _cur(dev, ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream)), "moe_balance_loss")
 
 
@@ -594,15 +609,16 @@ def moe_route_backward(shape, x, w_router, logits, topk_ids, dgates, dlogits, dx
     in fp32, each optional; dgates [T, k] or dlogits [T, E] (or both) come in."""
     dt, f32 = _dtype_of(shape), torch.float32
     T, d, E, k = shape.T, shape.d_model, shape.n_experts, shape.top_k
+    dev = _device()
     _check(lib().moe_route_backward(
-        ctypes.byref(shape), _cur(x, "x", dt, numel=T * d),
-        _cur(w_router, "w_router", dt, numel=E * d), _cur(logits, "logits", f32, numel=T * E),
-        _cur(topk_ids, "topk_ids", torch.int32, numel=T * k),
-        _cur(dgates, "dgates", f32, numel=T * k), _cur(dlogits, "dlogits", f32, numel=T * E),
-        _cur(token_mask, "token_mask", torch.uint8, numel=T),
-        _cur(dx_add, "dx_add", dt, numel=T * d), _cur(dx, "dx", dt, numel=T * d),
-        _cur(dw_router, "dw_router", f32, numel=E * d),
-        _cur(db_router, "db_router", f32, numel=E), _cur(ws, "ws", torch.uint8),
+        ctypes.byref(shape), _cur(dev, x, "x", dt, numel=T * d),
+        _cur(dev, w_router, "w_router", dt, numel=E * d), _cur(dev, logits, "logits", f32, numel=T * E),
+        _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(dev, dgates, "dgates", f32, numel=T * k), _cur(dev, dlogits, "dlogits", f32, numel=T * E),
+        _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
+        _cur(dev, dx_add, "dx_add", dt, numel=T * d), _cur(dev, dx, "dx", dt, numel=T * d),
+        _cur(dev, dw_router, "dw_router", f32, numel=E * d),
+        _cur(dev, db_router, "db_router", f32, numel=E), _cur(dev, ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_backward")
 
 
@@ -620,10 +636,11 @@ def moe_quantize_weights(shape, w, group, codes, scales, stream=None):
     E, rows, cols = w.shape
     if E != shape.n_experts:
         raise ValueError(f"w has {E} experts, the shape {shape.n_experts}")
+    dev = _device()
     _check(lib().moe_quantize_weights(
-        ctypes.byref(shape), _cur(w, "w", _dtype_of(shape)), int(rows), int(cols), int(group),
-        _cur(codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
-        _cur(scales, "scales", torch.bfloat16,
+        ctypes.byref(shape), _cur(dev, w, "w", _dtype_of(shape)), int(rows), int(cols), int(group),
+        _cur(dev, codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
+        _cur(dev, scales, "scales", torch.bfloat16,
              numel=quantized_scales_bytes(shape, rows, cols, group) // 2), _stream(stream)),
         "moe_quantize_weights")
 
@@ -633,12 +650,13 @@ def moe_dequantize_weights(shape, codes, scales, group, w, stream=None):
     E, rows, cols = w.shape
     if E != shape.n_experts:
         raise ValueError(f"w has {E} experts, the shape {shape.n_experts}")
+    dev = _device()
     _check(lib().moe_dequantize_weights(
         ctypes.byref(shape),
-        _cur(codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
-        _cur(scales, "scales", torch.bfloat16,
+        _cur(dev, codes, "codes", torch.uint8, numel=quantized_codes_bytes(shape, rows, cols)),
+        _cur(dev, scales, "scales", torch.bfloat16,
              numel=quantized_scales_bytes(shape, rows, cols, group) // 2),
-        int(rows), int(cols), int(group), _cur(w, "w", torch.float32), _stream(stream)),
+        int(rows), int(cols), int(group), _cur(dev, w, "w", torch.float32), _stream(stream)),
         "moe_dequantize_weights")
 
 
@@ -677,9 +695,9 @@ class QuantizedExperts:
         if (shape.n_experts, shape.d_model, shape.d_ff) != (self.E, self.d_model, self.d_ff):
             raise ValueError(f"experts of E {self.E}, d_model {self.d_model}, d_ff {self.d_ff}; the "
                              f"shape has {shape.n_experts}, {shape.d_model}, {shape.d_ff}")
-        if self.tensors[0].get_device() != torch.cuda.current_device():
+        if self.tensors[0].get_device() != _device():
             raise ValueError(f"experts are on {self.tensors[0].device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+                             f"cuda:{_device()}")
         return ctypes.byref(self.struct)
 
 
@@ -688,12 +706,13 @@ def moe_expert_ffn_quantized(shape, x, row_token, expert_offsets, experts, y_row
     """moe_expert_ffn with QuantizedExperts."""
     dt, T, d = _dtype_of(shape), shape.T, shape.d_model
     rows = min(T * shape.top_k, shape.n_experts * shape.capacity)  # moe_max_kept_rows
+    dev = _device()
     _check(lib().moe_expert_ffn_quantized(
-        ctypes.byref(shape), _cur(x, "x", dt, T * d),
-        _cur(row_token, "row_token", torch.int32, rows) if row_token.numel() else None,
-        _cur(expert_offsets, "expert_offsets", torch.int32, shape.n_experts + 1),
-        experts.of(shape), _cur(y_rows, "y_rows", dt, rows * d) if y_rows.numel() else None,
-        _cur(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "moe_expert_ffn_quantized")
+        ctypes.byref(shape), _cur(dev, x, "x", dt, T * d),
+        _cur(dev, row_token, "row_token", torch.int32, rows) if row_token.numel() else None,
+        _cur(dev, expert_offsets, "expert_offsets", torch.int32, shape.n_experts + 1),
+        experts.of(shape), _cur(dev, y_rows, "y_rows", dt, rows * d) if y_rows.numel() else None,
+        _cur(dev, ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "moe_expert_ffn_quantized")
 
 
 def moe_layer_forward_quantized(shape, x, w_router, b_router, experts, out, topk_ids=None,
@@ -703,14 +722,15 @@ def moe_layer_forward_quantized(shape, x, w_router, b_router, experts, out, topk
     torch.cuda.Event(enable_timing=True)."""
     dt, n = _dtype_of(shape), _n(shape)
     i32 = torch.int32
+    dev = _device()
     _check(lib().moe_layer_forward_quantized(
-        ctypes.byref(shape), _cur(x, "x", dt, numel=n["x"]),
-        _cur(w_router, "w_router", dt, numel=n["wr"]),
-        _cur(b_router, "b_router", torch.float32, numel=n["E"]), experts.of(shape),
-        _cur(out, "out", dt, numel=n["x"]), _cur(topk_ids, "topk_ids", i32, numel=n["Tk"]),
-        _cur(topk_gates, "topk_gates", torch.float32, numel=n["Tk"]),
-        _cur(slot_of, "slot_of", i32, numel=n["Tk"]),
-        _cur(drop_mask, "drop_mask", torch.uint8, numel=n["Tk"]),
-        _cur(expert_counts, "expert_counts", i32, numel=n["E"]), _cur(ws, "ws", torch.uint8),
+        ctypes.byref(shape), _cur(dev, x, "x", dt, numel=n["x"]),
+        _cur(dev, w_router, "w_router", dt, numel=n["wr"]),
+        _cur(dev, b_router, "b_router", torch.float32, numel=n["E"]), experts.of(shape),
+        _cur(dev, out, "out", dt, numel=n["x"]), _cur(dev, topk_ids, "topk_ids", i32, numel=n["Tk"]),
+        _cur(dev, topk_gates, "topk_gates", torch.float32, numel=n["Tk"]),
+        _cur(dev, slot_of, "slot_of", i32, numel=n["Tk"]),
+        _cur(dev, drop_mask, "drop_mask", torch.uint8, numel=n["Tk"]),
+        _cur(dev, expert_counts, "expert_counts", i32, numel=n["E"]), _cur(dev, ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream), _events(events)),
         "moe_layer_forward_quantized")
