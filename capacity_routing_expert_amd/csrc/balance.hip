@@ -15,8 +15,9 @@
 // column sums of its blocks, k_balance_finish adds those in block order.  A last block that did the
 // last step behind an agent-scope fence instead took 72 us at T 16384, E 64: every block's fence wrote
 // the L2's whole share of the gradient back.  Few elements take one launch of one block, which counts
-// and finishes for itself.  Column sums are fp32 inside a block (at most some hundred tokens a
-// lane) and fp64 across blocks; the loss is evaluated in fp64.
+// and finishes for itself.  Column sums are fp32 inside a block (256 blocks share the tokens: 256
+// experts' 8 million tokens are 512 additions a lane) and fp64 across blocks; the loss is evaluated
+// in fp64.  T 16384, E 64, top-6: 3.2 + 8.1 + 3.6 us; T 32771, E 256, top-8 (67 MB): 4.8 + 20.4 + 7.1.
 #include "router_rows.h"
 
 namespace moe {
@@ -26,7 +27,8 @@ namespace {
 constexpr int kCountCopies = 8;
 constexpr int kThreads = 1024;
 constexpr int kMaxCountBlocks = 64, kMaxBlocks = 256;
-// Up to this many logits one block does everything.
+// Up to this many logits one block does everything (one block / three launches, us: E 8, T 2048 11.2 /
+// 12.2, T 4096 15.7 / 12.6; E 64, T 256 11.6 / 12.4, T 512 15.9 / 12.6).
 constexpr int64_t kOneBlockElems = 16384;
 
 // Histogram of the ids of valid tokens t0 .. t1 - 1 into hist[copy * (E + 1) + e] and their number

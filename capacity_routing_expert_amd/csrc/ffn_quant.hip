@@ -363,8 +363,8 @@ __global__ __launch_bounds__(64 * WF * WK) void k_quant_rows(QArgs a) {
 //
 // Bound: the matrix instructions and their interleaved conversions and scale products (4 fp32
 // products for every CG / 32 matrix instructions), then the latency of the token rows.  E 8, d 2048,
-// f 8192, 4096 tokens, top-2: group 64 and 128 296 us up and 280 us down, 929 and 981 TFLOP/s; group
-// 32 334 and 328 us.  Without the products the loads alone take about 170 us.
+// f 8192, 4096 tokens, top-2: group 64 and 128 296 us up and 280 us down, 929 and 981 TFLOP/s (on a
+// slower card 316 and 298); group 32 334 and 328 us.  The loads without the products: about 170 us.
 template <int WF, int RT, int FT, int GROUP, int ACT>
 __global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
   constexpr bool GATED = ACT == kQGated;

@@ -5,8 +5,10 @@
 //   dl_te = p_te (dp_te - sum_j p_tj dp_tj) + dlogits_te      p = softmax of the logits
 //   dx = dx_add + dl W_r,   dW_r = dl^T x,   db = sum_t dl_t
 //
-// Bound: HBM, for the experts counts that the library takes in bf16 (x is read once for dW_r, dx
-// is written once; 4 T E d flops).  dl itself is E values a token, so it goes through memory
+// Bound: HBM, for the expert counts that the library takes in bf16 (x is read once for dW_r, dx
+// is written once; 4 T E d flops): T 32768, d 4096, E 8 7.4 us for dl, 101 us for dx (537 MB with
+// dx_add and dx), 69 us for dW_r (268 MB), 5.0 us for the sums over the token ranges; T 16384, d 2048,
+// E 64 8.0, 32.7, 24.3 and 4.8 us.  dl itself is E values a token, so it goes through memory
 // between the kernels: k_route_dlogits writes it once in the two layouts that the matrix
 // instructions want (experts contiguous for dx, tokens contiguous for dW_r).
 //
