@@ -198,6 +198,16 @@ def test_route_backward(T, d, E, k, masked, bf16):
     check_backward(x, w, lg, ids, dg, dlg, mask, add, bf16, got)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,d,E,k", [(9000, 2048, 40, 2),   # long token ranges of dW_r
+                                     (100, 64, 40, 20), (70, 72, 256, 256)])  # many choices
+def test_route_backward_long_ranges_and_many_choices(T, d, E, k, bf16):
+    x, w, lg, ids, dg, dlg, mask, add = backward_inputs(T, d, E, k, bf16, True, 6)
+    got = run_backward(x, w, lg, ids, dg, dlg, mask, add, bf16)
+    check_backward(x, w, lg, ids, dg, dlg, mask, add, bf16, got)
+    check_balance(lg, ids, mask, run_balance(lg, ids, mask))
+
+
 @pytest.mark.parametrize("T,d,E,k", [(19, 7, 3, 2), (100, 33, 9, 1), (700, 130, 40, 2)])
 def test_route_backward_odd_widths_f32(T, d, E, k):
     x, w, lg, ids, dg, dlg, _, add = backward_inputs(T, d, E, k, False, False, 4)
