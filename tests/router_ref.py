@@ -52,9 +52,14 @@ def balance(logits, ids, mask=None, coef=1.0, grad_scale=1.0, counts=None):
 
 def softmax_bound(logits, E):
     """Relative error of one fp32 probability: the subtraction (|l - max| u, as exp turns it into
-    a relative one), exp (2 steps), the sum of E terms, the reciprocal and the product."""
-    z = np.where(np.isfinite(logits), logits, 0.0)
-    spread = (z.max(axis=1) - z.min(axis=1))[:, None] if len(z) else np.zeros((0, 1))
+    a relative one), exp (2 steps), the sum of E terms, the reciprocal and the product.  A logit
+    120 or more below the row's largest counts for none of it: e^-120 < 2^-149, so fp32 has 0 there
+    and the bounds' terms in TINY cover the probability."""
+    z = np.where(np.isfinite(logits), np.asarray(logits, np.float64), 0.0)
+    if not len(z):
+        return np.zeros((0, 1))
+    m = z.max(axis=1, keepdims=True)
+    spread = m - np.where(z >= m - 120, z, m).min(axis=1, keepdims=True)
     return (2 * spread + E + 12) * U
 
 

@@ -248,6 +248,22 @@ def test_route_backward_edges(T, d, E, k, bf16):
     assert all(not a.any() for a in none.values())
 
 
+def test_logits_at_the_ends_of_fp32():
+    """Masks written as the lowest fp32 value, in part of a row and in all of it, beside the
+    highest one: differences leave fp32, probabilities do not."""
+    T, d, E, k = 96, 64, 12, 2
+    x, w, lg, ids, dg, dlg, _, add = backward_inputs(T, d, E, k, False, False, 13)
+    low, high = np.finfo(np.float32).min, np.finfo(np.float32).max
+    lg[:20, 5:] = low
+    lg[20:40] = low
+    lg[40:60, 3] = high
+    lg[50:60, 4:] = low
+    check_balance(lg, ids, None, run_balance(lg, ids, None))
+    got = run_backward(x, w, lg, ids, dg, dlg, None, add)
+    check_backward(x, w, lg, ids, dg, dlg, None, add, False, got)
+    assert all(np.isfinite(a).all() for a in got.values())
+
+
 def test_empty_batch_writes_zero_sums():
     shape = B.make_shape(0, 64, 8, 8, 2, 0, B.MOE_BF16)
     loss, counts, probs = (Guarded((1,), torch.float32), Guarded((8,), torch.int32),
