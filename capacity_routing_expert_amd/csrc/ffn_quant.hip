@@ -216,8 +216,8 @@ __device__ __forceinline__ void store_tile(const QArgs& a, const f32x4_t (&acc)[
 // two LDS buffers one step ahead, one barrier a step; otherwise (one or two tokens, where the
 // barriers cost more than the loads) every wave loads its own.
 //
-// Bound: the weight stream.  E 8, d 2048, f 8192, 64 tokens, group 32 (75 MB a product): 19.3 us
-// up, 22.9 us down, 3.9 and 3.3 TB/s; loading the same codes without products or token rows: 16.8
+// Bound: the weight stream.  E 8, d 2048, f 8192, 64 tokens, group 32 (75 MB a product): 18.4 us
+// up, 22.9 us down, 4.1 and 3.3 TB/s; loading the same codes without products or token rows: 16.8
 // and 18.3 us, and 2.3 us of it are an empty launch.  Column blocks outermost in the storage (runs of
 // 8 KiB a block of waves) instead of rows outermost: 24.2 -> 20.0 us up, 26.3 -> 22.2 us down.
 template <int RT, int FT, int WF, int WK, int D, bool STAGED, int GROUP, int ACT>
@@ -473,15 +473,18 @@ hipError_t run_rows(const QArgs& a, int64_t tiles, int64_t NT, hipStream_t st) {
 
 // Rows an expert on average, and blocks a variant would launch, decide (us of both products, unless said
 // otherwise; random routing):
-//  - more than 48 rows: 64 x 256 tiles of 8 waves, once they are 160 blocks (8 experts, d 2048, f
-//    8192, 1024 rows each: 594 against 662 for 32 x 256; 64 gated experts, d 2048, f 1408, 72 rows
-//    each: 146 against 159; 38 rows each: 111 against 98);
+//  - more than 48 rows: 64 x 256 tiles of 8 waves, once they are one a CU (8 experts, d 2048, f 8192,
+//    1024 rows each: 594 against 662 for 32 x 256; 64 gated experts, d 2048, f 1408, 72 rows each:
+//    146 against 159; 38 rows each: 111 against 98); gated, which has no 32 x 128, from 160 blocks
+//    on (2 experts, d 2048, f 4096, 200 rows each: 44 against 49);
 //  - at most 6 rows and 512 blocks: 16 token rows by 128 weight rows, waves of twice the width (64
 //    tokens, top-6, 64 gated experts of d 2048, f 1408: 57 against 63 for the next; 16 experts of
 //    4 rows, d 2048, f 4096, 44.5 against 43.2: about even at the limit);
-//  - else 32 rows x 256 weight rows, from 160 blocks on (64 experts, 24 rows each: 29 up / 31 down
-//    against 33 / 29 for the next);
-//  - else 32 x 128, from 256 blocks on (8 experts, f 8192, 16 rows each, up: 19.3 against 37);
+//  - else 32 rows x 256 weight rows, from 320 blocks on, 640 for more than 48 rows (2 experts, d 624,
+//    f 7400, 2200 rows each, 400 down: 236 against 177 for the next; 8 experts, d 2048, f 8192, 16
+//    rows each, 256 up: 42.0 against 40.1; 64 experts, 24 rows each: 29 up / 31 down against 33 /
+//    29); gated from 160 on (8 experts, f 4096, 16 rows each: 29.5 against 32.3 for the last but one);
+//  - else 32 x 128, from 256 blocks on (8 experts, f 8192, 16 rows each, up: 19 against 37);
 //  - else K is shared by groups of waves, 64 weight rows a block.  Four groups for long K: 32 token
 //    rows if the blocks, of 16 waves, are one a CU (d 2048, f 8192, 16 rows each: 41.8 against 46.0
 //    with 16 token rows; 20 rows each, where some CUs get two: 60.5 against 54.6).  Two groups
@@ -511,12 +514,12 @@ hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
   };
   // few row tiles go over all XCDs; more are dealt to pairs of them
   a.xcds = active < 8 ? 8 : 2;
-  if (mean > 48 && NT(256) * likely(64) >= 160)
+  if (mean > 48 && NT(256) * likely(64) >= (GATED ? 160 : 256))
     return launch_timed(k_quant_tiles<8, 4, 2, GROUP, ACT>,
                         dim3((unsigned)tile_grid(most(64), NT(256), a.xcds)), dim3(512), 0, st, a);
   if (mean <= 6 && NT(128) * likely(16) >= 512)
     return run_rows<1, 2 * F1, 4, 1, GATED ? 2 : 4, true, GROUP, ACT>(a, most(16), NT(128 * F1), st);
-  if (NT(256) * likely(32) >= 160)
+  if (NT(256) * likely(32) >= (GATED ? 160 : mean > 48 ? 640 : 320))
     return run_rows<2, 2, 8, 1, 3, true, GROUP, ACT>(a, most(32), NT(256), st);
   if constexpr (!GATED)
     if (NT(128) * likely(32) >= 256)

@@ -134,7 +134,8 @@ def test_expert_ffn(T, d, f, E, k, group, C, gated):
 # every kernel that the products choose from, by rows an expert, blocks and length, in both products
 VARIANT_SHAPES = [  # T, d, f, E, k, C
     (200, 136, 264, 256, 3, 256.0),  # few rows, many blocks
-    (640, 264, 136, 160, 2, 160.0),  # 32 rows by 256 weight rows
+    (640, 264, 136, 160, 2, 160.0),  # 32 rows by 256 weight rows: down, and up of gated experts
+    (480, 136, 520, 120, 2, 120.0),  # up
     (560, 248, 248, 140, 2, 140.0),  # 32 rows by 128
     (40, 4104, 136, 2, 1, 2.0),      # K shared by four groups of waves: up, 32 rows
     (40, 136, 4104, 2, 1, 2.0),      # down
