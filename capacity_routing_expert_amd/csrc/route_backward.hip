@@ -509,7 +509,8 @@ __global__ __launch_bounds__(256) void k_route_dw_bf16(const bf16_t* __restrict_
 // ---------------------------------------------------------------- fp32
 // The sum of a matrix instruction does not mind the order of its terms, so lane group kg takes experts
 // (dx) or tokens (dW_r) 4 kg .. 4 kg + 3 of 16, one 16-byte load, and tile i of four holds columns
-// 4 n + i: rows of x, W_r and dx move in 16-byte pieces, 256 B a row.  VEC: d is a multiple of 4.
+// 4 n + i: rows of x, W_r and dx move in 16-byte pieces, 256 B a row.  VEC: d is a multiple of 4 and the
+// arrays lie on 16 bytes.
 // T 1970, d 4024, E 11, with dx_add: dx 13.5 us (95 MB), dW_r 12.8 us (32 MB); with a dword a lane
 // and loads behind branches 57 us for the whole pass instead of 32.
 template <bool VEC>
@@ -835,7 +836,10 @@ hipError_t launch_route_backward(const moe_shape& s, const void* x, const void* 
                : E <= 32 ? dw_run(k_route_dw_f32<2, VEC>)
                          : dw_run(k_route_dw_f32<4, VEC>);
       };
-      err = d % 4 == 0 ? run(std::true_type()) : run(std::false_type());
+      // 16-byte pieces where every row starts on one (fp32 arrays need 4 bytes)
+      auto at16 = [](const void* p) { return (uintptr_t)p % 16 == 0; };
+      const bool vec16 = d % 4 == 0 && at16(x) && at16(w) && at16(dx) && at16(dx_add) && at16(dw);
+      err = vec16 ? run(std::true_type()) : run(std::false_type());
       if (err != hipSuccess) return err;
     }
   }

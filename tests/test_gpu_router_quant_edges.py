@@ -78,6 +78,32 @@ def test_arrays_off_16_bytes(T, E, k):
             assert np.all(np.abs(got[name].double().cpu().numpy() - r) <= b), (name, n)
 
 
+def test_f32_arrays_on_4_bytes():
+    """fp32 x, W_r, dx, dx_add and dW_r need 4 bytes: each off 16 in turn, and all of them, give the
+    bits of the aligned call (the sums are the same, only the pieces are not)."""
+    T, d, E, k = 300, 64, 20, 3
+    x, w, logits, ids, dg, mask = router_inputs(T, d, E, k, torch.float32)
+    add = torch.randn(T, d, device=DEV)
+    shape = B.make_shape(T, d, 8, E, k, 0, B.MOE_F32)
+    ws = torch.empty(B.workspace_bytes_route_backward(shape), dtype=torch.uint8, device=DEV)
+
+    def run(off):
+        place = lambda t, name: shifted(t, off[name]) if off.get(name) else t
+        dx = place(torch.full((T, d), 7.0, device=DEV), "dx")
+        dw = place(torch.full((E, d), 7.0, device=DEV), "dw")
+        db = torch.empty(E, device=DEV)
+        B.moe_route_backward(shape, place(x, "x"), place(w, "w"), logits, ids, dg, None, dx=dx,
+                             dw_router=dw, db_router=db, dx_add=place(add, "add"), token_mask=mask,
+                             ws=ws)
+        return dx, dw, db
+
+    want = run({})
+    for n in (1, 2, 3):
+        for off in [{name: n} for name in ("x", "w", "dx", "add", "dw")] + [
+                dict(x=n, w=n, dx=n, add=n, dw=n)]:
+            assert all(torch.equal(a, b) for a, b in zip(run(off), want)), off
+
+
 def test_logits_past_32_bit_offsets():
     """T x E past 2^31 elements: one block of tokens repeated.  Every repeat's gradients are the same
     bits, and dx those of the block alone; counts are multiples; the sums over tokens are within
