@@ -88,13 +88,16 @@ struct RouterRow {
         if (i * LPT + l < E) row[i * LPT + l] = v[i];
     }
   }
-  // logits -> softmax probabilities in place, fp32 (the padding's are 0; a row whose logits are
-  // all -inf has probabilities 0)
+  // logits -> softmax probabilities in place, fp32 (the padding's are 0).  A row whose logits are
+  // all -inf sums to 0 and has probabilities 0.  The maximum leaves NaN out (the padding is -inf, so
+  // it is -inf for a row of nothing but NaN, too); the exponentials do not, and the sum carries it
+  // to the whole row.
   static __device__ __forceinline__ void softmax(float (&v)[NV]) {
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
     m = row_max<LPT>(m);
+    m = m == -INFINITY ? 0.0f : m;  // -inf - 0 is -inf, where -inf - -inf would be NaN
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -102,9 +105,9 @@ struct RouterRow {
       s += v[i];
     }
     s = row_sum<LPT>(s);
-    const float inv = m == -INFINITY ? 0.0f : 1.0f / s;
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s;  // in any other row the maximum adds 1
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = m == -INFINITY ? 0.0f : v[i] * inv;
+    for (int i = 0; i < NV; ++i) v[i] *= inv;
   }
 };
 

@@ -532,7 +532,8 @@ size_t moe_workspace_bytes_route_backward(const moe_shape* shape);
  *              the experts'); may be dx itself, must not overlap it otherwise
  *   dx         [T, d_model] dtype out or NULL; must not overlap x
  *   dw_router  [E, d_model] fp32 out or NULL;  db_router [E] fp32 out or NULL
- * At least one output is given.  Products of bf16 inputs are formed with dl in bf16 terms (three
+ * At least one output is given.  A row whose logits are all -inf has probabilities 0; NaN in a valid
+ * row reaches the outputs.  Products of bf16 inputs are formed with dl in bf16 terms (three
  * for dw_router: 24 bits; two for dx: 16 bits, against the 8 that dx keeps) and summed in fp32;
  * f32: fp32 throughout.  Sums are in a fixed order: equal calls give equal bits.  In bf16,
  * dw_router must be 16-byte aligned. */

@@ -1,0 +1,149 @@
+"""Rows of NaN and of -inf in the balance loss and the router's backward pass, for expert counts
+with and without padding of a row over the lanes: a NaN in a valid row reaches the outputs, a row
+whose logits are all -inf has probabilities 0, and no row reaches another's."""
+from __future__ import annotations
+
+import sys
+
+import pytest
+import torch
+
+from capacity_routing_expert_amd import binding as B
+from capacity_routing_expert_amd import layer as L
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+NAN, INF = float("nan"), float("inf")
+EXPERTS = [1, 2, 3, 4, 5, 8, 12, 17, 24, 60, 64, 100, 128, 160, 256]
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    B.lib()  # loud failure if the library is missing
+    yield
+    torch.cuda.synchronize()
+
+
+def shifted(t, n):
+    """A copy of t whose first element lies n elements past an aligned address."""
+    flat = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    out = flat[n:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def bad_rows(E):
+    """Rows that hold a NaN: all of it, its negative, beside -inf on either side, beside numbers."""
+    rows = [torch.full((E,), NAN), torch.full((E,), -NAN)]
+    for at in {0, E // 2, E - 1}:
+        for rest in (-INF, 0.0, INF):
+            row = torch.full((E,), rest)
+            row[at] = NAN
+            rows.append(row)
+    return torch.stack(rows)
+
+
+def inputs(T, E, k, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    logits = torch.randn(T, E, generator=g, device=DEV)
+    ids = logits.topk(k, dim=1).indices.to(torch.int32).contiguous()
+    return g, logits, ids
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("T", [60, 20000])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_balance_nan_rows(E, T, off):
+    k = min(E, 2)
+    say(f"[balance, NaN rows] T={T} E={E} off={off}")
+    _, clean, ids = inputs(T, E, k, E)
+    bad = bad_rows(E).to(DEV)
+    for i in range(len(bad)):
+        at = (i * 7919 + 3) % T
+        logits = clean.clone()
+        logits[at] = bad[i]
+        got = L.balance_loss(shifted(logits, off), ids, coef=0.5)
+        assert bool(torch.isnan(got["loss"]).all()), i
+        assert bool(torch.isnan(got["probs"]).all()), i
+        nan = torch.isnan(got["dlogits"])
+        assert bool(nan[at].all()), i
+        assert int(nan.sum()) == E, i
+        # padding: the same row does not count
+        mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+        mask[at] = 0
+        got = L.balance_loss(shifted(logits, off), ids, coef=0.5, token_mask=mask)
+        assert all(bool(torch.isfinite(got[n]).all()) for n in ("loss", "probs", "dlogits")), i
+        assert not bool(got["dlogits"][at].any())
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_balance_empty_rows(E, off):
+    """Rows of -inf add nothing: probabilities and gradient 0, all else finite."""
+    T, k = 300, min(E, 2)
+    _, logits, ids = inputs(T, E, k, E + 1)
+    logits[::3] = -INF
+    got = L.balance_loss(shifted(logits, off), ids, coef=0.5)
+    assert not bool(got["dlogits"][::3].any())
+    assert all(bool(torch.isfinite(got[n]).all()) for n in ("loss", "probs", "dlogits"))
+    # the probabilities of the 200 other rows: each sums to 1 within E steps of fp32
+    assert abs(float(got["probs"].double().sum()) - 2 / 3) <= (E + 40) * 2.0 ** -24
+    none = L.balance_loss(torch.full_like(logits, -INF), ids, coef=0.5)
+    assert not bool(none["loss"].any()) and not bool(none["probs"].any())
+    assert not bool(none["dlogits"].any())
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_route_backward_nan_rows(E, bf16, off):
+    T, d, k = 200, 72, min(E, 2)
+    say(f"[route backward, NaN rows] E={E} bf16={bf16} off={off}")
+    g, clean, ids = inputs(T, E, k, E + 2)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    x = (torch.randn(T, d, generator=g, device=DEV)).to(dt)
+    w = (1 + torch.rand(E, d, generator=g, device=DEV)).to(dt)  # no zeros for a NaN to hide behind
+    dg = torch.randn(T, k, generator=g, device=DEV)
+    dl = torch.randn(T, E, generator=g, device=DEV)
+    bad = bad_rows(E).to(DEV)
+    for i in range(len(bad)):
+        at = (i * 37 + 3) % T
+        logits = clean.clone()
+        logits[at] = bad[i]
+        got = L.route_backward(x, w, shifted(logits, off), ids, dgates=dg, dlogits=dl)
+        nan = torch.isnan(got["dx"])
+        assert bool(nan[at].all()) and int(nan.sum()) == d, i
+        assert bool(torch.isnan(got["dw_router"]).all()), i
+        assert bool(torch.isnan(got["db_router"]).all()), i
+        mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+        mask[at] = 0
+        got = L.route_backward(x, w, shifted(logits, off), ids, dgates=dg, dlogits=dl,
+                               token_mask=mask)
+        assert all(bool(torch.isfinite(t).all()) for t in got.values()), i
+        assert not bool(got["dx"][at].any())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", EXPERTS)
+def test_route_backward_empty_rows(E, bf16):
+    """A row of -inf passes no gate gradient on: the same bits as with its dgates zero."""
+    T, d, k = 200, 72, min(E, 2)
+    g, logits, ids = inputs(T, E, k, E + 3)
+    logits[5::9] = -INF
+    dt = torch.bfloat16 if bf16 else torch.float32
+    x = torch.randn(T, d, generator=g, device=DEV).to(dt)
+    w = torch.randn(E, d, generator=g, device=DEV).to(dt)
+    dg = torch.randn(T, k, generator=g, device=DEV)
+    got = L.route_backward(x, w, logits, ids, dgates=dg)
+    assert not bool(got["dx"][5::9].any())
+    assert all(bool(torch.isfinite(t).all()) for t in got.values())
+    dg[5::9] = 0
+    want = L.route_backward(x, w, logits, ids, dgates=dg)
+    assert all(torch.equal(a, b) for a, b in zip(got.values(), want.values()))
