@@ -211,7 +211,10 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
   if (tid < E) atomicMin(&cmin, cnt[tid]);
   __syncthreads();
   if (a.count_part && blockIdx.x == 0 && tid <= E) a.totals[tid] = cnt[tid];
-  const float gscale = (float)(a.grad_scale * balance_norm(a, cnt[E]));
+  // The gradient's factor as mantissa and exponent: coef and grad_scale are any fp32 numbers, and a
+  // factor that left fp32 would make NaN of the zeros it multiplies (padding, equal counts).
+  int gexp;
+  const float gman = (float)frexp(a.grad_scale * balance_norm(a, cnt[E]), &gexp);
   float c[NV], acc[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_balance(BalanceArgs a) {
     if (a.dlogits) {
       dot = row_sum<LPT>(dot);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = gscale * v[i] * (c[i] - dot);
+      for (int i = 0; i < NV; ++i) v[i] = ldexpf(gman * v[i] * (c[i] - dot), gexp);
       if (t < a.T) Row::store(a.dlogits + t * E, E, l, v);
     }
   }

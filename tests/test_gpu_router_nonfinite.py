@@ -147,3 +147,31 @@ def test_route_backward_empty_rows(E, bf16):
     dg[5::9] = 0
     want = L.route_backward(x, w, logits, ids, dgates=dg)
     assert all(torch.equal(a, b) for a, b in zip(got.values(), want.values()))
+
+
+@pytest.mark.parametrize("coef,scale", [(1e30, 1e30), (-1e38, 1e38), (1e38, -3e38)])
+@pytest.mark.parametrize("T,E", [(50, 8), (300, 12), (9000, 64)])
+def test_balance_scale_past_fp32(T, E, coef, scale):
+    """coef times grad_scale leaves fp32, the formula's zeros do not: padding, and all rows where
+    the counts are equal."""
+    _, logits, ids = inputs(T, E, 2, 9)
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[::4] = 0
+    got = L.balance_loss(logits, ids, coef=coef, grad_scale=scale, token_mask=mask)
+    assert not bool(got["dlogits"][::4].any())
+    even = torch.arange(E, dtype=torch.int32, device=DEV).repeat(T, 1)
+    assert not bool(L.balance_loss(logits, even, coef=coef, grad_scale=scale)["dlogits"].any())
+
+
+def test_balance_gradient_back_in_fp32():
+    """coef E grad_scale = 2^141 and p = (1 - q, q) with q near 2^-14: one token on expert 0 has the
+    gradient 2^141 q (1 - q) times (1, -1), below 2^128.  In fp32 q is off by E + 12 steps and twice
+    its logit's (here 10), 1 - q by as much of q and by half a step of 1, 2^-24 / 2^-14 of q."""
+    logits = torch.tensor([[0.0, -10.0]], device=DEV)
+    ids = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    got = L.balance_loss(logits, ids, coef=2.0 ** 90, grad_scale=2.0 ** 50)
+    q = 1.0 / (1.0 + torch.exp(torch.tensor(10.0, dtype=torch.float64)).item())
+    want = 2.0 ** 141 * q * (1 - q)
+    d = got["dlogits"].double().cpu()[0]
+    assert abs(float(d[1]) + want) <= 40 * 2.0 ** -24 * want
+    assert abs(float(d[0]) - want) <= (40 * 2.0 ** -24 + 8 * 2.0 ** -24 / q) * want
