@@ -87,6 +87,20 @@ moe_status run_timed_stage(const hipEvent_t* ev, hipStream_t st, const char* wha
   return unused ? record_now(ev, 2, st) : MOE_OK;
 }
 
+// A call that the two arms are for and that is refused before layer_forward sees it disarms them.
+void drop_timing() {
+  hipEvent_t armed[4];
+  take_timing(armed);
+  take_stage_timing(armed);
+}
+
+// `n` event handles, none of them NULL
+moe_status check_events(moe_event_t const* events, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
+  return MOE_OK;
+}
+
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -311,6 +325,7 @@ moe_status layer_forward(const moe_shape* shape, const void* x, const void* w_ro
   hipEvent_t tev[4], sev[4];
   const bool timed = take_timing(tev);  // both consumed by this call even if it fails
   const bool stimed = take_stage_timing(sev);
+  if (events) MOE_TRY(check_events(events, 6));
   MOE_TRY(check_shape(shape));
   const moe_shape& s = *shape;
   auto rec = [&](int i) -> moe_status {
@@ -426,9 +441,7 @@ moe_status layer_forward_dropless(const moe_shape* shape, const void* x, const v
   const bool timed = take_timing(tev);  // consumed by this call even if it fails
   MOE_TRY(check_shape(shape));
   const moe_shape& s = *shape;
-  if (events)
-    for (int i = 0; i < 6; ++i)
-      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
+  if (events) MOE_TRY(check_events(events, 6));
   auto rec = [&](int i) -> moe_status {
     if (!events) return MOE_OK;
     hipError_t err = hipEventRecord((hipEvent_t)events[i], st);
@@ -544,9 +557,7 @@ moe_status layer_forward_batches(const moe_shape* batch_shape, int32_t n_batches
                                  moe_event_t const* events) {
   MOE_TRY(check_batches(batch_shape, n_batches, consolidate));
   const moe_shape& bs = *batch_shape;
-  if (events)
-    for (int i = 0; i < 5; ++i)
-      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
+  if (events) MOE_TRY(check_events(events, 5));
   auto rec = [&](int i) -> moe_status {
     if (!events) return MOE_OK;
     hipError_t err = hipEventRecord((hipEvent_t)events[i], st);
@@ -664,6 +675,18 @@ moe_status scratch_address(void** ptr) {
   }
   *ptr = g_scratch_ptr[dev];
   return MOE_OK;
+}
+
+// The scratch, for a shape whose workspace fits into it (an empty batch needs none).
+moe_status noalloc_scratch(const moe_shape* shape, void** ptr) {
+  MOE_TRY(check_shape(shape));
+  const size_t need = layout(*shape).total;
+  if (need > (size_t)MOE_NOALLOC_SCRATCH_BYTES)
+    return fail(MOE_ERR_WORKSPACE,
+                "this shape needs %zu bytes of scratch; the fixed scratch holds %zu bytes "
+                "(use moe_layer_forward with a workspace)",
+                need, (size_t)MOE_NOALLOC_SCRATCH_BYTES);
+  return shape->T > 0 ? scratch_address(ptr) : MOE_OK;
 }
 
 }  // namespace
@@ -870,15 +893,11 @@ moe_status moe_layer_forward_noalloc(const moe_shape* shape, const void* x, cons
                                      int32_t* topk_ids, float* topk_gates, int32_t* slot_of,
                                      uint8_t* drop_mask, int32_t* expert_counts,
                                      moe_stream_t stream) {
-  MOE_TRY(check_shape(shape));
-  const size_t need = layout(*shape).total;
-  if (need > (size_t)MOE_NOALLOC_SCRATCH_BYTES)
-    return fail(MOE_ERR_WORKSPACE,
-                "this shape needs %zu bytes of scratch; the fixed scratch holds %zu bytes "
-                "(use moe_layer_forward with a workspace)",
-                need, (size_t)MOE_NOALLOC_SCRATCH_BYTES);
   void* ws = nullptr;
-  if (shape->T > 0) MOE_TRY(scratch_address(&ws));
+  if (moe_status st = noalloc_scratch(shape, &ws); st != MOE_OK) {
+    drop_timing();
+    return st;
+  }
   return layer_forward(shape, x, w_router, b_router, w1, b1, w2, b2, out, topk_ids, topk_gates,
                        slot_of, drop_mask, expert_counts, ws, (size_t)MOE_NOALLOC_SCRATCH_BYTES,
                        (hipStream_t)stream, nullptr);
@@ -921,9 +940,10 @@ moe_status moe_layer_forward_profiled(const moe_shape* shape, const void* x,
                                       float* topk_gates, int32_t* slot_of, uint8_t* drop_mask,
                                       int32_t* expert_counts, void* ws, size_t ws_bytes,
                                       moe_stream_t stream, moe_event_t const* events) {
-  if (!events) return fail(MOE_ERR_INVALID_ARGUMENT, "events is NULL");
-  for (int i = 0; i < 6; ++i)
-    if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
+  if (!events) {
+    drop_timing();
+    return fail(MOE_ERR_INVALID_ARGUMENT, "events is NULL");
+  }
   return layer_forward(shape, x, w_router, b_router, w1, b1, w2, b2, out, topk_ids, topk_gates,
                        slot_of, drop_mask, expert_counts, ws, ws_bytes, (hipStream_t)stream,
                        events);
@@ -936,9 +956,6 @@ moe_status moe_layer_forward_padded(const moe_shape* shape, const void* x, const
                                     int32_t* expert_counts, void* y_rows, void* ws,
                                     size_t ws_bytes, moe_stream_t stream,
                                     moe_event_t const* events) {
-  if (events)
-    for (int i = 0; i < 6; ++i)
-      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
   return layer_forward(shape, x, w_router, b_router, w1, b1, w2, b2, out, topk_ids, topk_gates,
                        slot_of, drop_mask, expert_counts, ws, ws_bytes, (hipStream_t)stream,
                        events, true, y_rows);
@@ -950,9 +967,6 @@ moe_status moe_layer_forward_gated(const moe_shape* shape, const void* x, const 
                                    int32_t* slot_of, uint8_t* drop_mask, int32_t* expert_counts,
                                    void* ws, size_t ws_bytes, moe_stream_t stream,
                                    moe_event_t const* events) {
-  if (events)
-    for (int i = 0; i < 6; ++i)
-      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
   return layer_forward(shape, x, w_router, b_router, w13, nullptr, w2, nullptr, out, topk_ids,
                        topk_gates, slot_of, drop_mask, expert_counts, ws, ws_bytes,
                        (hipStream_t)stream, events, false, nullptr, true);
@@ -1251,14 +1265,9 @@ moe_status moe_layer_forward_quantized(const moe_shape* shape, const void* x, co
                                        size_t ws_bytes, moe_stream_t stream,
                                        moe_event_t const* events) {
   if (!experts) {
-    hipEvent_t armed[4];  // consumed by this call even if it fails
-    take_timing(armed);
-    take_stage_timing(armed);
+    drop_timing();
     return fail(MOE_ERR_INVALID_ARGUMENT, "experts is NULL");
   }
-  if (events)
-    for (int i = 0; i < 6; ++i)
-      if (!events[i]) return fail(MOE_ERR_INVALID_ARGUMENT, "events[%d] is NULL", i);
   return layer_forward(shape, x, w_router, b_router, experts->w1_codes, experts->b1,
                        experts->w2_codes, experts->b2, out, topk_ids, topk_gates, slot_of,
                        drop_mask, expert_counts, ws, ws_bytes, (hipStream_t)stream, events, false,

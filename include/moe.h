@@ -225,8 +225,8 @@ moe_status moe_layer_forward_profiled(const moe_shape* shape, const void* x,
 /* Kernel timing of the two expert GEMMs (the layer's expert-FFN stage, Worked Example: the
  * expert computations whose slowest expert sets the wall-clock time), with nothing inserted
  * between launches.  Arms the NEXT call on this thread of moe_layer_forward (or its _profiled,
- * _padded, _gated or _quantized form), moe_layer_forward_dropless(_gated), moe_expert_ffn(_quantized)
- * or moe_expert_ffn_pairs:
+ * _padded, _gated, _quantized or _noalloc form), moe_layer_forward_dropless(_gated),
+ * moe_expert_ffn(_quantized) or moe_expert_ffn_pairs:
  *   events[0], [1]  start and end of the up-projection's kernel
  *   events[2], [3]  start and end of the down-projection's kernel
  * recorded by the kernel launches themselves (hipExtLaunchKernel).  The events are the
