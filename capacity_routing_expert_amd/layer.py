@@ -373,9 +373,10 @@ def quantize_experts(w1: torch.Tensor, b1: torch.Tensor | None, w2: torch.Tensor
     if tuple(w1.shape) != (E, 2 * f if gated else f, d):
         raise ValueError(f"w1 is {tuple(w1.shape)}, w2 {tuple(w2.shape)}: w1 has to be "
                          f"{(E, 2 * f if gated else f, d)}")
-    return B.QuantizedExperts(E, d, f, group, gated, *quantize_weights(w1, group),
-                              None if gated else b1, *quantize_weights(w2, group),
-                              None if gated else b2)
+    if gated and (b1 is not None or b2 is not None):
+        raise ValueError("gated experts have no biases")
+    return B.QuantizedExperts(E, d, f, group, gated, *quantize_weights(w1, group), b1,
+                              *quantize_weights(w2, group), b2)
 
 
 def expert_ffn_quantized(shape: B.MoeShape, x: torch.Tensor, experts: B.QuantizedExperts,
