@@ -471,29 +471,36 @@ hipError_t run_rows(const QArgs& a, int64_t tiles, int64_t NT, hipStream_t st) {
                       dim3((unsigned)tile_grid(tiles, NT, a.xcds)), dim3(64 * WF * WK), lds, st, a);
 }
 
-// Rows an expert on average, and blocks a variant would launch, decide (us of both products, unless said
-// otherwise; random routing):
+// Rows an expert on average, and blocks a variant would launch, decide.  Kernel times in us, "up + down"
+// or of the product named, random routing, the weights of several layers in turn (more than the
+// caches hold):
 //  - more than 48 rows: 64 x 256 tiles of 8 waves, once they are one a CU (8 experts, d 2048, f 8192,
-//    1024 rows each: 594 against 662 for 32 x 256; 64 gated experts, d 2048, f 1408, 72 rows each:
-//    146 against 159; 38 rows each: 111 against 98); gated, which has no 32 x 128, from 160 blocks
-//    on (2 experts, d 2048, f 4096, 200 rows each: 44 against 49);
+//    1024 rows each, group 128: 317 + 295 against 372 + 312 for 32 x 256; 64 experts, d 2048, f 1408,
+//    72 rows each: 60 + 52 against 63 + 54; 38 rows each: 41 + 40 against 41 + 38.  At the limit it
+//    depends on the blocks: 48 rows each 42 + 41 against 48 + 45 with 384 and 512 tiles, 38 + 33
+//    against 31 + 28 for 32 experts of f 2048 with 256); gated, which has no 32 x 128, from 160
+//    blocks on (2 experts, d 2048, f 4096, 200 rows each, up: 23.6 against 28.9 for K shared);
 //  - at most 6 rows and 512 blocks: 16 token rows by 128 weight rows, waves of twice the width (64
-//    tokens, top-6, 64 gated experts of d 2048, f 1408: 57 against 63 for the next; 16 experts of
-//    4 rows, d 2048, f 4096, 44.5 against 43.2: about even at the limit);
+//    experts, d 2048, f 1408, 6 rows each: 22.5 + 20.9 against 23.0 + 22.3 for the 32 x 128; 16 experts of
+//    4 rows, d 2048, f 4096, 512 blocks up: 18.9 against 19.1).  Gated by 256, from 256 blocks on (64
+//    experts of 4 rows, d 1024, f 1408: 21.5 against 23.5 for 32 x 256 and for 16 x 128 with K shared;
+//    128 experts of 6 rows, d 2048, f 768, group 128: 39.3 against 45.3 and 41.0; but 64 experts of 6
+//    rows, d 2048, f 1408: 43.5 against 44.8 and 39.3);
 //  - else 32 rows x 256 weight rows, from 320 blocks on, 640 for more than 48 rows (2 experts, d 624,
-//    f 7400, 2200 rows each, 400 down: 236 against 177 for the next; 8 experts, d 2048, f 8192, 16
-//    rows each, 256 up: 42.0 against 40.1; 64 experts, 24 rows each: 29 up / 31 down against 33 /
-//    29); gated from 160 on (8 experts, f 4096, 16 rows each: 29.5 against 32.3 for the last but one);
-//  - else 32 x 128, from 256 blocks on (8 experts, f 8192, 16 rows each, up: 19 against 37);
+//    f 7400, 2200 rows each, 400 down: 155 against 93 for the next; 8 experts, d 2048, f 8192, 16
+//    rows each, 256 up: 21.9 against 20.3; 64 experts, d 2048, f 1408, 24 rows each, 384 up: 29.4
+//    against 33.2); gated from 160 on (8 experts, f 4096, 16 rows each, 256 up: 18.1 against 18.7 for
+//    the last but one);
+//  - else 32 x 128, from 256 blocks on (8 experts, f 8192, 16 rows each, up: 20.3 against 32.4);
 //  - else K is shared by groups of waves, 64 weight rows a block.  Four groups for long K: 32 token
-//    rows if the blocks, of 16 waves, are one a CU (d 2048, f 8192, 16 rows each: 41.8 against 46.0
-//    with 16 token rows; 20 rows each, where some CUs get two: 60.5 against 54.6).  Two groups
-//    for K below 4096 (8 gated experts, d 2048, f 768, 9 rows each: 12.2 against 14.6 with four), of 16
-//    token rows up to 24 rows an expert (24 rows each: 15.1 against 17.4 with 32 token rows; 64 rows
-//    each: 21.4 against 19.9);
+//    rows if the blocks, of 16 waves, are one a CU (d 2048, f 8192, 16 rows each, down: 22.0 against
+//    27.7 with 16 token rows; 20 rows each, where some CUs get two once an expert has more than 32:
+//    60.5 against 54.6 for both products).  Two groups for K below 4096 (8 gated experts, d 2048,
+//    f 768, 9 rows each, up: 8.8 against 9.3 with four), of 16 token rows up to 24 rows an expert (24
+//    rows each, up: 9.6 against 10.8 with 32 token rows; 64 rows each: 13.1 against 11.9);
 //  - few tokens with few such blocks: 16 weight rows a block, K shared by 8 waves that load their own
-//    token rows (1 token, f 8192: 14.8 against 23.0; 2 rows each, f 1408: 14.1 against 12.7, from 128
-//    blocks on therefore not).
+//    token rows (1 token, f 8192, down: 6.5 against 12.5; 2 rows each, f 1408: 8.8 + 8.5 against
+//    7.9 + 5.4, from 128 blocks on therefore not).
 // A gated tile holds a gate and an up row per feature: half the features a block.
 template <int GROUP, int ACT>
 hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
@@ -517,7 +524,7 @@ hipError_t run_quant(QArgs a, int64_t rows_ub, hipStream_t st) {
   if (mean > 48 && NT(256) * likely(64) >= (GATED ? 160 : 256))
     return launch_timed(k_quant_tiles<8, 4, 2, GROUP, ACT>,
                         dim3((unsigned)tile_grid(most(64), NT(256), a.xcds)), dim3(512), 0, st, a);
-  if (mean <= 6 && NT(128) * likely(16) >= 512)
+  if (mean <= 6 && NT(128 * F1) * likely(16) >= 512 / F1)
     return run_rows<1, 2 * F1, 4, 1, GATED ? 2 : 4, true, GROUP, ACT>(a, most(16), NT(128 * F1), st);
   if (NT(256) * likely(32) >= (GATED ? 160 : mean > 48 ? 640 : 320))
     return run_rows<2, 2, 8, 1, 3, true, GROUP, ACT>(a, most(32), NT(256), st);
