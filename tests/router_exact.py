@@ -1,0 +1,65 @@
+"""Inputs of the router's backward pass on which fp32 arithmetic makes no error,
+or hardly any, whatever the order of its sums, and the values that must come out (NumPy only).
+
+Sums of integers, or of multiples of one power of two, are exact in fp32 as long as they stay below
+2^24 of it, in every order; a product of bf16 numbers is exact, and so is a sum with nothing but
+zeros beside one term.  So a kernel that sums in fp32 gives the value itself, and one that keeps
+fewer bits anywhere does not."""
+from __future__ import annotations
+
+import numpy as np
+
+U = 2.0 ** -24  # half a step of fp32, relative
+
+
+def bf16(a):
+    """fp32 values rounded to bf16, ties to even."""
+    u = np.ascontiguousarray(a, np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7FFF + ((u >> 16) & 1)) >> 16 << 16
+    return u.astype(np.uint32).view(np.float32)
+
+
+def split(v, terms):
+    """v in that many bf16 terms, each the rounding of what the ones before it left; their sum."""
+    rest, out = np.asarray(v, np.float32), np.zeros(np.shape(v))
+    for _ in range(terms):
+        t = bf16(rest)
+        out = out + t
+        rest = (rest - t).astype(np.float32)
+    return out
+
+
+# ---------------------------------------------------------------- dW_r, db: dl alone
+def selection(T, d, E, seed):
+    """dl [T, E] with all 24 bits of fp32 and x [T, d] with one 1, -1, 2 or -0.5 a column, in distinct
+    rows where T allows it: dw[e, c] = dl[t, e] x[t, c] of the one t, exact.  Where T is below d rows
+    repeat, in columns of their own."""
+    rng = np.random.default_rng(seed)
+    dl = rng.standard_normal((T, E)).astype(np.float32)
+    rows = np.concatenate([rng.permutation(T) for _ in range(-(-d // T))])[:d]
+    x = np.zeros((T, d), np.float32)
+    x[rows, np.arange(d)] = rng.choice([1.0, -1.0, 2.0, -0.5], d)
+    dw = dl[rows].astype(np.float64).T * x[rows, np.arange(d)]
+    return dl, x, dw
+
+
+def integers(T, d, E, seed, limit=1 << 24):
+    """Integer dl and x whose sums over the tokens stay below 2^24: dw = dl^T x and db = sum dl are
+    exact in fp32 in any order.  dl needs two bf16 terms (up to 2^10 where T allows it)."""
+    rng = np.random.default_rng(seed)
+    top = max(1, min(1023, (limit - 1) // (2 * T)))
+    dl = rng.integers(-top, top + 1, (T, E)).astype(np.float32)
+    x = rng.integers(-2, 3, (T, d)).astype(np.float32)
+    return dl, x, dl.astype(np.float64).T @ x, dl.sum(axis=0, dtype=np.float64)
+
+
+def dx_integers(T, d, E, seed):
+    """dl integers of 15 bits (two bf16 terms), W_r of 0, 1 and -1 with at most 255 terms a sum, and an
+    addend that takes the leading bits of dl W_r away: the sums are integers below 2^24, exact in
+    fp32, and dx, their rounding, shows dl's last bits."""
+    rng = np.random.default_rng(seed)
+    dl = rng.integers(-(1 << 15) + 1, 1 << 15, (T, E)).astype(np.float32)
+    w = rng.integers(-1, 2, (E, d)).astype(np.float32)
+    sums = dl.astype(np.float64) @ w
+    add = -bf16(sums.astype(np.float32))
+    return dl, w, add, sums + add
