@@ -1,4 +1,4 @@
-"""Inputs of the router's backward pass on which fp32 arithmetic makes no error,
+"""Inputs of the balance loss and the router's backward pass on which fp32 arithmetic makes no error,
 or hardly any, whatever the order of its sums, and the values that must come out (NumPy only).
 
 Sums of integers, or of multiples of one power of two, are exact in fp32 as long as they stay below
@@ -63,3 +63,62 @@ def dx_integers(T, d, E, seed):
     sums = dl.astype(np.float64) @ w
     add = -bf16(sums.astype(np.float32))
     return dl, w, add, sums + add
+
+
+# ---------------------------------------------------------------- balance loss
+def balance_subsets(T, E, k, seed, masked):
+    """Rows with one value (any, e.g. 3.25) on 2^j experts and -inf on the rest: probabilities 2^-j
+    or 0, exact, and so their sums over tokens and their products with counts (multiples of 1/256
+    below 2^16 of them).  ids: the row's first k experts of a random order, any of the E."""
+    rng = np.random.default_rng(seed)
+    order = np.argsort(rng.random((T, E)), axis=1)
+    most = int(np.log2(E))
+    j = rng.integers(0, most + 1, T)
+    p = np.zeros((T, E))
+    for t in range(T):
+        p[t, order[t, :1 << j[t]]] = 0.5 ** j[t]
+    value = rng.integers(-40, 41, (T, 1)) / 4.0
+    logits = np.where(p > 0, value, -np.inf).astype(np.float32)
+    # experts of a skewed preference, so that the counts differ
+    score = rng.random((T, E)) + np.linspace(0, 1.5, E)
+    ids = np.argsort(-score, axis=1)[:, :k].astype(np.int32)
+    mask = (rng.random(T) < 0.8).astype(np.uint8) if masked else None
+    return logits, ids, mask, p
+
+
+def balance_values(p, ids, mask, coef, grad_scale):
+    """loss, counts, probs, dlogits of probabilities p, in 64 bits."""
+    T, E = p.shape
+    k = ids.shape[1]
+    keep = np.ones(T, bool) if mask is None else mask != 0
+    n = int(keep.sum())
+    c = np.bincount(ids[keep].ravel(), minlength=E)
+    grad = np.zeros((T, E))
+    if n == 0:
+        return 0.0, c, np.zeros(E), grad
+    above = (c - c.min()).astype(np.float64)
+    norm = coef * E / (float(n) * k) / n
+    pk = p[keep]
+    grad[keep] = grad_scale * norm * pk * (above - (pk @ above)[:, None])
+    return norm * float(c @ pk.sum(0)), c, pk.sum(0) / n, grad
+
+
+# |error| of what comes out, relative: the loss and the mean probabilities are evaluated in 64 bits
+# from exact sums and rounded to fp32 once (U, and a little for the evaluation); the gradient's
+# factor is rounded to fp32, its two products are (3 U)
+LOSS_REL, PROBS_REL, GRAD_REL = 1.001 * U, 1.001 * U, 3.001 * U
+
+
+def balance_faults(p, ids, mask, coef, grad_scale, got):
+    """Names of the outputs that are off by more than the bounds."""
+    loss, c, probs, grad = balance_values(p, ids, mask, coef, grad_scale)
+    bad = []
+    if not np.array_equal(got["counts"], c):
+        bad.append("counts")
+    if not abs(got["loss"] - loss) <= LOSS_REL * abs(loss):
+        bad.append("loss")
+    if not np.all(np.abs(got["probs"] - probs) <= PROBS_REL * probs):
+        bad.append("probs")
+    if not np.all(np.abs(got["dlogits"] - grad) <= GRAD_REL * np.abs(grad)):
+        bad.append("dlogits")
+    return bad

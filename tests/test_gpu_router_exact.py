@@ -1,4 +1,4 @@
-"""moe_route_backward on inputs where fp32 sums make no error (router_exact): the
+"""moe_balance_loss and moe_route_backward on inputs where fp32 sums make no error (router_exact): the
 outputs are the values themselves or their one rounding, for every kernel and length."""
 from __future__ import annotations
 
@@ -21,6 +21,9 @@ BACKWARD = [(1, 64, 1), (2, 128, 8), (3, 8, 3), (33, 72, 16), (130, 520, 17), (2
             (9000, 2048, 40), (20000, 2048, 64), (33000, 128, 12)]
 DX = [(1, 64, 1), (2, 128, 8), (33, 72, 16), (130, 520, 17), (257, 136, 40), (500, 1032, 64),
       (300, 72, 130), (200, 64, 250), (5000, 256, 8), (9000, 1032, 5)]
+BALANCE = [(1, 1, 1), (1, 2, 1), (5, 3, 2), (64, 8, 2), (700, 12, 3), (1023, 16, 1), (515, 32, 6),
+           (4097, 64, 6), (1000, 65, 4), (2049, 100, 8), (777, 130, 8), (3000, 256, 8), (9000, 8, 2),
+           (20000, 60, 4)]
 
 
 def say(*a):
@@ -90,3 +93,16 @@ def test_dx_is_one_rounding(T, d, E, bf16):
                            dlogits=dev(dl), dx_add=dev(add, dt))
     want = X.bf16(dx.astype(np.float32)).astype(np.float64) if bf16 else dx
     assert np.array_equal(host(got["dx"]), want)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,E,k", BALANCE)
+def test_balance_of_exact_probabilities(T, E, k, masked):
+    say(f"[balance, exact probabilities] T={T} E={E} k={k} masked={masked}")
+    logits, ids, mask, p = X.balance_subsets(T, E, k, T + E, masked)
+    coef, scale = 0.3125, -1.5
+    got = L.balance_loss(dev(logits), dev(ids), coef=coef, grad_scale=scale,
+                         token_mask=None if mask is None else dev(mask))
+    got = dict(loss=float(got["loss"]), counts=host(got["counts"]), probs=host(got["probs"]),
+               dlogits=host(got["dlogits"]))
+    assert X.balance_faults(p, ids, mask, coef, scale, got) == []

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import router_exact as X
-from test_gpu_router_exact import BACKWARD, DX
+from test_gpu_router_exact import BALANCE, BACKWARD, DX
 
 
 @pytest.mark.parametrize("T,d,E", BACKWARD)
@@ -30,3 +30,25 @@ def test_two_terms_give_dx_and_one_does_not(T, d, E):
     for terms, right in ((2, True), (1, False)):
         got = X.bf16((X.split(dl, terms) @ w + add).astype(np.float32))
         assert np.array_equal(got, X.bf16(dx.astype(np.float32))) == right, terms
+
+
+@pytest.mark.parametrize("T,E,k", BALANCE)
+def test_balance_values_tell_fewer_bits(T, E, k):
+    logits, ids, mask, p = X.balance_subsets(T, E, k, T + E, True)
+    if not mask.any():
+        mask[0] = 1
+    coef, scale = 0.3125, -1.5
+    loss, c, probs, grad = X.balance_values(p, ids, mask, coef, scale)
+    f32 = lambda a: np.asarray(a, np.float32).astype(np.float64)
+    right = dict(loss=float(f32(loss)), counts=c, probs=f32(probs), dlogits=f32(grad))
+    assert X.balance_faults(p, ids, mask, coef, scale, right) == []
+    less = lambda a: X.bf16(f32(a).astype(np.float32)).astype(np.float64).reshape(np.shape(a))
+    step = lambda a: f32(a) * (1 + 4 * X.U)  # two whole steps of fp32
+    for wrong in (less, step):
+        for name in ("loss", "probs", "dlogits"):
+            bad = dict(right, **{name: wrong(right[name])})
+            same = np.array_equal(bad[name], right[name])  # zeros, or few bits to begin with
+            assert X.balance_faults(p, ids, mask, coef, scale, bad) == ([] if same else [name])
+            assert not same or wrong is less or not np.any(right[name])
+    bad = dict(right, counts=c + (np.arange(E) == 0))
+    assert X.balance_faults(p, ids, mask, coef, scale, bad) == ["counts"]
