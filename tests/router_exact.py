@@ -122,3 +122,41 @@ def balance_faults(p, ids, mask, coef, grad_scale, got):
     if not np.all(np.abs(got["dlogits"] - grad) <= GRAD_REL * np.abs(grad)):
         bad.append("dlogits")
     return bad
+
+
+# ---------------------------------------------------------------- slope of the loss
+def directional_faults(x, w, ids, counts, grad_w, coef):
+    """Whether grad_w [E, d] is the gradient of the balance loss in W_r, the choices and counts held:
+    its slope along D = grad / |grad| of the analytic gradient against the central difference of the
+    loss, both in 64 bits.  Returns the difference, its bound and the slope.
+
+    The loss is the mean over tokens of E_p[a] with a_e = coef E c_e / (n k) and p the softmax of z =
+    x W^T.  Along D z moves by u_t = x_t D^T.  The third derivative of E_p[a] is the joint cumulant
+    of (a, u, u, u): E[a u u u] - 3 E[a u] E[u u] of the centred values, at most 4 A R_t^3 with A
+    and R_t the ranges of a and u_t over the experts; the difference is off by h^2 / 6 of its mean,
+    and by the loss's rounding, (E + 20) 2^-53 |loss| at either end, over h.  The gradient in fp32: a
+    relative 2^-16 of the slope's terms is 256 half steps, far above the (E + 60) U that the softmax,
+    the gradient's products and the fp32 sums over some hundred tokens come to."""
+    T, E = x.shape[0], w.shape[0]
+    k = ids.shape[1]
+    a = coef * E * counts / (float(T) * k)
+
+    def loss(wt):
+        z = x @ wt.T
+        p = np.exp(z - z.max(axis=1, keepdims=True))
+        p /= p.sum(axis=1, keepdims=True)
+        return float((p @ a).mean()), p
+
+    value, p = loss(w)
+    dl = p * (a - (p @ a)[:, None]) / T
+    D = dl.T @ x
+    D /= np.linalg.norm(D)
+    h = 2.0 ** -11
+    diff = (loss(w + h * D)[0] - loss(w - h * D)[0]) / (2 * h)
+    slope = float((grad_w * D).sum())
+    u = x @ D.T
+    R = u.max(axis=1) - u.min(axis=1)
+    bound = h * h / 6 * float((4 * (a.max() - a.min()) * R ** 3).mean())
+    bound += (E + 20) * 2.0 ** -53 * abs(value) / h
+    bound += 2.0 ** -16 * float((np.abs(dl).T @ np.abs(x) * np.abs(D)).sum())
+    return abs(diff - slope), bound, slope

@@ -1,5 +1,6 @@
 """moe_balance_loss and moe_route_backward on inputs where fp32 sums make no error (router_exact): the
-outputs are the values themselves or their one rounding, for every kernel and length."""
+outputs are the values themselves or their one rounding, for every kernel and length; and the balance
+loss's gradient in W_r, end to end, against the difference of the loss along it."""
 from __future__ import annotations
 
 import sys
@@ -106,3 +107,39 @@ def test_balance_of_exact_probabilities(T, E, k, masked):
     got = dict(loss=float(got["loss"]), counts=host(got["counts"]), probs=host(got["probs"]),
                dlogits=host(got["dlogits"]))
     assert X.balance_faults(p, ids, mask, coef, scale, got) == []
+
+
+def slope_case():
+    """x, W_r, the choices and coef of a router whose experts are far from evenly used."""
+    rng = np.random.default_rng(9)
+    T, d, E, k = 256, 64, 8, 2
+    x = rng.standard_normal((T, d)).astype(np.float32).astype(np.float64)
+    x[:, 0] = 1.0  # a common part, on which the experts' preferences differ
+    w = (rng.standard_normal((E, d)) / 8).astype(np.float32)
+    w[:, 0] = np.linspace(-1, 1, E).astype(np.float32)
+    w = w.astype(np.float64)
+    ids = np.argsort(-(x @ w.T), axis=1, kind="stable")[:, :k].astype(np.int32)
+    return x, w, ids, 1.0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradient_is_the_slope_of_the_loss(bf16):
+    """moe_route, moe_balance_loss and moe_route_backward: the gradient in W_r against the difference
+    of the loss along it."""
+    x, w, _, coef = slope_case()
+    if bf16:
+        x, w = (X.bf16(a.astype(np.float32)).astype(np.float64) for a in (x, w))
+    (T, d), E, k = x.shape, w.shape[0], 2
+    dt = torch.bfloat16 if bf16 else torch.float32
+    xd, wd = dev(x, dt), dev(w, dt)
+    shape = B.make_shape(T, d, 8, E, k, 0, B.MOE_BF16 if bf16 else B.MOE_F32)
+    ws = torch.empty(max(B.workspace_bytes(shape), 256), dtype=torch.uint8, device=DEV)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    gates, logits = torch.empty(T, k, device=DEV), torch.empty(T, E, device=DEV)
+    B.moe_route(shape, xd, wd, None, ids, gates, logits, ws)
+    bal = L.balance_loss(logits, ids, coef=coef)
+    got = L.route_backward(xd, wd, logits, ids, dlogits=bal["dlogits"])
+    off, bound, slope = X.directional_faults(x, w, ids.cpu().numpy(), host(bal["counts"]),
+                                             host(got["dw_router"]), coef)
+    say(f"[slope] off {off:.2e} bound {bound:.2e} slope {slope:.4f}")
+    assert off <= bound

@@ -1,10 +1,10 @@
 """The exact checks of the router's operators tell right from wrong (CPU): evaluations in the documented
-precision pass, and the same with fewer bf16 terms, or fewer bits in a sum, do not."""
+precision pass, and the same with fewer bf16 terms, fewer bits in a sum or a wrong gradient do not."""
 import numpy as np
 import pytest
 
 import router_exact as X
-from test_gpu_router_exact import BALANCE, BACKWARD, DX
+from test_gpu_router_exact import BALANCE, BACKWARD, DX, slope_case
 
 
 @pytest.mark.parametrize("T,d,E", BACKWARD)
@@ -52,3 +52,23 @@ def test_balance_values_tell_fewer_bits(T, E, k):
             assert not same or wrong is less or not np.any(right[name])
     bad = dict(right, counts=c + (np.arange(E) == 0))
     assert X.balance_faults(p, ids, mask, coef, scale, bad) == ["counts"]
+
+
+def test_the_slope_tells_a_wrong_gradient():
+    x, w, ids, coef = slope_case()
+    T, E = len(x), len(w)
+    counts = np.bincount(ids.ravel(), minlength=E).astype(np.float64)
+    z = x @ w.T
+    p = np.exp(z - z.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    a = coef * E * counts / (float(T) * ids.shape[1])
+    dl = p * (a - (p @ a)[:, None]) / T
+    right = dl.T @ x
+    f32 = right.astype(np.float32).astype(np.float64)
+    off, bound, slope = X.directional_faults(x, w, ids, counts, f32, coef)
+    assert off <= bound and bound <= 2e-3 * slope, (off, bound, slope)
+    no_dot = (p * a / T).T @ x            # without the softmax's coupling
+    half = (dl * (np.arange(E) % 2)).T @ x  # half of the experts left out
+    for wrong in (-f32, 2 * f32, 1.005 * f32, 0 * f32, no_dot, half, f32[::-1], f32[:, ::-1]):
+        off, bound, _ = X.directional_faults(x, w, ids, counts, wrong, coef)
+        assert off > bound
