@@ -216,8 +216,8 @@ __device__ __forceinline__ void store_tile(const QArgs& a, const f32x4_t (&acc)[
 // two LDS buffers one step ahead, one barrier a step; otherwise (one or two tokens, where the
 // barriers cost more than the loads) every wave loads its own.
 //
-// Bound: the weight stream.  E 8, d 2048, f 8192, 64 tokens, group 32 (75 MB a product): 18.4 us
-// up, 22.9 us down, 4.1 and 3.3 TB/s; loading the same codes without products or token rows: 16.8
+// Bound: the weight stream.  E 8, d 2048, f 8192, 64 tokens, group 32 (75 MB a product): 17.9 us
+// up, 23.4 us down, 4.2 and 3.2 TB/s; loading the same codes without products or token rows: 16.8
 // and 18.3 us, and 2.3 us of it are an empty launch.  Column blocks outermost in the storage (runs of
 // 8 KiB a block of waves) instead of rows outermost: 24.2 -> 20.0 us up, 26.3 -> 22.2 us down.
 template <int RT, int FT, int WF, int WK, int D, bool STAGED, int GROUP, int ACT>
@@ -363,8 +363,8 @@ __global__ __launch_bounds__(64 * WF * WK) void k_quant_rows(QArgs a) {
 //
 // Bound: the matrix instructions and their interleaved conversions and scale products (4 fp32
 // products for every CG / 32 matrix instructions), then the latency of the token rows.  E 8, d 2048,
-// f 8192, 4096 tokens, top-2: group 64 and 128 296 us up and 280 us down, 929 and 981 TFLOP/s (on a
-// slower card 316 and 298); group 32 334 and 328 us.  The loads without the products: about 170 us.
+// f 8192, 4096 tokens, top-2: group 128 306 us up and 284 us down, 898 and 968 TFLOP/s (on a
+// slower card 317 and 297); group 32 337 and 329 us.  The loads without the products: about 170 us.
 template <int WF, int RT, int FT, int GROUP, int ACT>
 __global__ __launch_bounds__(64 * WF) void k_quant_tiles(QArgs a) {
   constexpr bool GATED = ACT == kQGated;

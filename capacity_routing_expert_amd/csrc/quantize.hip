@@ -14,8 +14,11 @@
 // waves of a workgroup, on neighbouring rows of the same columns, one run of memory.  Scales:
 // [E][ceil(cols / 128)][rows][128 / group], the ones past cols zero.
 //
-// Bound: HBM (2 or 4 bytes in, 0.5 + 2 / group out, a weight).  A wave takes one block; a lane
-// 16 columns of a row, so a group is 2, 4 or 8 lanes.
+// Bound: HBM (2 or 4 bytes in, 0.5 + 2 / group out, a weight) and, short of it, the division.  A wave
+// takes one block; a lane 16 columns of a row, so a group is 2, 4 or 8 lanes.  8 x 8192 x 2048 bf16
+// weights, group 32 (268 MB in, 75 MB out): 127 - 145 us, 2.4 - 2.7 TB/s; with a product by the scale's
+// reciprocal instead of the division 113 (not the same codes), with stores of whole runs no less.
+// Reading back (75 MB in, 537 MB out): 328 us, 1.9 TB/s, eight 4-byte stores a lane, as w lies on 4 bytes.
 #include "moe_internal.h"
 
 namespace moe {

@@ -6,9 +6,9 @@
 //   dx = dx_add + dl W_r,   dW_r = dl^T x,   db = sum_t dl_t
 //
 // Bound: HBM, for the expert counts that the library takes in bf16 (x is read once for dW_r, dx
-// is written once; 4 T E d flops): T 32768, d 4096, E 8 7.4 us for dl, 101 us for dx (537 MB with
-// dx_add and dx), 69 us for dW_r (268 MB), 5.0 us for the sums over the token ranges; T 16384, d 2048,
-// E 64 8.0, 32.7, 24.3 and 4.8 us.  dl itself is E values a token, so it goes through memory
+// is written once; 4 T E d flops): T 32768, d 4096, E 8 7.4 us for dl, 104 us for dx (537 MB with
+// dx_add and dx), 71 us for dW_r (268 MB), 5.7 us for the sums over the token ranges; T 16384, d 2048,
+// E 64 7.9, 33.5, 24.1 and 4.9 us.  dl itself is E values a token, so it goes through memory
 // between the kernels: k_route_dlogits writes it once in the two layouts that the matrix
 // instructions want (experts contiguous for dx, tokens contiguous for dW_r).
 //
@@ -512,7 +512,9 @@ __global__ __launch_bounds__(256) void k_route_dw_bf16(const bf16_t* __restrict_
 // 4 n + i: rows of x, W_r and dx move in 16-byte pieces, 256 B a row.  VEC: d is a multiple of 4 and the
 // arrays lie on 16 bytes.
 // T 1970, d 4024, E 11, with dx_add: dx 13.5 us (95 MB), dW_r 12.8 us (32 MB); with a dword a lane
-// and loads behind branches 57 us for the whole pass instead of 32.
+// and loads behind branches 57 us for the whole pass instead of 32.  T 8192, d 4096, E 128, where the
+// matrix instructions (153 TFLOP/s in a large product) need 56 us each: dx 95 us, dW_r 156 us (x read
+// once for each 64 experts; 6 token ranges, on 6 of the 8 XCDs).
 template <bool VEC>
 __device__ __forceinline__ float4 load_cols(const float* row, int c, int d) {
   if constexpr (VEC) return c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0, 0, 0, 0);
