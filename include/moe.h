@@ -421,11 +421,10 @@ moe_status moe_layer_forward_batches(const moe_shape* batch_shape, int32_t n_bat
  * expert's weights once per batch, so the bytes of a weight are their time: 0.5 + 2 / group bytes
  * here against bf16's 2.  Long prompts are bound by the matrix cores, and there the conversions cost
  * time: 8 experts of d_model 2048, d_ff 8192 are ahead of packed bf16 weights up to 256 rows an
- * expert (group 32) or 1024 (group 128), and behind above (2048 rows: by 28 and 11 %).  A weight is
- * value(code) * scale: the code is a sign and one of the
- * magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; one bf16 scale serves `group` (32, 64 or 128) consecutive
- * columns of a row.  Storage of an [E, rows, cols] array (rows and cols multiples of 8), with
- * KC = ceil(cols / 128):
+ * expert (group 32) or 1024 (group 128), and behind above (2048 rows: by 28 and 11 %).
+ * A weight is value(code) * scale: the code is a sign and one of the magnitudes 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6; one bf16 scale serves `group` (32, 64 or 128) consecutive columns of a row.  Storage of an
+ * [E, rows, cols] array (rows and cols multiples of 8), with KC = ceil(cols / 128):
  *   codes  [E][KC][rows / 8] blocks of 512 bytes, 8 rows x 128 columns: column c of row r of a
  *          block is in the dword ((c % 32 / 8 * 8 + r) * 4 + c / 32), bits 4 (c % 8) and up, sign
  *          highest; columns past cols are zero
