@@ -1,0 +1,497 @@
+"""Cases of routing by scores with a selection bias and expert groups, its backward pass, the update
+of that bias, and the AdamW step: their inputs, plain forms, exact values and the work of one pass.
+
+`own` chooses what `run` does: the plain form in elementary torch operations, or the library's calls
+(`capacity_routing_expert_amd.binding`).  `exact` evaluates the definitions in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda:0"
+BLOCK = 256  # elements that share a step in the 8-bit optimiser states
+
+
+# ---------------------------------------------------------------- the cases
+def listed():
+    route = lambda name, T, d, E, k, dtype, score, G, g, top2, renorm, bias, masked: dict(
+        name=name, op="route", T=T, d=d, E=E, k=k, dtype=dtype, score=score, groups=G,
+        topk_groups=g, top2=top2, renorm=renorm, bias=bias, masked=masked)
+    back = lambda name, T, E, k, score, renorm, masked, add: dict(
+        name=name, op="route_backward", T=T, E=E, k=k, score=score, renorm=renorm, masked=masked,
+        add=add)
+    bias = lambda name, T, E, k, masked: dict(name=name, op="bias", T=T, E=E, k=k, masked=masked)
+    adamw = lambda name, tensors, n, odd, param, grad, bits, copy: dict(
+        name=name, op="adamw", tensors=tensors, n=n, odd=odd, param=param, grad=grad, bits=bits,
+        copy=copy)
+    return [
+        # one token of a serving step over the fine layer's 64 experts: latency
+        route("route_single_T1_E64", 1, 2048, 64, 6, "bf16", "softmax", 1, 1, False, True, False, False),
+        # a decode batch over many small experts in groups, kept even by the bias
+        route("route_decode_T64_E256_grouped", 64, 2048, 256, 8, "bf16", "sigmoid", 8, 4, True, True,
+              True, False),
+        # an fp32 batch with odd sizes, padded, the best expert of a group speaking for it
+        route("route_f32_T1003_d1000_E96", 1003, 1000, 96, 5, "f32", "softmax", 6, 2, False, False,
+              True, True),
+        # a training step's batch on the fine layer's router
+        route("route_fine_T16384_E64", 16384, 2048, 64, 6, "bf16", "sigmoid", 1, 1, False, True, True,
+              False),
+        # a few tokens, five experts: latency
+        back("route_bwd_T37_E5", 37, 5, 2, "sigmoid", True, False, False),
+        # the fine layer's router, its gates left as probabilities, with the balance loss's gradient
+        back("route_bwd_fine_T16384_E64", 16384, 64, 6, "softmax", False, False, True),
+        # many small experts, a padded batch with an odd number of tokens
+        back("route_bwd_padded_T32771_E256", 32771, 256, 8, "sigmoid", True, True, False),
+        # the decode layer watched for balance: one small batch
+        bias("bias_decode_T64_E8", 64, 8, 2, False),
+        # many small experts, a padded batch with an odd number of tokens
+        bias("bias_padded_T32771_E256", 32771, 256, 8, True),
+        # the routers of 32 layers with 64 experts and their biases, bf16 copies for the forward pass
+        adamw("adamw_32_routers", 64, 131072, 64, "f32", "f32", 32, True),
+        # gated experts of the flow diagram's width with odd remainders, states in 8 bits
+        adamw("adamw_8bit_gated_experts", 9, 4194304, 1001, "f32", "bf16", 8, True),
+        # the mid layer's expert weights, states in 32 bits: bound by memory
+        adamw("adamw_mid_experts", 2, 134217728, 65536, "f32", "bf16", 32, False),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("route", "route", "route_backward", "bias", "adamw"))
+    if op == "route":
+        G = rng.choice((1, 1, 2, 4, 8))
+        E = G * _log(rng, 1 if G > 1 else 2, 256 // G)
+        g = rng.randint(1, G)
+        k = rng.randint(1, min(8, g * (E // G)))
+        dtype = rng.choice(("bf16", "bf16", "f32"))
+        d = 8 * _log(rng, 8, 512) if dtype == "bf16" else _log(rng, 64, 2048)
+        T = _log(rng, 1, min(16384, (1 << 31) // (d * E)))
+        return dict(op=op, T=T, d=d, E=E, k=k, dtype=dtype, score=rng.choice(("softmax", "sigmoid")),
+                    groups=G, topk_groups=g, top2=rng.random() < 0.5, renorm=rng.random() < 0.6,
+                    bias=rng.random() < 0.6, masked=rng.random() < 0.3)
+    if op == "adamw":
+        tensors, param = _log(rng, 1, 128), rng.choice(("f32", "f32", "bf16"))
+        return dict(op=op, tensors=tensors, n=_log(rng, 256, (1 << 26) // tensors),
+                    odd=_log(rng, 1, 4096), param=param, grad=rng.choice(("f32", "bf16")),
+                    bits=rng.choice((8, 32)), copy=param == "f32" and rng.random() < 0.5)
+    E = _log(rng, 2, 256)
+    T, k, masked = _log(rng, 1, 32768), rng.randint(1, min(E, 8)), rng.random() < 0.5
+    if op == "bias":
+        return dict(op=op, T=T, E=E, k=k, masked=masked)
+    return dict(op=op, T=T, E=E, k=k, score=rng.choice(("softmax", "sigmoid")),
+                renorm=rng.random() < 0.5, masked=masked, add=rng.random() < 0.5)
+
+
+# ---------------------------------------------------------------- inputs
+def _generator(seed, salt):
+    return torch.Generator(device=DEV).manual_seed((seed * 1000003 + salt) & 0x7FFFFFFF)
+
+
+def _padding(g, T):
+    """A batch padded at its end and, here and there, inside: 1 for a real token."""
+    mask = torch.rand(T, generator=g, device=DEV) < 0.95
+    mask[T - T // 8:] = False
+    return mask.to(torch.uint8)
+
+
+def _dtype(name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _lengths(case):
+    """Elements of each tensor: odd-numbered ones are small or a little over n."""
+    n, odd = case["n"], case["odd"]
+    if case["param"] == "f32" and case["copy"] and case["bits"] == 32:
+        return [n if i % 2 == 0 else odd for i in range(case["tensors"])]  # matrices and their biases
+    return [n + odd * (i % 2) for i in range(case["tensors"])]
+
+
+def _inputs(case, seed):
+    """The tensors of one case, from the seed alone."""
+    op = case["op"]
+    g = _generator(seed, {"route": 1, "route_backward": 2, "bias": 3, "adamw": 4}[op])
+    rand = lambda *size: torch.randn(*size, generator=g, device=DEV)
+    if op == "adamw":
+        lengths = _lengths(case)
+        starts, total = [], 0
+        for n in lengths:
+            starts.append(total)
+            total += -(-n // BLOCK) * BLOCK
+        real = torch.zeros(total, dtype=torch.bool, device=DEV)
+        decay = torch.zeros(total, device=DEV)
+        for i, (a, n) in enumerate(zip(starts, lengths)):
+            real[a:a + n] = True
+            decay[a:a + n] = 0.0 if i % 4 == 1 else 0.1
+        # each tensor's gradients have a size of their own, and so have stretches within it
+        size = torch.exp(1.5 * rand(total // 64)).repeat_interleave(64) * real
+        s = dict(p=(0.02 * rand(total) * real).to(_dtype(case["param"])),
+                 g=(1e-3 * rand(total) * size).to(_dtype(case["grad"])), decay=decay,
+                 starts=starts, lengths=lengths, lr=3e-4, beta1=0.9, beta2=0.95, eps=1e-8, step=20,
+                 grad_scale=0.5)
+        m = 2e-4 * rand(total) * size
+        v = (3e-4 * size * (0.5 + torch.rand(total, generator=g, device=DEV))) ** 2
+        if case["bits"] == 32:
+            s.update(m=m, v=v)
+        else:
+            s["m"], s["m_step"] = _encode(m, 127)
+            s["v"], s["v_step"] = _encode(torch.sqrt(v), 255)
+        if case["copy"]:
+            s["copy"] = s["p"].to(torch.bfloat16)
+        return s
+    T, E, k = case["T"], case["E"], case["k"]
+    if op == "route":
+        d, dt = case["d"], _dtype(case["dtype"])
+        s = dict(x=rand(T, d).to(dt), w=(1.5 * rand(E, d) / math.sqrt(d)).to(dt), b=0.5 * rand(E),
+                 score_bias=0.1 * rand(E) if case["bias"] else None)
+        s["mask"] = _padding(g, T) if case["masked"] else None
+        return s
+    logits = rand(T, E) + rand(E)
+    ids = torch.topk(logits + 0.3 * rand(T, E), k, dim=1).indices.to(torch.int32).contiguous()
+    mask = _padding(g, T) if case["masked"] else None
+    if op == "bias":
+        return dict(ids=ids, mask=mask, score_bias=0.1 * rand(E), rate=0.001)
+    dgates = 0.02 * rand(T, k)
+    dgates[torch.rand(T, k, generator=g, device=DEV) < 0.15] = 0.0  # dropped assignments
+    return dict(logits=logits, ids=ids, mask=mask, dgates=dgates, scale=2.5,
+                add=0.001 * rand(T, E) if case["add"] else None)
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    s["case"] = case
+    if not own:
+        return s
+    from capacity_routing_expert_amd import binding as B
+    op = case["op"]
+    if op == "adamw":
+        def views(name):
+            return [s[name][a:a + n] for a, n in zip(s["starts"], s["lengths"])]
+
+        def steps(name):
+            return [s[name][a // BLOCK:(a + n + BLOCK - 1) // BLOCK]
+                    for a, n in zip(s["starts"], s["lengths"])]
+
+        quantized = case["bits"] == 8
+        s["tensors"] = B.AdamWTensors(
+            views("p"), views("g"), views("m"), views("v"),
+            m_steps=steps("m_step") if quantized else None,
+            v_steps=steps("v_step") if quantized else None,
+            copies=views("copy") if case["copy"] else None,
+            weight_decay=[0.0 if i % 4 == 1 else 0.1 for i in range(case["tensors"])])
+        if quantized:
+            s["m_out"], s["v_out"] = (torch.zeros_like(s["decay"]) for _ in range(2))
+            s["m_views"], s["v_views"] = views("m_out"), views("v_out")
+        return s
+    T, E, k = case["T"], case["E"], case["k"]
+    if op == "route":
+        dt = B.MOE_BF16 if case["dtype"] == "bf16" else B.MOE_F32
+        s["shape"] = B.make_shape(T, case["d"], 8, E, k, 0, dt)
+        s["routing"] = B.make_routing(case["score"], n_groups=case["groups"],
+                                      topk_groups=case["topk_groups"],
+                                      group_score="top2" if case["top2"] else "max",
+                                      renormalize=case["renorm"], scale=2.5)
+        s.update(ids=torch.empty(T, k, dtype=torch.int32, device=DEV),
+                 gates=torch.empty(T, k, device=DEV), logits=torch.empty(T, E, device=DEV))
+        n = B.workspace_bytes_route_scored(s["shape"])
+        s["ws"] = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
+        return s
+    s["shape"] = B.make_shape(T, 8, 8, E, k, 0, B.MOE_F32)
+    if op == "bias":
+        s["counts"] = torch.empty(E, dtype=torch.int32, device=DEV)
+        n = B.workspace_bytes_balance_bias(s["shape"])
+        s["ws"] = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
+    else:
+        s["routing"] = B.make_routing(case["score"], renormalize=case["renorm"], scale=s["scale"])
+        s["dlogits"] = torch.empty(T, E, device=DEV)
+    return s
+
+
+# ---------------------------------------------------------------- one pass
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"route": _own_route, "route_backward": _own_route_backward, "bias": _own_bias,
+                "adamw": _own_adamw}[op](state)
+    return {"route": _plain_route, "route_backward": _plain_route_backward, "bias": _plain_bias,
+            "adamw": _plain_adamw}[op](state)
+
+
+def _own_route(s):
+    from capacity_routing_expert_amd import binding as B
+    B.moe_route_scored(s["shape"], s["routing"], s["x"], s["w"], s["b"], s["score_bias"], s["ids"],
+                       s["gates"], logits=s["logits"], token_mask=s["mask"], ws=s["ws"])
+    return {"ids": s["ids"], "gates": s["gates"], "logits": s["logits"]}
+
+
+def _own_route_backward(s):
+    from capacity_routing_expert_amd import binding as B
+    B.moe_route_scored_backward(s["shape"], s["routing"], s["logits"], s["ids"], s["dgates"],
+                                s["dlogits"], dlogits_add=s["add"], token_mask=s["mask"])
+    return s["dlogits"]
+
+
+def _own_bias(s):
+    from capacity_routing_expert_amd import binding as B
+    B.moe_balance_bias(s["shape"], s["rate"], s["score_bias"], s["counts"], topk_ids=s["ids"],
+                       token_mask=s["mask"], ws=s["ws"])
+    return {"score_bias": s["score_bias"], "counts": s["counts"]}
+
+
+def _own_adamw(s):
+    from capacity_routing_expert_amd import binding as B
+    B.moe_adamw_step(s["tensors"], s["lr"], s["beta1"], s["beta2"], s["eps"], s["step"],
+                     grad_scale=s["grad_scale"])
+    out = {"p": s["p"], "m": s["m"], "v": s["v"]}
+    if "copy" in s:
+        out["copy"] = s["copy"]
+    if s["case"]["bits"] == 8:  # the values of the codes
+        B.moe_adamw_moments(s["tensors"], s["m_views"], s["v_views"])
+        out.update(m=s["m_out"], v=s["v_out"])
+    return out
+
+
+def _plain_route(s):
+    case = s["case"]
+    T, E, k, G = case["T"], case["E"], case["k"], case["groups"]
+    # 64 bits: the choice turns on the last bits of the scores
+    z = s["x"].double() @ s["w"].double().T + s["b"].double()
+    if case["score"] == "softmax":
+        p = torch.exp(z - z.amax(1, keepdim=True))
+        p = p / p.sum(1, keepdim=True)
+    else:
+        p = 1.0 / (1.0 + torch.exp(-z))
+    choose = p.float()
+    if s["score_bias"] is not None:
+        choose = choose + s["score_bias"]
+    if G > 1:
+        inside = choose.view(T, G, E // G).sort(dim=2, descending=True).values
+        group = inside[:, :, 0]
+        if case["top2"] and E // G > 1:
+            group = group + inside[:, :, 1]
+        best = torch.sort(group, dim=1, descending=True, stable=True).indices[:, :case["topk_groups"]]
+        stays = torch.zeros(T, G, dtype=torch.bool, device=DEV).scatter_(1, best, True)
+        choose = torch.where(stays.repeat_interleave(E // G, 1), choose, -math.inf)
+    ids = torch.sort(choose, dim=1, descending=True, stable=True).indices[:, :k]
+    gates = p.gather(1, ids)
+    if case["renorm"]:
+        gates = gates / gates.sum(1, keepdim=True)
+    gates, logits, ids = (2.5 * gates).float(), z.float(), ids.to(torch.int32)
+    if s["mask"] is not None:
+        there = (s["mask"] > 0).unsqueeze(1)
+        ids = torch.where(there, ids, -1)
+        gates, logits = gates * there, logits * there
+    return {"ids": ids, "gates": gates, "logits": logits}
+
+
+def _plain_route_backward(s):
+    case = s["case"]
+    ids = s["ids"].long()
+    if case["score"] == "softmax":
+        p = torch.exp(s["logits"] - s["logits"].amax(1, keepdim=True))
+        p = p / p.sum(1, keepdim=True)
+    else:
+        p = 1.0 / (1.0 + torch.exp(-s["logits"]))
+    h = s["scale"] * s["dgates"]
+    if case["renorm"]:
+        chosen = p.gather(1, ids)
+        total = chosen.sum(1, keepdim=True)
+        h = (h - (h * chosen).sum(1, keepdim=True) / total) / total
+    up = torch.zeros_like(p).scatter_add_(1, ids, h)
+    if case["score"] == "sigmoid":
+        dl = up * p * (1.0 - p)
+    elif case["renorm"]:
+        dl = up * p  # sum_j p_j up_j is zero
+    else:
+        dl = p * (up - (p * up).sum(1, keepdim=True))
+    if s["add"] is not None:
+        dl = dl + s["add"]
+    if s["mask"] is not None:
+        dl = dl * s["mask"].float().unsqueeze(1)
+    return dl
+
+
+def _plain_bias(s):
+    E = s["case"]["E"]
+    ids = s["ids"].long()
+    one = torch.ones_like(ids) if s["mask"] is None else s["mask"].long().unsqueeze(1).expand_as(ids)
+    counts = torch.zeros(E, dtype=torch.int64, device=DEV).scatter_add_(0, ids.flatten(),
+                                                                        one.reshape(-1))
+    s["score_bias"] += s["rate"] * torch.sign(counts.sum() - E * counts).float()
+    return {"score_bias": s["score_bias"], "counts": counts.to(torch.int32)}
+
+
+def _encode(x, top):
+    """Codes (int8 or uint8) of x in blocks of 256 and the blocks' steps: |x| is near code^2 step."""
+    v = x.view(-1, BLOCK)
+    # a divisor on the device: torch takes a number's reciprocal, which rounds twice
+    step = v.abs().amax(1, keepdim=True) / torch.full((1, 1), float(top * top), device=DEV)
+    y = torch.where(step > 0, v.abs() / step, torch.zeros_like(v))
+    code = torch.floor(torch.sqrt(y) + 0.5).clamp(max=top)
+    if top == 255:  # a root that is not zero stays so: it is divided by
+        code = torch.where(v > 0, code.clamp(min=1.0), code)
+        return code.to(torch.uint8).view(-1), step.view(-1)
+    return (code * torch.sign(v)).to(torch.int8).view(-1), step.view(-1)
+
+
+def _decode(code, step):
+    c = code.float().view(-1, BLOCK)
+    return (c * c.abs() * step.view(-1, 1)).view(-1)
+
+
+def _plain_adamw(s):
+    case = s["case"]
+    quantized = case["bits"] == 8
+    m, v = s["m"], s["v"]
+    if quantized:
+        m, v = _decode(m, s["m_step"]), _decode(v, s["v_step"])
+        v = v * v
+    g = s["g"].float() * s["grad_scale"]
+    # the betas are 32-bit numbers, and each operation below is rounded
+    b1, b2 = torch.tensor([s["beta1"], s["beta2"]], dtype=torch.float32).tolist()
+    m = m * b1 + g * (1.0 - b1)
+    v = v * b2 + (g * g) * (1.0 - b2)
+    r = torch.sqrt(v)
+    rate = s["lr"] / (1.0 - b1 ** s["step"])
+    root = math.sqrt(1.0 - b2 ** s["step"])
+    p = s["p"].float()
+    p = p * (1.0 - s["lr"] * s["decay"]) - rate * m / (r / root + s["eps"])
+    s["p"].copy_(p)
+    out = {"p": s["p"]}
+    if case["copy"]:
+        s["copy"].copy_(p)
+        out["copy"] = s["copy"]
+    if not quantized:
+        s["m"].copy_(m)
+        s["v"].copy_(v)
+        return {**out, "m": s["m"], "v": s["v"]}
+    for name, x, top in (("m", m, 127), ("v", r, 255)):
+        code, step = _encode(x, top)
+        s[name].copy_(code)
+        s[name + "_step"].copy_(step)
+        out[name] = _decode(code, step)
+    out["v"] = out["v"] * out["v"]
+    return out
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+def exact(case, seed):
+    s = _inputs(case, seed)
+    op = case["op"]
+    if op == "adamw":
+        return _exact_adamw(case, s)
+    T, E, k = case["T"], case["E"], case["k"]
+    keep = torch.ones(T, dtype=torch.bool, device=DEV) if s["mask"] is None else s["mask"] > 0
+    if op == "bias":
+        counts = torch.bincount(s["ids"][keep].flatten().long(), minlength=E)
+        mean = counts.double().mean()
+        return {"score_bias": s["score_bias"].double() + s["rate"] * torch.sign(mean - counts),
+                "counts": counts.to(torch.int32)}
+    if op == "route":
+        z = torch.empty(T, E, dtype=torch.float64, device=DEV)
+        for t in range(0, T, 4096):
+            z[t:t + 4096] = torch.mm(s["x"][t:t + 4096].double(), s["w"].double().t().contiguous())
+        z += s["b"].double()
+        p = torch.softmax(z, 1) if case["score"] == "softmax" else torch.sigmoid(z)
+        a = p.float() + (s["score_bias"] if s["score_bias"] is not None else 0.0)
+        G = case["groups"]
+        if G > 1:
+            parts = a.reshape(T, G, -1)
+            top = torch.topk(parts, 2 if case["top2"] and E > G else 1, dim=2).values.sum(2)
+            # the rank of a group: those that are better, or as good and before it
+            better = (top.unsqueeze(1) > top.unsqueeze(2)).sum(2)
+            before = torch.ones(G, G, device=DEV).tril(-1).bool()
+            better += ((top.unsqueeze(1) == top.unsqueeze(2)) & before).sum(2)
+            a = a.masked_fill((better >= case["topk_groups"]).repeat_interleave(E // G, 1), -math.inf)
+        order = torch.argsort(-a, dim=1, stable=True)[:, :k]
+        gates = torch.take_along_dim(p, order, 1)
+        if case["renorm"]:
+            gates = gates / gates.sum(1, keepdim=True)
+        ids = order.to(torch.int32)
+        gates, z = 2.5 * gates, z.clone()
+        ids[~keep], gates[~keep], z[~keep] = -1, 0.0, 0.0
+        return {"ids": ids, "gates": gates, "logits": z}
+    z = s["logits"].double()
+    p = torch.softmax(z, 1) if case["score"] == "softmax" else torch.sigmoid(z)
+    idx, dg = s["ids"].long(), s["scale"] * s["dgates"].double()
+    chosen = torch.take_along_dim(p, idx, 1)
+    dl = torch.zeros_like(p)
+    if case["renorm"]:
+        share = chosen / chosen.sum(1, keepdim=True)
+        part = share * (dg - (share * dg).sum(1, keepdim=True))
+        if case["score"] == "sigmoid":
+            part = part * torch.sigmoid(-torch.take_along_dim(z, idx, 1))
+        for c in range(k):
+            dl.scatter_add_(1, idx[:, c:c + 1], part[:, c:c + 1])
+    elif case["score"] == "sigmoid":
+        for c in range(k):
+            dl.scatter_add_(1, idx[:, c:c + 1], dg[:, c:c + 1])
+        dl *= p * torch.sigmoid(-z)
+    else:
+        for c in range(k):
+            dl.scatter_add_(1, idx[:, c:c + 1], dg[:, c:c + 1])
+        dl = p * dl - p * (chosen * dg).sum(1, keepdim=True)
+    if s["add"] is not None:
+        dl = dl + s["add"].double()
+    dl[~keep] = 0.0
+    return dl
+
+
+def _exact_adamw(case, s):
+    """In 64 bits; what the states hold is rounded where the states' definition rounds to 32 bits."""
+    f = lambda t: t.float().double()
+    m, v = s["m"].double(), s["v"].double()
+    if case["bits"] == 8:
+        m = f(torch.sign(m) * m.square() * s["m_step"].double().repeat_interleave(BLOCK))
+        v = f(f(v.square() * s["v_step"].double().repeat_interleave(BLOCK)).square())
+    b1, b2 = torch.tensor([s["beta1"], s["beta2"]], dtype=torch.float32).double().tolist()
+    c1, c2 = torch.tensor([1.0 - b1, 1.0 - b2], dtype=torch.float32).double().tolist()
+    g = f(s["g"].double() * s["grad_scale"])
+    m = f(f(b1 * m) + f(c1 * g))
+    v = f(f(b2 * v) + f(c2 * f(g.square())))
+    t = s["step"]
+    m_hat, v_hat = m / (1.0 - b1 ** t), v / (1.0 - b2 ** t)
+    p = s["p"].double()
+    p = p - s["lr"] * s["decay"].double() * p - s["lr"] * m_hat / (v_hat.sqrt() + s["eps"])
+    del m_hat, v_hat, g
+    out = {"p": p}
+    if case["copy"]:
+        out["copy"] = p
+    if case["bits"] == 32:
+        return {**out, "m": m, "v": v}
+    for name, x, top in (("m", m, 127), ("v", f(v.sqrt()), 255)):
+        rows = x.reshape(-1, BLOCK)
+        step = f(rows.abs().max(1, keepdim=True).values / top ** 2)
+        ratio = f(rows.abs() / step).nan_to_num(0.0)
+        code = torch.floor(f(f(ratio.sqrt()) + 0.5)).clamp(max=top)
+        if name == "v":
+            code = torch.maximum(code, (rows > 0).double())
+        x = f(torch.copysign(code.square(), rows) * step)
+        out[name] = (f(x.square()) if name == "v" else x).reshape(-1)
+    return out
+
+
+# ---------------------------------------------------------------- the work of one pass
+def work(case):
+    op = case["op"]
+    size = lambda name: 2 if name == "bf16" else 4
+    if op == "adamw":
+        n = sum(_lengths(case))
+        state = 16 if case["bits"] == 32 else 4 + 16.0 / BLOCK + 8  # the 8-bit moments' values too
+        return {"bytes": int(n * (2 * size(case["param"]) + size(case["grad"]) + state +
+                                  (2 if case["copy"] else 0))), "flops": 20 * n}
+    T, E, k = case["T"], case["E"], case["k"]
+    masked = T if case["masked"] else 0
+    if op == "route":
+        return {"bytes": (T + E) * case["d"] * size(case["dtype"]) + 4 * T * E + 8 * T * k + masked +
+                4 * E * (2 if case["bias"] else 1), "flops": 2 * T * E * case["d"] + 10 * T * E}
+    if op == "bias":
+        return {"bytes": 4 * T * k + masked + 12 * E, "flops": T * k}
+    # only a softmax that is left as it is takes more logits than the chosen ones
+    reads = 4 * T * (E if case["score"] == "softmax" and not case["renorm"] else k)
+    return {"bytes": reads + (8 if case["add"] else 4) * T * E + 8 * T * k + masked,
+            "flops": 10 * T * k + T * E}
