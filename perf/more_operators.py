@@ -1,5 +1,6 @@
-"""Cases of routing by scores with a selection bias and expert groups, its backward pass, the update
-of that bias, and the AdamW step: their inputs, plain forms, exact values and the work of one pass.
+"""Cases of routing by scores with a selection bias and expert groups, the update of that bias, the
+backward passes of the combine and of the gates, and the AdamW step: their inputs, plain forms, exact
+values and the work of one pass.
 
 `own` chooses what `run` does: the plain form in elementary torch operations, or the library's calls
 (`capacity_routing_expert_amd.binding`).  `exact` evaluates the definitions in 64 bits.
@@ -26,11 +27,11 @@ def listed():
     adamw = lambda name, tensors, n, odd, param, grad, bits, copy: dict(
         name=name, op="adamw", tensors=tensors, n=n, odd=odd, param=param, grad=grad, bits=bits,
         copy=copy)
+    comb = lambda name, T, d, E, k, dtype, rows: dict(
+        name=name, op="combine_backward", T=T, d=d, E=E, k=k, dtype=dtype, rows=rows)
     return [
-        # one token of a serving step over the fine layer's 64 experts: latency
-        route("route_single_T1_E64", 1, 2048, 64, 6, "bf16", "softmax", 1, 1, False, True, False, False),
-        # a decode batch over many small experts in groups, kept even by the bias
-        route("route_decode_T64_E256_grouped", 64, 2048, 256, 8, "bf16", "sigmoid", 8, 4, True, True,
+        # one token of a serving step over many small experts in groups, kept even by the bias: latency
+        route("route_single_T1_E256_grouped", 1, 2048, 256, 8, "bf16", "sigmoid", 8, 4, True, True,
               True, False),
         # an fp32 batch with odd sizes, padded, the best expert of a group speaking for it
         route("route_f32_T1003_d1000_E96", 1003, 1000, 96, 5, "f32", "softmax", 6, 2, False, False,
@@ -38,12 +39,15 @@ def listed():
         # a training step's batch on the fine layer's router
         route("route_fine_T16384_E64", 16384, 2048, 64, 6, "bf16", "sigmoid", 1, 1, False, True, True,
               False),
+        # the decode layer's batch: gradients on its gates alone, the experts being frozen
+        comb("combine_bwd_decode_T64_d2048", 64, 2048, 8, 2, "bf16", False),
+        # the fine layer's batch, gradients on the gates and on the expert rows
+        comb("combine_bwd_fine_T16384_d2048", 16384, 2048, 64, 6, "bf16", True),
         # a few tokens, five experts: latency
         back("route_bwd_T37_E5", 37, 5, 2, "sigmoid", True, False, False),
-        # the fine layer's router, its gates left as probabilities, with the balance loss's gradient
-        back("route_bwd_fine_T16384_E64", 16384, 64, 6, "softmax", False, False, True),
-        # many small experts, a padded batch with an odd number of tokens
-        back("route_bwd_padded_T32771_E256", 32771, 256, 8, "sigmoid", True, True, False),
+        # many small experts, a padded batch with an odd number of tokens, gates left as
+        # probabilities, with the balance loss's gradient
+        back("route_bwd_padded_T32771_E256", 32771, 256, 8, "softmax", False, True, True),
         # the decode layer watched for balance: one small batch
         bias("bias_decode_T64_E8", 64, 8, 2, False),
         # many small experts, a padded batch with an odd number of tokens
@@ -62,7 +66,7 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(("route", "route", "route_backward", "bias", "adamw"))
+    op = rng.choice(("route", "route", "combine_backward", "route_backward", "bias", "adamw"))
     if op == "route":
         G = rng.choice((1, 1, 2, 4, 8))
         E = G * _log(rng, 1 if G > 1 else 2, 256 // G)
@@ -81,6 +85,11 @@ def draw(rng):
                     bits=rng.choice((8, 32)), copy=param == "f32" and rng.random() < 0.5)
     E = _log(rng, 2, 256)
     T, k, masked = _log(rng, 1, 32768), rng.randint(1, min(E, 8)), rng.random() < 0.5
+    if op == "combine_backward":
+        dtype = rng.choice(("bf16", "bf16", "f32"))
+        d = 8 * _log(rng, 8, 512) if dtype == "bf16" else _log(rng, 64, 4096)
+        return dict(op=op, T=min(T, (1 << 27) // (d * k)), d=d, E=E, k=k, dtype=dtype,
+                    rows=rng.random() < 0.5)
     if op == "bias":
         return dict(op=op, T=T, E=E, k=k, masked=masked)
     return dict(op=op, T=T, E=E, k=k, score=rng.choice(("softmax", "sigmoid")),
@@ -114,7 +123,8 @@ def _lengths(case):
 def _inputs(case, seed):
     """The tensors of one case, from the seed alone."""
     op = case["op"]
-    g = _generator(seed, {"route": 1, "route_backward": 2, "bias": 3, "adamw": 4}[op])
+    g = _generator(seed, {"route": 1, "route_backward": 2, "bias": 3, "adamw": 4,
+                         "combine_backward": 5}[op])
     rand = lambda *size: torch.randn(*size, generator=g, device=DEV)
     if op == "adamw":
         lengths = _lengths(case)
@@ -150,6 +160,26 @@ def _inputs(case, seed):
                  score_bias=0.1 * rand(E) if case["bias"] else None)
         s["mask"] = _padding(g, T) if case["masked"] else None
         return s
+    if op == "combine_backward":
+        d, dt = case["d"], _dtype(case["dtype"])
+        # slots by expert, at most 1.25 times the even share each: the rest has none
+        ids = torch.topk(rand(T, E) + 0.5 * rand(E), k, dim=1).indices.flatten()
+        order = torch.sort(ids, stable=True).indices
+        counts = torch.bincount(ids, minlength=E)
+        begin = torch.cumsum(counts, 0) - counts
+        capacity = max(1, 5 * T * k // (4 * E))
+        rank = torch.empty_like(ids)
+        rank[order] = torch.arange(T * k, device=DEV) - begin[ids[order]]
+        kept = counts.clamp(max=capacity)
+        slots = (torch.cumsum(kept, 0) - kept)[ids] + rank
+        slots = torch.where(rank < capacity, slots, -1).to(torch.int32).view(T, k)
+        n = min(T * k, E * capacity)
+        y = torch.empty(n, d, dtype=dt, device=DEV)
+        for i in range(0, n, 16384):
+            y[i:i + 16384] = rand(min(16384, n - i), d)
+        return dict(dout=(0.1 * rand(T, d)).to(dt), slots=slots, y=y, capacity=capacity,
+                    gates=torch.softmax(rand(T, k), 1), dgates=torch.empty(T, k, device=DEV),
+                    dy=torch.zeros(n, d, dtype=dt, device=DEV) if case["rows"] else None)
     logits = rand(T, E) + rand(E)
     ids = torch.topk(logits + 0.3 * rand(T, E), k, dim=1).indices.to(torch.int32).contiguous()
     mask = _padding(g, T) if case["masked"] else None
@@ -200,6 +230,10 @@ def prepare(case, seed):
         n = B.workspace_bytes_route_scored(s["shape"])
         s["ws"] = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
         return s
+    if op == "combine_backward":
+        dt = B.MOE_BF16 if case["dtype"] == "bf16" else B.MOE_F32
+        s["shape"] = B.make_shape(T, case["d"], 8, E, k, s["capacity"], dt)
+        return s
     s["shape"] = B.make_shape(T, 8, 8, E, k, 0, B.MOE_F32)
     if op == "bias":
         s["counts"] = torch.empty(E, dtype=torch.int32, device=DEV)
@@ -216,9 +250,9 @@ def run(state):
     op = state["case"]["op"]
     if own:
         return {"route": _own_route, "route_backward": _own_route_backward, "bias": _own_bias,
-                "adamw": _own_adamw}[op](state)
+                "adamw": _own_adamw, "combine_backward": _own_combine_backward}[op](state)
     return {"route": _plain_route, "route_backward": _plain_route_backward, "bias": _plain_bias,
-            "adamw": _plain_adamw}[op](state)
+            "adamw": _plain_adamw, "combine_backward": _plain_combine_backward}[op](state)
 
 
 def _own_route(s):
@@ -233,6 +267,20 @@ def _own_route_backward(s):
     B.moe_route_scored_backward(s["shape"], s["routing"], s["logits"], s["ids"], s["dgates"],
                                 s["dlogits"], dlogits_add=s["add"], token_mask=s["mask"])
     return s["dlogits"]
+
+
+def _gate_gradients(s):
+    out = {"dgates": s["dgates"]}
+    if s["dy"] is not None:
+        out["dy"] = s["dy"]
+    return out
+
+
+def _own_combine_backward(s):
+    from capacity_routing_expert_amd import binding as B
+    B.moe_combine_backward(s["shape"], s["dout"], s["gates"], s["slots"], s["y"],
+                           dgates=s["dgates"], dy_rows=s["dy"])
+    return _gate_gradients(s)
 
 
 def _own_bias(s):
@@ -315,6 +363,17 @@ def _plain_route_backward(s):
     return dl
 
 
+def _plain_combine_backward(s):
+    slots = s["slots"].long()
+    kept = slots >= 0
+    dout = s["dout"].float().unsqueeze(1)
+    rows = s["y"][slots.clamp(min=0)].float()
+    s["dgates"].copy_((rows * dout).sum(2) * kept)
+    if s["dy"] is not None:
+        s["dy"][slots[kept]] = (s["gates"].unsqueeze(2) * dout)[kept].to(s["dy"].dtype)
+    return _gate_gradients(s)
+
+
 def _plain_bias(s):
     E = s["case"]["E"]
     ids = s["ids"].long()
@@ -385,6 +444,19 @@ def exact(case, seed):
     if op == "adamw":
         return _exact_adamw(case, s)
     T, E, k = case["T"], case["E"], case["k"]
+    if op == "combine_backward":
+        dgates = torch.zeros(T, k, dtype=torch.float64, device=DEV)
+        dy = torch.zeros(s["y"].shape, dtype=torch.float64, device=DEV) if case["rows"] else None
+        dout = s["dout"].double()
+        for c in range(k):
+            t = torch.nonzero(s["slots"][:, c] >= 0).flatten()
+            at = s["slots"][t, c].long()
+            for i in range(0, len(t), 4096):
+                dgates[t[i:i + 4096], c] = torch.linalg.vecdot(s["y"][at[i:i + 4096]].double(),
+                                                               dout[t[i:i + 4096]])
+            if dy is not None:
+                dy[at] = s["gates"][t, c:c + 1].double() * dout[t]
+        return {"dgates": dgates} if dy is None else {"dgates": dgates, "dy": dy}
     keep = torch.ones(T, dtype=torch.bool, device=DEV) if s["mask"] is None else s["mask"] > 0
     if op == "bias":
         counts = torch.bincount(s["ids"][keep].flatten().long(), minlength=E)
@@ -485,6 +557,12 @@ def work(case):
         return {"bytes": int(n * (2 * size(case["param"]) + size(case["grad"]) + state +
                                   (2 if case["copy"] else 0))), "flops": 20 * n}
     T, E, k = case["T"], case["E"], case["k"]
+    if op == "combine_backward":
+        capacity = max(1, 5 * T * k // (4 * E))
+        n = min(T * k, E * capacity) * case["d"] * size(case["dtype"])
+        return {"bytes": T * case["d"] * size(case["dtype"]) + n + 8 * T * k +
+                (n + 4 * T * k if case["rows"] else 0),
+                "flops": 2 * T * k * case["d"] * (2 if case["rows"] else 1)}
     masked = T if case["masked"] else 0
     if op == "route":
         return {"bytes": (T + E) * case["d"] * size(case["dtype"]) + 4 * T * E + 8 * T * k + masked +
