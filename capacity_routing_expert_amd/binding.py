@@ -35,7 +35,10 @@ EXPORTS = ("moe_capacity", "moe_workspace_bytes", "moe_max_kept_rows", "moe_stat
            "moe_layer_forward_noalloc", "moe_workspace_bytes_balance", "moe_balance_loss",
            "moe_workspace_bytes_route_backward", "moe_route_backward", "moe_quantized_codes_bytes",
            "moe_quantized_scales_bytes", "moe_quantize_weights", "moe_dequantize_weights",
-           "moe_expert_ffn_quantized", "moe_layer_forward_quantized")
+           "moe_expert_ffn_quantized", "moe_layer_forward_quantized",
+           "moe_workspace_bytes_route_scored", "moe_route_scored", "moe_route_scored_backward",
+           "moe_combine_backward", "moe_workspace_bytes_balance_bias", "moe_balance_bias", "moe_adamw_check",
+           "moe_adamw_step", "moe_adamw_moments")
 
 
 class MoeShape(ctypes.Structure):
@@ -51,6 +54,28 @@ class MoeQuantizedExperts(ctypes.Structure):
                 ("b1", ctypes.c_void_p), ("w2_codes", ctypes.c_void_p),
                 ("w2_scales", ctypes.c_void_p), ("b2", ctypes.c_void_p),
                 ("group", ctypes.c_int32), ("gated", ctypes.c_int32)]
+
+
+class MoeRouting(ctypes.Structure):
+    """moe_routing; make_routing fills it."""
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeAdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor; AdamWTensors fills an array of them and keeps the tensors."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_steps", "v_steps",
+                                               "copy")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)]
+
+
+class MoeAdamWConfig(ctypes.Structure):
+    """moe_adamw_config."""
+    _fields_ = [("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("lr", ctypes.c_float), ("beta1", ctypes.c_float),
+                ("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("step", ctypes.c_int64), ("dynamic", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -146,7 +171,27 @@ def lib() -> ctypes.CDLL:
         # shape, x, w_router, b_router, experts, out, ids, gates, slot_of, drop, counts, ws,
         # ws_bytes, stream, events
         L.moe_layer_forward_quantized.argtypes = [SP, P, P, P, QP] + [P] * 7 + [SZ, P, P]
-        for name in ("moe_quantize_weights", "moe_dequantize_weights", "moe_expert_ffn_quantized",
+        for name in ("moe_workspace_bytes_route_scored", "moe_workspace_bytes_balance_bias"):
+            getattr(L, name).argtypes = [SP]
+            getattr(L, name).restype = SZ
+        RP = ctypes.POINTER(MoeRouting)
+        # shape, routing, x, w_router, b_router, score_bias, token_mask, ids, gates, logits, ws,
+        # ws_bytes, stream
+        L.moe_route_scored.argtypes = [SP, RP] + [P] * 9 + [SZ, P]
+        # shape, routing, logits, ids, dgates, dlogits_add, token_mask, dlogits, stream
+        L.moe_route_scored_backward.argtypes = [SP, RP] + [P] * 7
+        # shape, dout, gates, slot_of, y_rows, dgates, dy_rows, stream
+        L.moe_combine_backward.argtypes = [SP] + [P] * 7
+        # shape, topk_ids, token_mask, rate, score_bias, counts, ws, ws_bytes, stream
+        L.moe_balance_bias.argtypes = [SP, P, P, ctypes.c_float, P, P, P, SZ, P]
+        CP, TP = ctypes.POINTER(MoeAdamWConfig), ctypes.POINTER(MoeAdamWTensor)
+        L.moe_adamw_check.argtypes = [CP, TP, I32]
+        L.moe_adamw_step.argtypes = [CP, TP, I32, P]
+        # config, tensors, n, m_out, v_out, stream
+        L.moe_adamw_moments.argtypes = [CP, TP, I32, P, P, P]
+        for name in ("moe_route_scored", "moe_route_scored_backward", "moe_combine_backward",
+                     "moe_balance_bias", "moe_adamw_check", "moe_adamw_step", "moe_adamw_moments",
+                     "moe_quantize_weights", "moe_dequantize_weights", "moe_expert_ffn_quantized",
                      "moe_layer_forward_quantized", "moe_balance_loss", "moe_route_backward", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
                      "moe_layer_forward", "moe_layer_forward_profiled", "moe_layer_forward_padded",
                      "moe_layer_forward_noalloc",
@@ -734,3 +779,202 @@ def moe_layer_forward_quantized(shape, x, w_router, b_router, experts, out, topk
         _cur(dev, expert_counts, "expert_counts", i32, numel=n["E"]), _cur(dev, ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0, _stream(stream), _events(events)),
         "moe_layer_forward_quantized")
+
+
+# ---------------------------------------------------------------- routing by scores
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP_TWO = 0, 1
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP_TWO}
+
+
+def make_routing(score: str = "softmax", n_groups: int = 1, topk_groups: int = 1,
+                 group_score: str = "max", renormalize: bool = False,
+                 scale: float = 1.0) -> MoeRouting:
+    """How experts are chosen and gates formed (moe_routing)."""
+    if score not in _SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(_SCORES)}")
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score {group_score!r} is not one of {sorted(_GROUP_SCORES)}")
+    return MoeRouting(_SCORES[score], int(n_groups), int(topk_groups), _GROUP_SCORES[group_score],
+                      int(bool(renormalize)), float(scale))
+
+
+def workspace_bytes_route_scored(shape: MoeShape) -> int:
+    return int(lib().moe_workspace_bytes_route_scored(ctypes.byref(shape)))
+
+
+def moe_route_scored(shape, routing, x, w_router, b_router, score_bias, topk_ids, topk_gates,
+                     logits=None, token_mask=None, ws=None, stream=None):
+    """moe_route with the scores, bias, groups and gates of `routing`; b_router, score_bias [E] and
+    token_mask [T] uint8 may be None."""
+    dt, f32 = _dtype_of(shape), torch.float32
+    T, d, E, k = shape.T, shape.d_model, shape.n_experts, shape.top_k
+    dev = _device()
+    _check(lib().moe_route_scored(
+        ctypes.byref(shape), ctypes.byref(routing), _cur(dev, x, "x", dt, numel=T * d),
+        _cur(dev, w_router, "w_router", dt, numel=E * d),
+        _cur(dev, b_router, "b_router", f32, numel=E),
+        _cur(dev, score_bias, "score_bias", f32, numel=E),
+        _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
+        _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(dev, topk_gates, "topk_gates", f32, numel=T * k),
+        _cur(dev, logits, "logits", f32, numel=T * E), _cur(dev, ws, "ws", torch.uint8),
+        ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_scored")
+
+
+def moe_route_scored_backward(shape, routing, logits, topk_ids, dgates, dlogits, dlogits_add=None,
+                              token_mask=None, stream=None):
+    """dlogits [T, E] (+ dlogits_add, which may be dlogits) from the gradient dgates [T, k]."""
+    f32 = torch.float32
+    T, E, k = shape.T, shape.n_experts, shape.top_k
+    dev = _device()
+    _check(lib().moe_route_scored_backward(
+        ctypes.byref(shape), ctypes.byref(routing), _cur(dev, logits, "logits", f32, numel=T * E),
+        _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k),
+        _cur(dev, dgates, "dgates", f32, numel=T * k),
+        _cur(dev, dlogits_add, "dlogits_add", f32, numel=T * E),
+        _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
+        _cur(dev, dlogits, "dlogits", f32, numel=T * E), _stream(stream)),
+        "moe_route_scored_backward")
+
+
+def moe_combine_backward(shape, dout, topk_gates, slot_of, y_rows, dgates=None, dy_rows=None,
+                         stream=None):
+    """Gradients of moe_combine: dgates [T, k] fp32 (needs y_rows) and dy_rows (needs topk_gates),
+    each optional; y_rows and dy_rows hold every row that a slot names."""
+    dt, T, d, k = _dtype_of(shape), shape.T, shape.d_model, shape.top_k
+    rows = min(T * k, shape.n_experts * shape.capacity)  # moe_max_kept_rows
+    dev = _device()
+    _check(lib().moe_combine_backward(
+        ctypes.byref(shape), _cur(dev, dout, "dout", dt, T * d),
+        _cur(dev, topk_gates, "topk_gates", torch.float32, T * k),
+        _cur(dev, slot_of, "slot_of", torch.int32, T * k), _cur(dev, y_rows, "y_rows", dt, rows * d),
+        _cur(dev, dgates, "dgates", torch.float32, T * k),
+        _cur(dev, dy_rows, "dy_rows", dt, rows * d), _stream(stream)), "moe_combine_backward")
+
+
+def workspace_bytes_balance_bias(shape: MoeShape) -> int:
+    return int(lib().moe_workspace_bytes_balance_bias(ctypes.byref(shape)))
+
+
+def moe_balance_bias(shape, rate, score_bias, expert_counts=None, topk_ids=None, token_mask=None,
+                     ws=None, stream=None):
+    """score_bias [E] moved by `rate` towards even counts, in place: the counts of topk_ids (written
+    to expert_counts where given), or expert_counts where topk_ids is None."""
+    T, E, k = shape.T, shape.n_experts, shape.top_k
+    dev = _device()
+    bias = _cur(dev, score_bias, "score_bias", torch.float32, numel=E)
+    ids = _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k)
+    if topk_ids is not None and T == 0:
+        ids = bias  # an empty tensor has no address, and None would mean given counts; never read
+    _check(lib().moe_balance_bias(
+        ctypes.byref(shape), ids, _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
+        float(rate), bias, _cur(dev, expert_counts, "expert_counts", torch.int32, numel=E),
+        _cur(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0, _stream(stream)),
+        "moe_balance_bias")
+
+
+# ---------------------------------------------------------------- AdamW
+class AdamWTensors:
+    """The tensors of one optimiser: lists of params, grads and moments (any shapes; entry i of every
+    list has the elements of params[i], all contiguous and on one device), checked once.  m and v are
+    fp32, or int8 and uint8 with m_steps and v_steps ([ceil(n / 256)] fp32 each); copies, bf16, are
+    written after each step; weight_decay is a number or one per tensor."""
+
+    def __init__(self, params, grads, m, v, m_steps=None, v_steps=None, copies=None,
+                 weight_decay=0.0):
+        n = len(params)
+        quantized = m_steps is not None or v_steps is not None
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        lists = {"params": params, "grads": grads, "m": m, "v": v, "weight_decay": decay}
+        for name, x in (("m_steps", m_steps), ("v_steps", v_steps)):
+            if quantized:
+                lists[name] = x
+        if copies is not None:
+            lists["copies"] = copies
+        for name, x in lists.items():
+            if x is None or len(x) != n:
+                raise ValueError(f"{name} has {0 if x is None else len(x)} entries, params {n}")
+        self.device = params[0].device if n else None
+        self.bits = 8 if quantized else 32
+        self.param_dtype = self._one_dtype(params, "params")
+        self.params, self.m, self.v = list(params), list(m), list(v)
+        self.m_steps, self.v_steps, self.copies = m_steps, v_steps, copies
+        self.array = (MoeAdamWTensor * max(n, 1))()
+        self.n = n
+        f32 = torch.float32
+        sdt = (torch.int8, torch.uint8) if quantized else (f32, f32)
+        for i in range(n):
+            a, k = self.array[i], params[i].numel()
+            a.param = self._at(params[i], f"params[{i}]", self.param_dtype, k)
+            a.m = self._at(m[i], f"m[{i}]", sdt[0], k)
+            a.v = self._at(v[i], f"v[{i}]", sdt[1], k)
+            if quantized:
+                a.m_steps = self._at(m_steps[i], f"m_steps[{i}]", f32, (k + 255) // 256)
+                a.v_steps = self._at(v_steps[i], f"v_steps[{i}]", f32, (k + 255) // 256)
+            if copies is not None and copies[i] is not None:
+                a.copy = self._at(copies[i], f"copies[{i}]", torch.bfloat16, k)
+            a.n = k
+            a.weight_decay = float(decay[i])
+        self.set_grads(grads)
+
+    def _one_dtype(self, tensors, name):
+        kinds = {t.dtype for t in tensors}
+        if len(kinds) > 1 or not kinds <= {torch.float32, torch.bfloat16}:
+            raise TypeError(f"{name}: one dtype, float32 or bfloat16, not {sorted(map(str, kinds))}")
+        return kinds.pop() if kinds else torch.float32
+
+    def _at(self, t, name, dtype, numel):
+        p = _ptr(t, name, dtype, self.device, numel)
+        if t.numel() != numel:
+            raise ValueError(f"{name} holds {t.numel()} elements, {numel} are expected")
+        return p
+
+    def set_grads(self, grads):
+        """Other gradients for the steps to come; checks that all tensors are apart."""
+        if len(grads) != self.n:
+            raise ValueError(f"grads has {len(grads)} entries, params {self.n}")
+        self.grad_dtype = self._one_dtype(grads, "grads")
+        self.grads = list(grads)
+        for i, g in enumerate(grads):
+            self.array[i].grad = self._at(g, f"grads[{i}]", self.grad_dtype, self.params[i].numel())
+        c = self.config(0.0, 0.0, 0.0, 1.0, 1, 1.0, None)
+        _check(lib().moe_adamw_check(ctypes.byref(c), self.array, self.n), "moe_adamw_check")
+
+    def config(self, lr, beta1, beta2, eps, step, grad_scale, dynamic):
+        code = lambda t: MOE_BF16 if t is torch.bfloat16 else MOE_F32
+        return MoeAdamWConfig(code(self.param_dtype), code(self.grad_dtype), self.bits, lr, beta1,
+                              beta2, eps, grad_scale, step, dynamic)
+
+    def on(self, dev):
+        if self.n and self.device.index != dev:
+            raise ValueError(f"the tensors are on {self.device}, the current device is cuda:{dev}")
+
+
+def moe_adamw_step(tensors: AdamWTensors, lr, beta1, beta2, eps, step, grad_scale=1.0, dynamic=None,
+                   stream=None):
+    """One AdamW step of all tensors; `step` counts from 1.  dynamic [4] fp32 on the device (lr,
+    grad_scale, step, skip) takes the place of lr, grad_scale and step."""
+    dev = _device()
+    tensors.on(dev)
+    c = tensors.config(lr, beta1, beta2, eps, step, grad_scale,
+                       _cur(dev, dynamic, "dynamic", torch.float32, numel=4))
+    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.array, tensors.n, _stream(stream)),
+           "moe_adamw_step")
+
+
+def moe_adamw_moments(tensors: AdamWTensors, m_out=None, v_out=None, stream=None):
+    """The fp32 moments [n] each of all tensors: lists of outputs (or None, or None entries)."""
+    tensors.on(_device())
+    outs = []
+    for name, x in (("m_out", m_out), ("v_out", v_out)):
+        if x is not None and len(x) != tensors.n:
+            raise ValueError(f"{name} has {len(x)} entries, the optimiser {tensors.n}")
+        outs.append(x if x is None else (ctypes.c_void_p * max(tensors.n, 1))(*[
+            None if t is None else tensors._at(t, f"{name}[{i}]", torch.float32,
+                                               tensors.params[i].numel())
+            for i, t in enumerate(x)]))
+    c = tensors.config(0.0, 0.0, 0.0, 1.0, 1, 1.0, None)
+    _check(lib().moe_adamw_moments(ctypes.byref(c), tensors.array, tensors.n, *outs,
+                                   _stream(stream)), "moe_adamw_moments")

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "dispatch.hip", "gemm_bf16.hip", "ffn_f32.hip", "combine.hip",
            "schedule.hip", "balance.hip", "route_backward.hip", "quantize.hip",
-           "ffn_quant.hip"]
+           "ffn_quant.hip", "route_scored.hip", "route_scored_backward.hip", "combine_backward.hip",
+           "balance_bias.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,375 @@
+// AdamW over many tensors at once, moments in fp32 or in 8 bits.
+//
+//   g' = grad_scale g
+//   m  = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+//   p  = p - lr wd p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+// m and v are fp32 numbers formed by the operations as written, each rounded (no fused ones), so that
+// the 8-bit codes below are the same wherever they are computed; p takes the unquantised m and v.
+//
+// 8 bits: blocks of 256 consecutive elements of a tensor share one fp32 step for m and one for
+// r = sqrt(v).  A code c stands for c |c| step (c = -127 .. 127) and for r = c^2 step (c = 0 .. 255);
+// step = max |x| / c_max^2, c = the root of |x| / step rounded to nearest.  Squares, because the
+// elements of a block differ by orders of magnitude: 2 / c apart relatively, down to 1 / c_max^2 of
+// the largest.  r and not v, because r divides: its relative error is the update's.  An r that is not
+// zero keeps a code of 1 at least.  Rounding to nearest: of a v that hardly moves (beta2 0.999) the
+// steps of one pass are below half a code, so codes move only as the block's largest does and by
+// large gradients, which still holds r within 6.5 % of fp32's on average over 4000 steps of Gaussian
+// gradients whose size varies by e^(+-1) within a block; rounding at random, unbiased, adds its noise
+// every step and holds it within 8 %.
+//
+// Bound: memory, 28 bytes an element for fp32 moments and gradients, 14 to 18 for 8 bits.  The tensors'
+// addresses go along as kernel arguments, 48 to a launch; a block takes 4096 elements of one tensor, a
+// thread 4 neighbours at a time, so that a wave has exactly the 256 that share a step.
+#include <math.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTensors = 48;    // a launch
+constexpr int kChunk = 4096;    // elements a block
+constexpr int kQuantBlock = 256;
+
+struct AdamRec {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_steps;
+  float* v_steps;
+  bf16_t* copy;
+  int64_t n;
+  float wd;
+  int vec;  // every array lies where 4 elements load at once
+};
+struct AdamArgs {
+  AdamRec rec[kTensors];
+  int32_t start[kTensors];  // first block of each tensor
+  int32_t count;
+  float lr, beta1, beta2, eps, grad_scale, rate, inv_root;
+  double log_beta1, log_beta2;
+  const float* dynamic;
+};
+
+struct Rates {
+  float lr, grad_scale, rate, inv_root;
+};
+
+// The 4 elements of a lane, as loaded.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int64_t i, int64_t n, bool whole, float (&o)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, int64_t i, int64_t n, bool whole,
+                                             float (&o)[4]) {
+  if (whole) {
+    const float4 f = *reinterpret_cast<const float4*>(p + i);
+    o[0] = f.x, o[1] = f.y, o[2] = f.z, o[3] = f.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = i + j < n ? p[i + j] : 0.0f;
+  }
+}
+template <>
+__device__ __forceinline__ void load4<bf16_t>(const bf16_t* p, int64_t i, int64_t n, bool whole,
+                                              float (&o)[4]) {
+  if (whole) {
+    const uint2 f = *reinterpret_cast<const uint2*>(p + i);
+    o[0] = __uint_as_float(f.x << 16), o[1] = __uint_as_float(f.x & 0xFFFF0000u);
+    o[2] = __uint_as_float(f.y << 16), o[3] = __uint_as_float(f.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = i + j < n ? bf16_to_f32(p[i + j]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, bool whole,
+                                       const float (&o)[4]) {
+  if (whole) {
+    *reinterpret_cast<float4*>(p + i) = make_float4(o[0], o[1], o[2], o[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = o[j];
+  }
+}
+__device__ __forceinline__ void store4(bf16_t* p, int64_t i, int64_t n, bool whole,
+                                       const float (&o)[4]) {
+  const uint32_t a = pack_bf16x2(o[0], o[1]), b = pack_bf16x2(o[2], o[3]);
+  if (whole) {
+    *reinterpret_cast<uint2*>(p + i) = make_uint2(a, b);
+  } else {
+    const bf16_t w[4] = {(bf16_t)a, (bf16_t)(a >> 16), (bf16_t)b, (bf16_t)(b >> 16)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = w[j];
+  }
+}
+// 4 codes in a dword, the first lowest
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n, bool whole) {
+  if (whole) return *reinterpret_cast<const uint32_t*>(p + i);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) w |= (uint32_t)p[i + j] << (8 * j);
+  return w;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, bool whole, uint32_t w) {
+  if (whole) {
+    *reinterpret_cast<uint32_t*>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) p[i + j] = (uint8_t)(w >> (8 * j));
+  }
+}
+__device__ __forceinline__ void decode_m(uint32_t w, float step, float (&o)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = (int)(int8_t)(w >> (8 * j));
+    o[j] = (float)(c * (c < 0 ? -c : c)) * step;
+  }
+}
+__device__ __forceinline__ void decode_v(uint32_t w, float step, float (&o)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = (int)((w >> (8 * j)) & 0xFFu);
+    const float r = (float)(c * c) * step;
+    o[j] = r * r;
+  }
+}
+
+// The largest of the wave's values, as the bit patterns of |x| order them: NaN above infinity
+// above all else.
+__device__ __forceinline__ float wave_absmax(const float (&x)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    m = u > m ? u : m;
+  }
+  auto take = [&](uint32_t o) { m = o > m ? o : m; };
+  take(dpp32<0xB1>(m));
+  take(dpp32<0x4E>(m));
+  take(dpp32<0x141>(m));
+  take(dpp32<0x140>(m));
+  take((uint32_t)__shfl_xor((int)m, 16, 64));
+  take((uint32_t)__shfl_xor((int)m, 32, 64));
+  return __uint_as_float(m);
+}
+// Codes of x under `step`; a block whose step is not finite has no value left that is: codes 0 (or 1).
+template <int TOP>
+__device__ __forceinline__ int encode(float x, float step) {
+  const float y = step > 0.0f ? fabsf(x) / step : 0.0f;
+  const float c = floorf(sqrtf(y) + 0.5f);
+  int code = c >= 0.0f ? (int)fminf(c, (float)TOP) : 0;
+  if (TOP == 255) return x > 0.0f && code < 1 ? 1 : code;
+  return x < 0.0f ? -code : code;
+}
+
+// m and v of one element, each operation rounded
+__device__ __forceinline__ void moments(float g, float beta1, float beta2, float& m, float& v) {
+#pragma clang fp contract(off)
+  const float keep_m = m * beta1, new_m = g * (1.0f - beta1);
+  m = keep_m + new_m;
+  const float sq = g * g;
+  const float keep_v = v * beta2, new_v = sq * (1.0f - beta2);
+  v = keep_v + new_v;
+}
+
+__device__ __forceinline__ int tensor_of(const int32_t* start, int count, int block) {
+  const int lane = threadIdx.x & 63;
+  const bool before = lane < count && start[lane < count ? lane : 0] <= block;
+  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(before)) - 1);
+}
+
+template <typename P, typename G, bool Q8>
+__global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
+  const int ti = tensor_of(a.start, a.count, (int)blockIdx.x);
+  const AdamRec& r = a.rec[ti];
+  const int64_t n = r.n, base = (int64_t)((int)blockIdx.x - a.start[ti]) * kChunk;
+  Rates c{a.lr, a.grad_scale, a.rate, a.inv_root};
+  if (a.dynamic) {
+    if (a.dynamic[3] != 0.0f) return;
+    c.lr = a.dynamic[0];
+    c.grad_scale = a.dynamic[1];
+    const double t = fmax((double)a.dynamic[2], 1.0);
+    c.rate = (float)((double)c.lr / -expm1(t * a.log_beta1));
+    c.inv_root = (float)(1.0 / sqrt(-expm1(t * a.log_beta2)));
+  }
+  const float lr_wd = c.lr * r.wd;
+  P* p = (P*)r.p;
+  const G* g = (const G*)r.g;
+  bf16_t* copy = r.copy;
+  const bool whole = r.vec && base + kChunk <= n;
+#pragma unroll
+  for (int it = 0; it < kChunk / 1024; ++it) {
+    const int64_t i = base + it * 1024 + (int64_t)threadIdx.x * 4;
+    if (!whole && base + it * 1024 + (threadIdx.x & ~63) * 4 >= n) return;  // waves leave together
+    float pv[4], gv[4], mv[4], vv[4];
+    load4<P>(p, i, n, whole, pv);
+    load4<G>(g, i, n, whole, gv);
+    const int64_t qb = i / kQuantBlock;
+    if constexpr (Q8) {
+      decode_m(load_codes((const uint8_t*)r.m, i, n, whole), r.m_steps[qb], mv);
+      decode_v(load_codes((const uint8_t*)r.v, i, n, whole), r.v_steps[qb], vv);
+    } else {
+      load4<float>((const float*)r.m, i, n, whole, mv);
+      load4<float>((const float*)r.v, i, n, whole, vv);
+    }
+    float rv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      moments(gv[j] * c.grad_scale, a.beta1, a.beta2, mv[j], vv[j]);
+      rv[j] = sqrtf(vv[j]);
+      const float q = fmaf(-lr_wd, pv[j], pv[j]);
+      pv[j] = q - c.rate * mv[j] / fmaf(rv[j], c.inv_root, a.eps);
+    }
+    store4(p, i, n, whole, pv);
+    if (copy) store4(copy, i, n, whole, pv);
+    if constexpr (Q8) {
+      // elements past the tensor's end are zeros
+      const float ms = wave_absmax(mv) / 16129.0f, vs = wave_absmax(rv) / 65025.0f;
+      uint32_t mc = 0, vc = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mc |= ((uint32_t)encode<127>(mv[j], ms) & 0xFFu) << (8 * j);
+        vc |= (uint32_t)encode<255>(rv[j], vs) << (8 * j);
+      }
+      store_codes((uint8_t*)r.m, i, n, whole, mc);
+      store_codes((uint8_t*)r.v, i, n, whole, vc);
+      if ((threadIdx.x & 63) == 0) {
+        r.m_steps[qb] = ms;
+        r.v_steps[qb] = vs;
+      }
+    } else {
+      store4((float*)r.m, i, n, whole, mv);
+      store4((float*)r.v, i, n, whole, vv);
+    }
+  }
+}
+
+struct MomentRec {
+  const void* m;
+  const void* v;
+  const float* m_steps;
+  const float* v_steps;
+  float* m_out;
+  float* v_out;
+  int64_t n;
+  int vec;
+};
+struct MomentArgs {
+  MomentRec rec[kTensors];
+  int32_t start[kTensors];
+  int32_t count;
+};
+
+template <bool Q8>
+__global__ __launch_bounds__(256) void k_adamw_moments(const MomentArgs a) {
+  const int ti = tensor_of(a.start, a.count, (int)blockIdx.x);
+  const MomentRec& r = a.rec[ti];
+  const int64_t n = r.n, base = (int64_t)((int)blockIdx.x - a.start[ti]) * kChunk;
+  const bool whole = r.vec && base + kChunk <= n;
+#pragma unroll
+  for (int it = 0; it < kChunk / 1024; ++it) {
+    const int64_t i = base + it * 1024 + (int64_t)threadIdx.x * 4;
+    if (!whole && i >= n) return;
+    float mv[4], vv[4];
+    if constexpr (Q8) {
+      decode_m(load_codes((const uint8_t*)r.m, i, n, whole), r.m_steps[i / kQuantBlock], mv);
+      decode_v(load_codes((const uint8_t*)r.v, i, n, whole), r.v_steps[i / kQuantBlock], vv);
+    } else {
+      load4<float>((const float*)r.m, i, n, whole, mv);
+      load4<float>((const float*)r.v, i, n, whole, vv);
+    }
+    if (r.m_out) store4(r.m_out, i, n, whole, mv);
+    if (r.v_out) store4(r.v_out, i, n, whole, vv);
+  }
+}
+
+bool aligned_to(size_t a, std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((uintptr_t)p % a != 0) return false;
+  return true;
+}
+
+// Deals n tensors out to launches: fill(args, slot, tensor) fills a record, go(args, blocks) launches.
+// Chunks of a launch are below 2^31 for any sizes that fit a GPU's memory (kChunk elements each).
+template <typename Args, typename Fill, typename Go>
+hipError_t for_launches(Args& args, const moe_adamw_tensor* ts, int n, Fill fill, Go go) {
+  int slot = 0;
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (ts[i].n == 0) continue;
+    args.start[slot] = (int32_t)blocks;
+    fill(args.rec[slot], i);
+    blocks += (ts[i].n + kChunk - 1) / kChunk;
+    if (++slot == kTensors) {
+      args.count = slot;
+      if (hipError_t err = go(args, blocks); err != hipSuccess) return err;
+      slot = 0;
+      blocks = 0;
+    }
+  }
+  args.count = slot;
+  return slot ? go(args, blocks) : hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,
+                        hipStream_t st) {
+  AdamArgs args;
+  args.lr = c.lr;
+  args.beta1 = c.beta1;
+  args.beta2 = c.beta2;
+  args.eps = c.eps;
+  args.grad_scale = c.grad_scale;
+  args.log_beta1 = log((double)c.beta1);
+  args.log_beta2 = log((double)c.beta2);
+  args.dynamic = c.dynamic;
+  const double t = (double)(c.step < 1 ? 1 : c.step);
+  args.rate = (float)((double)c.lr / -expm1(t * args.log_beta1));
+  args.inv_root = (float)(1.0 / sqrt(-expm1(t * args.log_beta2)));
+  const bool p16 = c.param_dtype == MOE_BF16, g16 = c.grad_dtype == MOE_BF16, q8 = c.state_bits == 8;
+  auto fill = [&](AdamRec& r, int i) {
+    const moe_adamw_tensor& x = ts[i];
+    r = AdamRec{x.param, x.grad, x.m, x.v, x.m_steps, x.v_steps, (bf16_t*)x.copy, x.n, x.weight_decay, 0};
+    r.vec = aligned_to(p16 ? 8 : 16, {x.param}) && aligned_to(g16 ? 8 : 16, {x.grad}) &&
+            aligned_to(q8 ? 4 : 16, {x.m, x.v}) && aligned_to(8, {x.copy});
+  };
+  auto launch = [&](auto kern) {
+    return for_launches(args, ts, n, fill, [&](const AdamArgs& a, int64_t blocks) {
+      hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+      return hipGetLastError();
+    });
+  };
+  if (p16) {
+    if (g16) return q8 ? launch(k_adamw<bf16_t, bf16_t, true>) : launch(k_adamw<bf16_t, bf16_t, false>);
+    return q8 ? launch(k_adamw<bf16_t, float, true>) : launch(k_adamw<bf16_t, float, false>);
+  }
+  if (g16) return q8 ? launch(k_adamw<float, bf16_t, true>) : launch(k_adamw<float, bf16_t, false>);
+  return q8 ? launch(k_adamw<float, float, true>) : launch(k_adamw<float, float, false>);
+}
+
+hipError_t launch_adamw_moments(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,
+                                float* const* m_out, float* const* v_out, hipStream_t st) {
+  MomentArgs args;
+  const bool q8 = c.state_bits == 8;
+  auto fill = [&](MomentRec& r, int i) {
+    const moe_adamw_tensor& x = ts[i];
+    r = MomentRec{x.m, x.v, x.m_steps, x.v_steps, m_out ? m_out[i] : nullptr,
+                  v_out ? v_out[i] : nullptr, x.n, 0};
+    r.vec = aligned_to(q8 ? 4 : 16, {x.m, x.v}) && aligned_to(16, {r.m_out, r.v_out});
+  };
+  auto launch = [&](auto kern) {
+    return for_launches(args, ts, n, fill, [&](const MomentArgs& a, int64_t blocks) {
+      hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+      return hipGetLastError();
+    });
+  };
+  return q8 ? launch(k_adamw_moments<true>) : launch(k_adamw_moments<false>);
+}
+
+}  // namespace moe

@@ -6,7 +6,9 @@
 #include <string.h>
 
 #include <algorithm>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "moe_internal.h"
@@ -290,6 +292,104 @@ moe_status check_quantize(const moe_shape* shape, int32_t rows, int32_t cols, in
     return fail(MOE_ERR_INVALID_ARGUMENT, "group = %d is not 32, 64 or 128", group);
   if (quantized_codes_bytes(1, rows, cols) >= kMaxQuantizedBytes)
     return fail(MOE_ERR_UNSUPPORTED, "4-bit matrix of %d x %d: 2 GiB or more per expert", rows, cols);
+  return MOE_OK;
+}
+
+moe_status check_routing(const moe_shape& s, const moe_routing* r) {
+  if (!r) return fail(MOE_ERR_INVALID_ARGUMENT, "routing is NULL");
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "score %d unknown", r->score);
+  if (r->n_groups < 1 || s.n_experts % r->n_groups != 0)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "n_groups = %d does not divide n_experts = %d", r->n_groups,
+                s.n_experts);
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "topk_groups = %d not in [1, n_groups = %d]",
+                r->topk_groups, r->n_groups);
+  if (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP_TWO)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "group_score %d unknown", r->group_score);
+  if (s.top_k > r->topk_groups * (s.n_experts / r->n_groups))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "top_k = %d of %d groups of %d experts", s.top_k,
+                r->topk_groups, s.n_experts / r->n_groups);
+  if (r->renormalize != 0 && r->renormalize != 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "renormalize = %d is not 0 or 1", r->renormalize);
+  if (!isfinite(r->scale) || !(r->scale > 0.0f))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scale = %g must be positive and finite", r->scale);
+  return MOE_OK;
+}
+
+moe_status check_adamw_lists(const moe_adamw_config* c, const moe_adamw_tensor* ts, int32_t n) {
+  if (!c) return fail(MOE_ERR_INVALID_ARGUMENT, "config is NULL");
+  if (c->state_bits != 8 && c->state_bits != 32)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "state_bits = %d is not 8 or 32", c->state_bits);
+  if (n < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "n_tensors = %d < 0", n);
+  if (n > 0 && !ts) return fail(MOE_ERR_INVALID_ARGUMENT, "tensors is NULL");
+  return MOE_OK;
+}
+
+// a pointer of entry i of a list of tensors
+moe_status check_entry(const void* p, size_t a, const char* name, int i) {
+  if (!p) return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d].%s is NULL", i, name);
+  if (!aligned(p, a))
+    return fail(MOE_ERR_UNSUPPORTED, "tensors[%d].%s is not %zu-byte aligned", i, name, a);
+  return MOE_OK;
+}
+
+moe_status check_adamw_state(const moe_adamw_config& c, const moe_adamw_tensor& t, int i) {
+  const size_t a = c.state_bits == 8 ? 1 : 4;
+  MOE_TRY(check_entry(t.m, a, "m", i));
+  MOE_TRY(check_entry(t.v, a, "v", i));
+  if (c.state_bits == 8) {
+    MOE_TRY(check_entry(t.m_steps, 4, "m_steps", i));
+    MOE_TRY(check_entry(t.v_steps, 4, "v_steps", i));
+  } else if (t.m_steps || t.v_steps) {
+    return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d]: steps with 32-bit states", i);
+  }
+  return MOE_OK;
+}
+
+moe_status check_adamw_n(const moe_adamw_tensor& t, int i) {
+  if (t.n < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d].n = %lld < 0", i, (long long)t.n);
+  if (t.n >= ((int64_t)1 << 36))
+    return fail(MOE_ERR_UNSUPPORTED, "tensors[%d].n = %lld >= 2^36", i, (long long)t.n);
+  return MOE_OK;
+}
+
+moe_status check_adamw(const moe_adamw_config* config, const moe_adamw_tensor* ts, int32_t n) {
+  MOE_TRY(check_adamw_lists(config, ts, n));
+  const moe_adamw_config& c = *config;
+  if ((c.param_dtype != MOE_F32 && c.param_dtype != MOE_BF16) ||
+      (c.grad_dtype != MOE_F32 && c.grad_dtype != MOE_BF16))
+    return fail(MOE_ERR_UNSUPPORTED, "param_dtype %d or grad_dtype %d unknown", c.param_dtype,
+                c.grad_dtype);
+  if (!(c.beta1 >= 0.0f && c.beta1 < 1.0f) || !(c.beta2 >= 0.0f && c.beta2 < 1.0f))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "beta1 = %g, beta2 = %g not in [0, 1)", c.beta1, c.beta2);
+  if (!isfinite(c.eps) || !(c.eps > 0.0f))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "eps = %g must be positive and finite", c.eps);
+  if (c.dynamic) {
+    if (!aligned(c.dynamic, 4)) return fail(MOE_ERR_UNSUPPORTED, "dynamic is not 4-byte aligned");
+  } else {
+    if (!isfinite(c.lr) || !(c.lr >= 0.0f) || !isfinite(c.grad_scale))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "lr = %g, grad_scale = %g: finite, lr >= 0", c.lr,
+                  c.grad_scale);
+    if (c.step < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "step = %lld < 1", (long long)c.step);
+  }
+  const size_t pa = c.param_dtype == MOE_BF16 ? 2 : 4, ga = c.grad_dtype == MOE_BF16 ? 2 : 4;
+  for (int i = 0; i < n; ++i) {
+    const moe_adamw_tensor& t = ts[i];
+    MOE_TRY(check_adamw_n(t, i));
+    if (t.n == 0) continue;
+    MOE_TRY(check_entry(t.param, pa, "param", i));
+    MOE_TRY(check_entry(t.grad, ga, "grad", i));
+    MOE_TRY(check_adamw_state(c, t, i));
+    if (t.copy) {
+      if (c.param_dtype != MOE_F32)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d]: copy of a bf16 param", i);
+      MOE_TRY(check_entry(t.copy, 2, "copy", i));
+    }
+    if (!isfinite(t.weight_decay) || !(t.weight_decay >= 0.0f))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d].weight_decay = %g: finite, >= 0", i,
+                  t.weight_decay);
+  }
   return MOE_OK;
 }
 
@@ -1272,6 +1372,196 @@ moe_status moe_layer_forward_quantized(const moe_shape* shape, const void* x, co
                        experts->w2_codes, experts->b2, out, topk_ids, topk_gates, slot_of,
                        drop_mask, expert_counts, ws, ws_bytes, (hipStream_t)stream, events, false,
                        nullptr, experts->gated != 0, experts);
+}
+
+size_t moe_workspace_bytes_route_scored(const moe_shape* shape) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  return route_scored_ws_bytes(*shape);
+}
+
+moe_status moe_route_scored(const moe_shape* shape, const moe_routing* routing, const void* x,
+                            const void* w_router, const float* b_router, const float* score_bias,
+                            const uint8_t* token_mask, int32_t* topk_ids, float* topk_gates,
+                            float* logits, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_routing(s, routing));
+  if (s.n_experts * (int64_t)s.d_model * (int64_t)elem_bytes(s) >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "w_router of %d x %d: 2 GiB or more", s.n_experts, s.d_model);
+  if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or enqueue
+  MOE_TRY(check_data_ptr(s, x, "x"));
+  MOE_TRY(check_data_ptr(s, w_router, "w_router"));
+  if (b_router) MOE_TRY(check_ptr(b_router, 4, "b_router"));
+  if (score_bias) MOE_TRY(check_ptr(score_bias, 4, "score_bias"));
+  MOE_TRY(check_ptr(topk_ids, 4, "topk_ids"));
+  MOE_TRY(check_ptr(topk_gates, 4, "topk_gates"));
+  if (logits) MOE_TRY(check_ptr(logits, 4, "logits"));
+  MOE_TRY(check_ws_bytes(route_scored_ws_bytes(s), ws, ws_bytes));
+  hipError_t err = launch_route_scored(s, *routing, x, w_router, b_router, score_bias, token_mask,
+                                       topk_ids, topk_gates, logits, ws, (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "route by scores");
+}
+
+moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* routing,
+                                     const float* logits, const int32_t* topk_ids,
+                                     const float* dgates, const float* dlogits_add,
+                                     const uint8_t* token_mask, float* dlogits,
+                                     moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_routing(s, routing));
+  if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or enqueue
+  MOE_TRY(check_ptr(logits, 4, "logits"));
+  MOE_TRY(check_ptr(topk_ids, 4, "topk_ids"));
+  MOE_TRY(check_ptr(dgates, 4, "dgates"));
+  if (dlogits_add) MOE_TRY(check_ptr(dlogits_add, 4, "dlogits_add"));
+  MOE_TRY(check_ptr(dlogits, 4, "dlogits"));
+  const size_t bytes = (size_t)s.T * s.n_experts * 4, choices = (size_t)s.T * s.top_k * 4;
+  if (overlap(dlogits, bytes, logits, bytes))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits overlaps logits");
+  if (overlap(dlogits, bytes, topk_ids, choices) || overlap(dlogits, bytes, dgates, choices))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits overlaps topk_ids or dgates");
+  if (dlogits_add != dlogits && overlap(dlogits, bytes, dlogits_add, bytes))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits_add overlaps dlogits without being it");
+  hipError_t err = launch_route_scored_backward(s, *routing, logits, topk_ids, dgates, dlogits_add,
+                                                token_mask, dlogits, (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "route by scores, backward");
+}
+
+moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const float* topk_gates,
+                                const int32_t* slot_of, const void* y_rows, float* dgates,
+                                void* dy_rows, moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  if (!dgates && !dy_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dgates and dy_rows are both NULL");
+  if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or enqueue
+  MOE_TRY(check_data_ptr(s, dout, "dout"));
+  MOE_TRY(check_ptr(slot_of, 4, "slot_of"));
+  const size_t row = (size_t)s.d_model * elem_bytes(s), rows = (size_t)max_rows(s) * row;
+  const size_t choices = (size_t)s.T * s.top_k * 4;
+  if (dgates) {
+    MOE_TRY(check_ptr(dgates, 4, "dgates"));
+    if (rows > 0) MOE_TRY(check_data_ptr(s, y_rows, "y_rows"));
+    if (overlap(dgates, choices, topk_gates, choices) || overlap(dgates, choices, slot_of, choices))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps topk_gates or slot_of");
+  }
+  if (dy_rows) {
+    MOE_TRY(check_data_ptr(s, dy_rows, "dy_rows"));
+    MOE_TRY(check_ptr(topk_gates, 4, "topk_gates"));
+    if (overlap(dy_rows, rows, dout, (size_t)s.T * row))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps dout");
+    if (dgates && dy_rows != y_rows && overlap(dy_rows, rows, y_rows, rows))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps y_rows without being it");
+  }
+  hipError_t err = launch_combine_backward(s, dout, topk_gates, slot_of, y_rows, dgates, dy_rows,
+                                           (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "combine backward");
+}
+
+size_t moe_workspace_bytes_balance_bias(const moe_shape* shape) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  return balance_bias_ws_bytes(*shape);
+}
+
+moe_status moe_balance_bias(const moe_shape* shape, const int32_t* topk_ids,
+                            const uint8_t* token_mask, float rate, float* score_bias,
+                            int32_t* expert_counts, void* ws, size_t ws_bytes,
+                            moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  if (!isfinite(rate) || !(rate >= 0.0f))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "rate = %g must be finite and >= 0", rate);
+  MOE_TRY(check_ptr(score_bias, 4, "score_bias"));
+  if (!topk_ids && !expert_counts)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "topk_ids and expert_counts are both NULL");
+  if (topk_ids) MOE_TRY(check_ptr(topk_ids, 4, "topk_ids"));
+  if (expert_counts) MOE_TRY(check_ptr(expert_counts, 4, "expert_counts"));
+  if (overlap(score_bias, (size_t)s.n_experts * 4, expert_counts, (size_t)s.n_experts * 4))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "score_bias overlaps expert_counts");
+  if (topk_ids) {
+    const size_t need = balance_bias_ws_bytes(s);
+    if (need) MOE_TRY(check_ws_bytes(need, ws, ws_bytes));
+  }
+  hipError_t err = launch_balance_bias(s, topk_ids, token_mask, rate, score_bias, expert_counts, ws,
+                                       (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "balance bias");
+}
+
+moe_status moe_adamw_check(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                           int32_t n_tensors) {
+  MOE_TRY(check_adamw(config, tensors, n_tensors));
+  const moe_adamw_config& c = *config;
+  struct Range {
+    uintptr_t from, to;
+    int tensor;
+    bool written;
+  };
+  std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[(size_t)n_tensors * 7 + 1]);
+  if (!ranges) return fail(MOE_ERR_UNSUPPORTED, "no host memory to check %d tensors", n_tensors);
+  size_t count = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    const size_t n = (size_t)t.n, steps = (n + 255) / 256 * 4, state = c.state_bits == 8 ? 1 : 4;
+    if (n == 0) continue;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+      if (p) ranges[count++] = Range{(uintptr_t)p, (uintptr_t)p + bytes, i, written};
+    };
+    add(t.param, n * (c.param_dtype == MOE_BF16 ? 2 : 4), true);
+    add(t.grad, n * (c.grad_dtype == MOE_BF16 ? 2 : 4), false);
+    add(t.m, n * state, true);
+    add(t.v, n * state, true);
+    add(t.m_steps, steps, true);
+    add(t.v_steps, steps, true);
+    add(t.copy, n * 2, true);
+  }
+  std::sort(ranges.get(), ranges.get() + count,
+            [](const Range& a, const Range& b) { return a.from < b.from; });
+  // the furthest end so far, of what is written and of everything
+  uintptr_t written_to = 0, all_to = 0;
+  for (size_t i = 0; i < count; ++i) {
+    const Range& r = ranges[i];
+    if (r.from < written_to || (r.written && r.from < all_to))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "an array of tensors[%d] overlaps another of the list",
+                  r.tensor);
+    all_to = std::max(all_to, r.to);
+    if (r.written) written_to = std::max(written_to, r.to);
+  }
+  return MOE_OK;
+}
+
+moe_status moe_adamw_step(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                          int32_t n_tensors, moe_stream_t stream) {
+  MOE_TRY(check_adamw(config, tensors, n_tensors));
+  hipError_t err = launch_adamw(*config, tensors, n_tensors, (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "adamw step");
+}
+
+moe_status moe_adamw_moments(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                             int32_t n_tensors, float* const* m_out, float* const* v_out,
+                             moe_stream_t stream) {
+  MOE_TRY(check_adamw_lists(config, tensors, n_tensors));
+  const size_t state = config->state_bits == 8 ? 1 : 4;
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    MOE_TRY(check_adamw_n(t, i));
+    if (t.n == 0) continue;
+    MOE_TRY(check_adamw_state(*config, t, i));
+    const size_t n = (size_t)t.n, steps = t.m_steps ? (n + 255) / 256 * 4 : 0;
+    float* outs[2] = {m_out ? m_out[i] : nullptr, v_out ? v_out[i] : nullptr};
+    for (float* o : outs) {
+      if (!o) continue;
+      MOE_TRY(check_entry(o, 4, o == outs[0] ? "m_out" : "v_out", i));
+      if (overlap(o, n * 4, t.m, n * state) || overlap(o, n * 4, t.v, n * state) ||
+          overlap(o, n * 4, t.m_steps, steps) || overlap(o, n * 4, t.v_steps, steps))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d]: an output overlaps the state", i);
+    }
+    if (overlap(outs[0], n * 4, outs[1], n * 4))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d]: m_out overlaps v_out", i);
+  }
+  hipError_t err = launch_adamw_moments(*config, tensors, n_tensors, m_out, v_out,
+                                        (hipStream_t)stream);
+  return err == hipSuccess ? MOE_OK : device_error(err, "adamw moments");
 }
 
 }  // extern "C"

@@ -261,4 +261,32 @@ hipError_t launch_quant_up(const moe_shape& s, const moe_quantized_experts& q, c
 hipError_t launch_quant_down(const moe_shape& s, const moe_quantized_experts& q, const void* h,
                              const int32_t* offsets, void* y, int64_t rows_ub, hipStream_t st);
 
+// ---- routing by scores (route_scored.hip) and its backward pass (route_scored_backward.hip);
+// b_router, score_bias, mask, logits and add may be NULL; T > 0
+size_t route_scored_ws_bytes(const moe_shape& s);
+hipError_t launch_route_scored(const moe_shape& s, const moe_routing& r, const void* x,
+                               const void* w_router, const float* b_router,
+                               const float* score_bias, const uint8_t* mask, int32_t* ids,
+                               float* gates, float* logits, void* ws, hipStream_t st);
+hipError_t launch_route_scored_backward(const moe_shape& s, const moe_routing& r,
+                                        const float* logits, const int32_t* ids,
+                                        const float* dgates, const float* add, const uint8_t* mask,
+                                        float* dlogits, hipStream_t st);
+
+// ---- update of the selection bias (balance_bias.hip): counts of ids, or given where ids is NULL
+size_t balance_bias_ws_bytes(const moe_shape& s);
+hipError_t launch_balance_bias(const moe_shape& s, const int32_t* ids, const uint8_t* mask,
+                               float rate, float* bias, int32_t* counts, void* ws, hipStream_t st);
+
+// ---- backward pass of the combine (combine_backward.hip): dgates with y, dy with gates; T > 0
+hipError_t launch_combine_backward(const moe_shape& s, const void* dout, const float* gates,
+                                   const int32_t* slot_of, const void* y, float* dgates, void* dy,
+                                   hipStream_t st);
+
+// ---- AdamW (adamw.hip); m_out, v_out or their entries may be NULL
+hipError_t launch_adamw(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,
+                        hipStream_t st);
+hipError_t launch_adamw_moments(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,
+                                float* const* m_out, float* const* v_out, hipStream_t st);
+
 }  // namespace moe

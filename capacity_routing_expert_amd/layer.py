@@ -410,3 +410,130 @@ def layer_forward_quantized(dev: dict, experts: B.QuantizedExperts, top_k: int, 
                                   slot_of=res["slot_of"], drop_mask=res["drop_mask"],
                                   expert_counts=res["counts"], ws=ws, events=events)
     return res
+
+
+# ---------------------------------------------------------------- routing by scores
+def route_scored(x: torch.Tensor, w_router: torch.Tensor, b_router: torch.Tensor | None, top_k: int,
+                 routing: B.MoeRouting, score_bias: torch.Tensor | None = None,
+                 token_mask: torch.Tensor | None = None, want_logits: bool = True,
+                 ws: torch.Tensor | None = None) -> dict:
+    """moe_route_scored: ids, gates and, when want_logits, logits."""
+    T, d = x.shape
+    E = w_router.shape[0]
+    shape = B.make_shape(T, d, 8, E, top_k, 0, B.MOE_BF16 if x.dtype == torch.bfloat16 else B.MOE_F32)
+    if ws is None:
+        ws = torch.empty(max(B.workspace_bytes_route_scored(shape), 256), dtype=torch.uint8,
+                         device=x.device)
+    res = {
+        "ids": torch.empty((T, top_k), dtype=torch.int32, device=x.device),
+        "gates": torch.empty((T, top_k), dtype=torch.float32, device=x.device),
+        "logits": torch.empty((T, E), dtype=torch.float32, device=x.device) if want_logits else None,
+    }
+    B.moe_route_scored(shape, routing, x, w_router, b_router, score_bias, res["ids"], res["gates"],
+                       logits=res["logits"], token_mask=token_mask, ws=ws)
+    return res
+
+
+def layer_forward_scored(dev: dict, top_k: int, capacity: int, routing: B.MoeRouting,
+                         score_bias: torch.Tensor | None = None,
+                         token_mask: torch.Tensor | None = None,
+                         experts: B.QuantizedExperts | None = None) -> dict:
+    """The layer with routing by scores, stage by stage, and what its backward pass takes: out, ids,
+    gates, logits, y_rows and moe_dispatch's outputs.  `experts`: 4-bit experts in place of
+    dev["w1"] .. dev["b2"]."""
+    x = dev["x"]
+    if experts is None:
+        shape = shape_of(dev, top_k, capacity)
+    else:
+        shape = B.make_shape(x.shape[0], x.shape[1], experts.d_ff, experts.E, top_k, capacity,
+                             B.MOE_BF16 if x.dtype == torch.bfloat16 else B.MOE_F32)
+    res = route_scored(x, dev["w_router"], dev["b_router"], top_k, routing, score_bias, token_mask)
+    res["shape"] = shape
+    res.update(dispatch(shape, res["ids"], res["gates"]))
+    if experts is None:
+        res["y_rows"] = expert_ffn(shape, dev, res["row_token"], res["offsets"])
+    else:
+        res["y_rows"] = expert_ffn_quantized(shape, x, experts, res["row_token"], res["offsets"])
+    res["out"] = combine(shape, x, res["gates"], res["slot_of"], res["y_rows"])
+    return res
+
+
+def combine_backward(shape: B.MoeShape, dout: torch.Tensor, gates: torch.Tensor,
+                     slot_of: torch.Tensor, y_rows: torch.Tensor, want_rows: bool = False) -> dict:
+    """Gradients of the combine: dgates [T, k] and, when want_rows, dy_rows like y_rows (rows that no
+    slot names are zero)."""
+    res = {
+        "dgates": torch.empty((shape.T, shape.top_k), dtype=torch.float32, device=dout.device),
+        "dy_rows": torch.zeros_like(y_rows) if want_rows else None,
+    }
+    B.moe_combine_backward(shape, dout, gates, slot_of, y_rows, dgates=res["dgates"],
+                           dy_rows=res["dy_rows"])
+    return res
+
+
+def route_scored_backward(logits: torch.Tensor, ids: torch.Tensor, dgates: torch.Tensor,
+                          routing: B.MoeRouting, dlogits_add: torch.Tensor | None = None,
+                          token_mask: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits [T, E], which route_backward takes on (its dgates then being None)."""
+    T, E = logits.shape
+    shape = B.make_shape(T, 8, 8, E, ids.shape[1], 0, B.MOE_F32)
+    dlogits = torch.empty_like(logits)
+    B.moe_route_scored_backward(shape, routing, logits, ids, dgates, dlogits,
+                                dlogits_add=dlogits_add, token_mask=token_mask)
+    return dlogits
+
+
+def balance_bias(ids: torch.Tensor, score_bias: torch.Tensor, rate: float,
+                 token_mask: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Moves score_bias [E] towards even counts of ids [T, k], in place; returns the counts [E]."""
+    T, k = ids.shape
+    E = score_bias.numel()
+    shape = B.make_shape(T, 8, 8, E, k, 0, B.MOE_F32)
+    if ws is None:
+        ws = torch.empty(max(B.workspace_bytes_balance_bias(shape), 256), dtype=torch.uint8,
+                         device=score_bias.device)
+    counts = torch.empty((E,), dtype=torch.int32, device=score_bias.device)
+    B.moe_balance_bias(shape, rate, score_bias, counts, topk_ids=ids, token_mask=token_mask, ws=ws)
+    return counts
+
+
+# ---------------------------------------------------------------- AdamW
+class AdamW:
+    """AdamW over a list of tensors, all fp32 or all bf16, with moments of 32 or 8 bits that start at
+    zero.  copies: bf16 tensors (or None entries) that receive the new fp32 params, for the forward
+    pass."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, state_bits: int = 32, copies=None):
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits is {state_bits}, not 8 or 32")
+        self.lr, self.betas, self.eps, self.steps = lr, betas, eps, 0
+        like = lambda dt: [torch.zeros(p.numel(), dtype=dt, device=p.device) for p in params]
+        steps = lambda: [torch.zeros((p.numel() + 255) // 256, device=p.device) for p in params]
+        q = state_bits == 8
+        self.m, self.v = like(torch.int8 if q else torch.float32), like(torch.uint8 if q else torch.float32)
+        self.m_steps, self.v_steps = (steps(), steps()) if q else (None, None)
+        self.params, self.copies, self.weight_decay = list(params), copies, weight_decay
+        self.tensors = None
+
+    def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
+        """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
+        takes their places, for a captured step."""
+        if self.tensors is None:
+            self.tensors = B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
+                                          v_steps=self.v_steps, copies=self.copies,
+                                          weight_decay=self.weight_decay)
+        elif any(a is not b for a, b in zip(grads, self.tensors.grads)) or len(grads) != self.tensors.n:
+            self.tensors.set_grads(grads)
+        B.moe_adamw_step(self.tensors, self.lr, *self.betas, self.eps, self.steps + 1,
+                         grad_scale=grad_scale, dynamic=dynamic)
+        self.steps += 1
+
+    def moments(self) -> tuple:
+        """The fp32 moments, two lists."""
+        m, v = ([torch.empty(p.numel(), device=p.device) for p in self.params] for _ in range(2))
+        if self.tensors is None:
+            return [x.zero_() for x in m], [x.zero_() for x in v]
+        B.moe_adamw_moments(self.tensors, m, v)
+        return m, v

@@ -27,8 +27,8 @@
  *     device fault shows up at the caller's next synchronisation.
  *   - Arguments are checked on the host before anything is enqueued; on any non-OK status
  *     no output has been touched.  moe_last_error() then gives a one-line reason.
- *   - T == 0 is valid and enqueues nothing (moe_balance_loss and moe_route_backward write the
- *     zeros that their sums over no tokens are).
+ *   - T == 0 is valid and enqueues nothing (moe_balance_loss, moe_route_backward and
+ *     moe_balance_bias write the zeros that their sums over no tokens are).
  *   - Calls that share a workspace must not overlap (same stream, or ordered by events).
  *   - Layouts: W_r [E, d_model]; W1 [E, d_ff, d_model]; b1 [E, d_ff]; W2 [E, d_model, d_ff];
  *     b2 [E, d_model]; x and out [T, d_model]; per-assignment arrays [T, top_k], with
@@ -544,6 +544,165 @@ moe_status moe_route_backward(const moe_shape* shape, const void* x, const void*
                               const float* dlogits, const uint8_t* token_mask, const void* dx_add,
                               void* dx, float* dw_router, float* db_router, void* ws,
                               size_t ws_bytes, moe_stream_t stream);
+
+/* ---- Routing by scores.  "Expert Networks": routing collapses onto few experts unless something
+ * spreads the tokens.  Here that is a bias on the choice alone: the gates come from the unbiased
+ * scores, and moe_balance_bias moves the bias after each batch, with no loss and no gradient. */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP_TWO = 1 } moe_group_score;
+
+typedef struct {
+  int32_t score;       /* moe_score: s = softmax(l) over all E experts, or 1 / (1 + e^-l) */
+  int32_t n_groups;    /* groups of E / n_groups consecutive experts; 1: no groups */
+  int32_t topk_groups; /* groups that a token's experts are taken from */
+  int32_t group_score; /* moe_group_score: the largest biased score, or the sum of the two largest */
+  int32_t renormalize; /* 1: a token's gates are divided by the sum of its chosen scores */
+  float scale;         /* factor of the gates */
+} moe_routing;
+
+/* Workspace bytes for moe_route_scored (at most 64 MiB); 0 for an invalid shape. */
+size_t moe_workspace_bytes_route_scored(const moe_shape* shape);
+
+/* moe_route with other scores.  With l = W_r x + b_r and s the scores of l, an expert is chosen by
+ * a = fl32(s) + score_bias (one fp32 addition): of the groups, the topk_groups with the best group
+ * score; of their experts, the top_k with the largest a.  Ties go to the lower group and expert.
+ *   score_bias [E] fp32 or NULL (zeros).  -inf takes an expert out: it is never chosen and counts in
+ *              no group's score (one expert that is on speaks for its group alone)
+ *   token_mask [T] uint8 or NULL: 0 marks a token that is not there (padding): ids -1, gates 0,
+ *              logits 0
+ *   topk_ids   [T, k] int32 out, the largest a first; -1 where fewer than k experts are on
+ *   topk_gates [T, k] fp32 out: scale * s, or scale * s / (sum of the token's chosen s); 0 at id -1
+ *   logits     [T, E] fp32 or NULL out: l rounded to fp32 (moe_route_scored_backward takes them)
+ * Other arguments as moe_route, whose results these are with softmax, one group, no bias and no
+ * renormalising.  moe_dispatch takes ids and gates as they are: an id of -1 is dropped and not counted.
+ * Logits and scores are evaluated in fp64 and gates rounded once.  Renormalised gates are the ratios
+ * of the scores as real numbers, also where a score is below fp64's range; they are 0 where every
+ * chosen score is 0 (logits of -inf).  A softmax row of nothing but -inf has scores 0.  A NaN score or
+ * bias is above every number in the choice, and reaches the gates.
+ * Errors: MOE_ERR_INVALID_ARGUMENT also for n_groups that does not divide E, topk_groups not in
+ * [1, n_groups], top_k > topk_groups * E / n_groups, a scale that is not positive and finite, unknown
+ * enum values; MOE_ERR_UNSUPPORTED when w_router reaches 2 GiB. */
+moe_status moe_route_scored(const moe_shape* shape, const moe_routing* routing, const void* x,
+                            const void* w_router, const float* b_router, const float* score_bias,
+                            const uint8_t* token_mask, int32_t* topk_ids, float* topk_gates,
+                            float* logits, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Backward pass of moe_route_scored's gates down to the logits; moe_route_backward (dgates NULL,
+ * dlogits this one's) takes them on to x, W_r and b_r.  The choice is a constant of the gradient.
+ *   logits      [T, E] fp32 in (moe_route_scored's).  Only a softmax that is not renormalised reads
+ *               whole rows, the others read the chosen entries
+ *   topk_ids    [T, k] int32 in; an id outside [0, E) takes no gradient (and has no share of a
+ *               renormalised sum), an id that a token holds twice takes both
+ *   dgates      [T, k] fp32 in: gradient on topk_gates (zero where the assignment dropped)
+ *   dlogits_add [T, E] fp32 in or NULL: a gradient that dlogits is added to (moe_balance_loss); may
+ *               be dlogits itself, must not overlap it otherwise
+ *   token_mask  [T] uint8 or NULL: 0 marks a token that is not there; nothing of its rows is read, its
+ *               dlogits row is zero
+ *   dlogits     [T, E] fp32 out; must not overlap logits
+ * fp32 throughout.  Reads shape->T, n_experts and top_k, routing->score, renormalize and scale.  Equal
+ * calls give equal bits.  T == 0 enqueues nothing. */
+moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* routing,
+                                     const float* logits, const int32_t* topk_ids,
+                                     const float* dgates, const float* dlogits_add,
+                                     const uint8_t* token_mask, float* dlogits,
+                                     moe_stream_t stream);
+
+/* Backward pass of moe_combine: where the gradient on the gates comes from.
+ *   dgates[t, c]  = sum_j dout[t, j] y_rows[slot, j], 0 for a dropped choice
+ *   dy_rows[slot] = topk_gates[t, c] * dout[t]
+ * (the residual's part of dx is dout itself).
+ *   dout       [T, d_model] dtype in: gradient on moe_combine's out
+ *   topk_gates [T, k] fp32 in; NULL without dy_rows
+ *   slot_of    [T, k] int32 in, as moe_combine takes it (either layout), -1 for dropped; no two
+ *              assignments share a slot
+ *   y_rows     [rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates
+ *   dgates     [T, k] fp32 out or NULL
+ *   dy_rows    [rows, d_model] dtype out or NULL; rows that no slot names are left as they are.  May be
+ *              y_rows itself, must not overlap it otherwise, nor dout
+ * At least one output is given.  Products are summed in fp32 in a fixed order: equal calls give equal
+ * bits.  T == 0 enqueues nothing. */
+moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const float* topk_gates,
+                                const int32_t* slot_of, const void* y_rows, float* dgates,
+                                void* dy_rows, moe_stream_t stream);
+
+/* Workspace bytes for moe_balance_bias; 0 for an invalid shape, and where it needs none. */
+size_t moe_workspace_bytes_balance_bias(const moe_shape* shape);
+
+/* Update of the selection bias after a batch: with c_e assignments to expert e, over the n experts
+ * that are on (bias not -inf) and the total of their counts,
+ *   score_bias[e] += rate where n c_e < total, -= rate where n c_e > total
+ * compared in whole numbers; an expert that is off stays off.
+ *   topk_ids      [T, k] int32 in: counted here, an id outside [0, E) is not.  NULL: expert_counts
+ *                 holds the counts (summed over several batches or GPUs), token_mask and T are not
+ *                 looked at
+ *   token_mask    [T] uint8 or NULL: 0 marks a token whose ids are not counted
+ *   rate          >= 0 and finite
+ *   score_bias    [E] fp32 in and out
+ *   expert_counts [E] int32 out, or NULL; in if topk_ids is NULL, where all counts are below 2^31
+ * Reads shape->T, n_experts and top_k; T == 0 writes counts of zero and leaves the bias. */
+moe_status moe_balance_bias(const moe_shape* shape, const int32_t* topk_ids,
+                            const uint8_t* token_mask, float rate, float* score_bias,
+                            int32_t* expert_counts, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
+
+/* ---- AdamW over many tensors at once: what the gradients are for.  Per element, in fp32:
+ *   g' = grad_scale * grad;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   param = param - lr wd param - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * m and v take the operations as written, each rounded to fp32: products before sums, 1 - beta an fp32
+ * number.
+ * 8 bits: blocks of 256 consecutive elements of a tensor have one fp32 step for m and one for r =
+ * sqrt(v).  m's code c (int8, -127 .. 127) stands for c |c| step, v's (uint8) for (c^2 step)^2.  Stored
+ * are step = max |m| / 16129 and max r / 65025, and c = floor(sqrt(|m| / step) + 1/2) with m's sign (r
+ * alike, at least 1 where r > 0), each operation rounded to fp32; the update itself takes m and v
+ * before they are stored.  A block that an infinity or a NaN gets into has no finite value left.  All
+ * zeros are the state before the first step, in both forms. */
+
+typedef struct {
+  void* param;         /* [n] param_dtype, in and out */
+  const void* grad;    /* [n] grad_dtype */
+  void* m;             /* [n] fp32, or int8 codes */
+  void* v;             /* [n] fp32, or uint8 codes */
+  float* m_steps;      /* [ceil(n / 256)] at 8 bits, NULL at 32 */
+  float* v_steps;
+  void* copy;          /* [n] bf16 out or NULL: the new param rounded (fp32 params only) */
+  int64_t n;           /* elements; 0: nothing of the entry is looked at */
+  float weight_decay;  /* wd, >= 0 */
+} moe_adamw_tensor;
+
+typedef struct {
+  int32_t param_dtype; /* moe_dtype; bf16 params are rounded to nearest after every step */
+  int32_t grad_dtype;  /* moe_dtype */
+  int32_t state_bits;  /* 32 or 8 */
+  float lr;            /* >= 0 */
+  float beta1, beta2;  /* in [0, 1) */
+  float eps;           /* > 0 */
+  float grad_scale;    /* finite */
+  int64_t step;        /* number of this step, from 1 */
+  const float* dynamic; /* NULL, or [4] on the device: lr, grad_scale, step, skip take the place of
+                           the fields above (which are not looked at), read when the kernels run, so
+                           that a captured step goes on counting.  A step below 1 counts as 1; with
+                           skip other than 0 nothing is written.  fp32 counts to 2^24 steps */
+} moe_adamw_config;
+
+/* Whether the tensors of a list are apart: MOE_OK, or MOE_ERR_INVALID_ARGUMENT if something that a
+ * step writes overlaps anything else of the list; and the checks of moe_adamw_step.  Host only, a
+ * sort of up to 7 ranges a tensor; to be called when a list is made, not every step. */
+moe_status moe_adamw_check(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                           int32_t n_tensors);
+
+/* One step.  `tensors` is a host array, not kept after the call; arrays need their element's alignment
+ * (16-byte alignment, 8 for bf16 and 4 for codes, is faster).  The tensors must be apart
+ * (moe_adamw_check).  n < 2^36 a tensor. */
+moe_status moe_adamw_step(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                          int32_t n_tensors, moe_stream_t stream);
+
+/* The fp32 moments that the states stand for: m_out[i] and v_out[i] (host arrays of device pointers;
+ * an array or an entry may be NULL) receive [n] fp32 each.  Of config only state_bits is read, of the
+ * tensors m, v, the steps and n.  Outputs must not overlap the states. */
+moe_status moe_adamw_moments(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
+                             int32_t n_tensors, float* const* m_out, float* const* v_out,
+                             moe_stream_t stream);
 
 #ifdef __cplusplus
 }
