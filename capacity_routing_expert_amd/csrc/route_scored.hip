@@ -20,12 +20,33 @@ namespace moe {
 
 namespace {
 
+// 8 fp32 columns as two 16-byte loads (d % 4 == 0, arrays on 4 bytes)
+struct Chunk8F4 {
+  uint4 v[2];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, bool ok, int64_t row, int c, int d) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = c * 8 + h * 4;
+      v[h] = buffer_load16(m, ok && col < d ? (uint32_t)((row * d + col) * 4) : kBufferOOR);
+    }
+  }
+  __device__ __forceinline__ void widen(double* o) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      o[4 * h] = __uint_as_float(v[h].x);
+      o[4 * h + 1] = __uint_as_float(v[h].y);
+      o[4 * h + 2] = __uint_as_float(v[h].z);
+      o[4 * h + 3] = __uint_as_float(v[h].w);
+    }
+  }
+};
+
 // ---------------------------------------------------------------- partial logits
 // A block of WD x WE waves takes 16 R tokens and 16 EBG WE experts: wave (wd, we) takes expert tiles
 // we EBG .. of them and every (S WD)-th quad of 32 columns from quad split WD + wd on.  The waves of
 // one we are added in the order of wd, so equal calls give equal bits.  Lane layout of the operands
 // and results as in k_route_mfma.
-template <typename TIn, int R, int EBG, int WD, int WE>
+template <typename TIn, typename Chunk, int R, int EBG, int WD, int WE>
 __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
     const TIn* __restrict__ x, const TIn* __restrict__ w, int64_t T, int d, int E, int S,
     int64_t tok_base, int64_t n_tok, double* __restrict__ part) {
@@ -47,7 +68,7 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int b = 0; b < EBG; ++b) acc[r][b] = f64x4_t{0.0, 0.0, 0.0, 0.0};
-  Chunk8<TIn> xr[R], wr[EBG];
+  Chunk xr[R], wr[EBG];
   auto load = [&](int cq) {
     const int c = cq * 4 + q;
 #pragma unroll
@@ -143,147 +164,200 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // one that choice c took.
 constexpr uint32_t kLeastKey = 0x00800000u;
 
-// Reductions over a row of 16 lanes, in the order xor 8, 4, 2, 1; every lane gets the result.
-template <typename Op>
-__device__ __forceinline__ double row16(double v, Op op) {
-#pragma unroll
-  for (int s = 8; s >= 1; s >>= 1)
-    v = op(v, __longlong_as_double((long long)xor_partner((uint64_t)__double_as_longlong(v), s)));
-  return v;
-}
-__device__ __forceinline__ uint64_t row16_max(uint64_t v) {
-#pragma unroll
-  for (int s = 8; s >= 1; s >>= 1) {
-    const uint64_t o = xor_partner(v, s);
-    v = o > v ? o : v;
+// The lanes that hold a token: 16 (a DPP row, for up to 32 experts) or the whole wave.  sum and max in a
+// fixed order, every lane gets the result.
+template <int LPT>
+struct Lanes {
+  static __device__ __forceinline__ double partner(double v, int s) {
+    return __longlong_as_double((long long)xor_partner((uint64_t)__double_as_longlong(v), s));
   }
-  return v;
+  static __device__ __forceinline__ double sum(double v) {
+#pragma unroll
+    for (int s = 1; s < LPT; s <<= 1) v += partner(v, s);
+    return v;
+  }
+  static __device__ __forceinline__ double max(double v) {  // leaves NaN out
+#pragma unroll
+    for (int s = 1; s < LPT; s <<= 1) v = fmax(v, partner(v, s));
+    return v;
+  }
+  static __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+    auto take = [&](uint32_t o) { v = o > v ? o : v; };
+    take(dpp32<0xB1>(v));
+    take(dpp32<0x4E>(v));
+    take(dpp32<0x141>(v));
+    take(dpp32<0x140>(v));
+    return v;
+  }
+  // the largest key of the token's lanes, and the lowest lane (of LPT) that has it
+  static __device__ __forceinline__ uint32_t best(uint32_t v, int& lane) {
+    uint32_t m = row_max_u32(v);
+    const int here = threadIdx.x & 63;
+    if constexpr (LPT == 64) {
+      const uint32_t a = __builtin_amdgcn_readlane(m, 0), b = __builtin_amdgcn_readlane(m, 16);
+      const uint32_t c = __builtin_amdgcn_readlane(m, 32), d = __builtin_amdgcn_readlane(m, 48);
+      const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
+      m = ab > cd ? ab : cd;
+      lane = __ffsll((long long)__ballot(v == m)) - 1;
+    } else {
+      const uint64_t row = __ballot(v == m) >> (here & 48);
+      lane = __ffs((int)(row & 0xFFFFu)) - 1;
+    }
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t from(uint32_t v, int lane) {
+    if constexpr (LPT == 64) return __builtin_amdgcn_readlane(v, __builtin_amdgcn_readfirstlane(lane));
+    return (uint32_t)__shfl((int)v, lane, LPT);
+  }
+};
+
+// The two largest keys of two pairs (best >= second).
+__device__ __forceinline__ void two_largest(uint32_t& best, uint32_t& second, uint32_t b2, uint32_t s2) {
+  const uint32_t low = best < b2 ? best : b2, high = second > s2 ? second : s2;
+  best = best > b2 ? best : b2;
+  second = low > high ? low : high;
+}
+// one expert that is on speaks for its group alone; a group without any is the last
+__device__ __forceinline__ uint32_t group_key(uint32_t best, uint32_t second, int top2) {
+  return top2 && second ? order_key(key_value(best) + key_value(second)) : best;
 }
 
-// 16 lanes a token, lane l of them holds experts l, l + 16, ... (NV of them).  The lanes of a token
-// share its row of keys in LDS only where there are groups.
-template <int NV>
+// LPT lanes a token, lane l of them holds experts l NV .. l NV + NV - 1, so that the lowest expert of
+// equal ones is the lowest lane's first.  Groups that are a power of two of a wave's lanes are
+// reduced by lane moves, others through LDS ([tokens of the block][E + n_groups] keys).
+template <int LPT, int NV>
 __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
-  extern __shared__ uint32_t shared_keys[];  // groups: [16 tokens][E + n_groups]
-  const int l = threadIdx.x & 15, row = threadIdx.x >> 4;
-  const int64_t t = (int64_t)blockIdx.x * 16 + row;
+  using W = Lanes<LPT>;
+  constexpr int TPB = 256 / LPT;
+  extern __shared__ uint32_t shared_keys[];
+  const int l = threadIdx.x % LPT, row = threadIdx.x / LPT;
+  const int64_t t = (int64_t)blockIdx.x * TPB + row;
   const bool there = t < a.n_tok;
   const int64_t tt = a.tok_base + t;
   const bool real = there && (!a.mask || a.mask[tt]);
-  const int E = a.E, k = a.k;
-  auto add = [](double u, double v) { return u + v; };
-  auto larger = [](double u, double v) { return fmax(u, v); };
+  const int E = a.E, k = a.k, e0 = l * NV;
+  const int lanes = (E + NV - 1) / NV;  // that hold experts
 
+  // Loads past E or the tokens take the last expert's or the first token's in their place, and need no
+  // branch that would have to be waited for.
   double z[NV];
+  float sb[NV];
+  const double* part = a.part + (there ? t * E : 0);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) z[i] = 0.0;
-  if (real) {
-    const double* p = a.part + t * E;
-    for (int s = 0; s < a.S; ++s, p += a.n_tok * E)
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * 16 + l < E) z[i] += p[i * 16 + l];
-    if (a.b_router)
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * 16 + l < E) z[i] += (double)a.b_router[i * 16 + l];
+  for (int i = 0; i < NV; ++i) {
+    const int e = e0 + i < E ? e0 + i : E - 1;
+    z[i] = part[e];
+    sb[i] = a.score_bias ? a.score_bias[e] : 0.0f;
   }
+  if (a.S > 1) {
+#pragma unroll 7
+    for (int s = 1; s < a.S; ++s)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        z[i] += part[(int64_t)s * a.n_tok * E + (e0 + i < E ? e0 + i : E - 1)];
+  }
+  if (a.b_router)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] += (double)a.b_router[e0 + i < E ? e0 + i : E - 1];
   if (there && a.logits)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i * 16 + l < E) a.logits[tt * E + i * 16 + l] = (float)z[i];
+      if (e0 + i < E) a.logits[tt * E + e0 + i] = real ? (float)z[i] : 0.0f;
 
-  // scores in place of the logits: p[i], 0 past E
-  double p[NV];
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] = i * 16 + l < E ? 1.0 / (1.0 + exp(-z[i])) : 0.0;
-  } else {
-    double m = -INFINITY;
+  // scores: e^-l gives 1 / (1 + e^-l), e^(l - m) its share of the sum; 0 past E
+  double m = 0.0;
+  if (!a.sigmoid) {
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i * 16 + l < E) m = fmax(m, z[i]);
-    m = row16(m, larger);
+      if (e0 + i < E) m = fmax(m, z[i]);
+    m = W::max(m);
     if (m == -INFINITY) m = 0.0;  // nothing but -inf (and NaN, which fmax leaves out): zeros
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      p[i] = i * 16 + l < E ? exp(z[i] - m) : 0.0;
-      sum += p[i];
-    }
-    sum = row16(sum, add);
-    if (sum == 0.0) sum = 1.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] = p[i] / sum;
   }
-
+  double p[NV], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    p[i] = e0 + i < E ? exp(a.sigmoid ? -z[i] : z[i] - m) : 0.0;
+    sum += p[i];
+  }
+  if (!a.sigmoid) {
+    sum = W::sum(sum);
+    if (sum == 0.0) sum = 1.0;
+  }
   uint32_t key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = i * 16 + l;
-    key[i] = 0;
-    if (e < E) {
-      float v = (float)p[i];
-      bool off = false;
-      if (a.score_bias) {
-        const float b = a.score_bias[e];
-        off = b == -INFINITY;
-        v += b;
-      }
-      if (!off) key[i] = order_key(v);
-    }
+    p[i] = a.sigmoid ? 1.0 / (1.0 + p[i]) : p[i] / sum;
+    const bool on = e0 + i < E && sb[i] != -INFINITY;
+    // the bias is added also where there is none: a score is no -0
+    key[i] = on ? order_key((float)p[i] + sb[i]) : 0u;
   }
 
   if (a.topk_groups < a.n_groups) {  // uniform over the grid
-    const int G = a.n_groups, gs = E / G;
-    uint32_t* keys = shared_keys + row * (E + G);
-    uint32_t* group = keys + E;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * 16 + l < E) keys[i * 16 + l] = key[i];
-    __syncthreads();
-    for (int g = l; g < G; g += 16) {
+    const int G = a.n_groups, gs = E / G, lpg = gs / NV;  // lanes a group
+    if (LPT == 64 && lpg * NV == gs && (lpg & (lpg - 1)) == 0) {
       uint32_t best = 0, second = 0;
-      for (int j = 0; j < gs; ++j) {
-        const uint32_t v = keys[g * gs + j];
-        const uint32_t low = v < best ? v : best;
-        best = v > best ? v : best;
-        second = low > second ? low : second;
-      }
-      // one expert that is on speaks for its group alone; a group without any is the last
-      group[g] = a.top2 && second ? order_key(key_value(best) + key_value(second)) : best;
-    }
-    __syncthreads();
-    // a group stays if fewer than topk_groups are better (or as good and before it)
-    for (int g = l; g < G; g += 16) {
-      const uint32_t mine = group[g];
-      int better = 0;
-      for (int o = 0; o < G; ++o) better += group[o] > mine || (group[o] == mine && o < g);
-      keys[g] = better < a.topk_groups;  // the experts' keys are in registers
-    }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * 16 + l < E && !keys[(i * 16 + l) / gs]) key[i] = 0;
+      for (int i = 0; i < NV; ++i) two_largest(best, second, key[i], 0u);
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1)
+        if (s < lpg) {
+          const uint64_t o = xor_partner(((uint64_t)best << 32) | second, s);
+          two_largest(best, second, (uint32_t)(o >> 32), (uint32_t)o);
+        }
+      const uint32_t mine = group_key(best, second, a.top2);
+      // a group stays if fewer than topk_groups are better (or as good and before it)
+      const int g = l / lpg;
+      int better = 0;
+      for (int o = 0; o < G; ++o) {
+        const uint32_t other = __builtin_amdgcn_readlane(mine, o * lpg);
+        better += other > mine || (other == mine && o < g);
+      }
+      if (better >= a.topk_groups)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = 0;
+    } else {
+      uint32_t* keys = shared_keys + row * (E + G);
+      uint32_t* group = keys + E;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (e0 + i < E) keys[e0 + i] = key[i];
+      __syncthreads();
+      for (int g = l; g < G; g += LPT) {
+        uint32_t best = 0, second = 0;
+        for (int j = 0; j < gs; ++j) two_largest(best, second, keys[g * gs + j], 0u);
+        group[g] = group_key(best, second, a.top2);
+      }
+      __syncthreads();
+      for (int g = l; g < G; g += LPT) {
+        const uint32_t mine = group[g];
+        int better = 0;
+        for (int o = 0; o < G; ++o) better += group[o] > mine || (group[o] == mine && o < g);
+        keys[g] = better < a.topk_groups;  // the experts' keys are in registers
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (e0 + i < E && !keys[(e0 + i) / gs]) key[i] = 0;
+    }
   }
 
   int taken = 0;
   if (real)
     for (; taken < k; ++taken) {
-      uint32_t best = 0, at = 0;
+      uint32_t best = key[0], at = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 1; i < NV; ++i)
         if (key[i] > best) {
           best = key[i];
           at = i;
         }
-      const uint64_t win =
-          row16_max(((uint64_t)best << 32) | (0xFFFFFFFFu - (at * 16 + (uint32_t)l)));
-      if ((uint32_t)(win >> 32) < kLeastKey) break;  // all 16 lanes agree
-      const uint32_t e = 0xFFFFFFFFu - (uint32_t)win;
+      int lane;
+      if (W::best(l < lanes ? best : 0u, lane) < kLeastKey) break;  // all lanes of the token agree
+      if (l == lane)
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (e == (uint32_t)(i * 16 + l)) key[i] = 1 + taken;
+        for (int i = 0; i < NV; ++i)
+          if (at == (uint32_t)i) key[i] = 1 + taken;
     }
   if (!there) return;
 
@@ -294,15 +368,15 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (chosen(i)) total += p[i];
-    total = row16(total, add);
+    total = W::sum(total);
     // Scores that the range of fp64 has lost, or nearly: e^l instead, from the largest chosen logit
     // (1 + e^l is 1 there); all of them zero (-inf): the gates are zero.
     if (total < 1e-280) {
-      double m = -INFINITY;
+      m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (chosen(i)) m = fmax(m, z[i]);
-      m = row16(m, larger);
+      m = W::max(m);
       if (m == -INFINITY) m = 0.0;
       total = 0.0;
 #pragma unroll
@@ -311,7 +385,7 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
           p[i] = exp(z[i] - m);
           total += p[i];
         }
-      total = row16(total, add);
+      total = W::sum(total);
       if (total == 0.0) total = 1.0;
     }
   }
@@ -319,10 +393,10 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
   for (int i = 0; i < NV; ++i)
     if (chosen(i)) {
       const int64_t at = tt * k + (key[i] - 1);
-      a.ids[at] = i * 16 + l;
+      a.ids[at] = e0 + i;
       a.gates[at] = (float)(a.scale * (p[i] / total));
     }
-  for (int c = taken + l; c < k; c += 16) {  // masked, or too few experts are on
+  for (int c = taken + l; c < k; c += LPT) {  // masked, or too few experts are on
     a.ids[tt * k + c] = -1;
     a.gates[tt * k + c] = 0.0f;
   }
@@ -356,37 +430,37 @@ Plan plan(const moe_shape& s) {
   return p;
 }
 
-template <typename TIn, int R, int EBG, int WD, int WE>
+template <typename TIn, typename Chunk, int R, int EBG, int WD, int WE>
 hipError_t launch_logits(const moe_shape& s, const TIn* x, const TIn* w, const Plan& p,
                          int64_t base, int64_t n, double* part, hipStream_t st) {
   const dim3 grid((unsigned)((n + 16 * R - 1) / (16 * R)),
                   (unsigned)((s.n_experts + 16 * EBG * WE - 1) / (16 * EBG * WE)), (unsigned)p.S);
-  hipLaunchKernelGGL((k_scored_logits<TIn, R, EBG, WD, WE>), grid, dim3(64 * WD * WE), 0, st, x, w,
+  hipLaunchKernelGGL((k_scored_logits<TIn, Chunk, R, EBG, WD, WE>), grid, dim3(64 * WD * WE), 0, st, x, w,
                      s.T, s.d_model, s.n_experts, p.S, base, n, part);
   return hipGetLastError();
 }
 
-template <typename TIn>
-hipError_t logits_any(const moe_shape& s, const TIn* x, const TIn* w, const Plan& p, int64_t base,
+template <typename TIn, typename Chunk>
+hipError_t logits_any(const moe_shape& s, const void* x, const void* w, const Plan& p, int64_t base,
                       int64_t n, double* part, hipStream_t st) {
-  if (!p.large) return launch_logits<TIn, 1, 1, 8, 1>(s, x, w, p, base, n, part, st);
-  if (s.n_experts <= 16) return launch_logits<TIn, 2, 1, 4, 1>(s, x, w, p, base, n, part, st);
-  if (s.n_experts <= 32) return launch_logits<TIn, 2, 2, 4, 1>(s, x, w, p, base, n, part, st);
-  return launch_logits<TIn, 2, 2, 4, 2>(s, x, w, p, base, n, part, st);
+  const TIn *xi = (const TIn*)x, *wi = (const TIn*)w;
+  if (!p.large) return launch_logits<TIn, Chunk, 1, 1, 8, 1>(s, xi, wi, p, base, n, part, st);
+  if (s.n_experts <= 16) return launch_logits<TIn, Chunk, 2, 1, 4, 1>(s, xi, wi, p, base, n, part, st);
+  if (s.n_experts <= 32) return launch_logits<TIn, Chunk, 2, 2, 4, 1>(s, xi, wi, p, base, n, part, st);
+  return launch_logits<TIn, Chunk, 2, 2, 4, 2>(s, xi, wi, p, base, n, part, st);
 }
 
 hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.n_tok + 15) / 16));
-  const size_t lds = a.topk_groups < a.n_groups ? (size_t)16 * 4 * (a.E + a.n_groups) : 0;
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, grid, dim3(256), lds, st, a);
+  auto go = [&](auto kern, int tokens) {
+    const size_t lds = a.topk_groups < a.n_groups ? (size_t)tokens * 4 * (a.E + a.n_groups) : 0;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((a.n_tok + tokens - 1) / tokens)), dim3(256), lds, st, a);
     return hipGetLastError();
   };
-  if (a.E <= 16) return go(k_scored_choose<1>);
-  if (a.E <= 32) return go(k_scored_choose<2>);
-  if (a.E <= 64) return go(k_scored_choose<4>);
-  if (a.E <= 128) return go(k_scored_choose<8>);
-  return go(k_scored_choose<16>);
+  if (a.E <= 16) return go(k_scored_choose<16, 1>, 16);
+  if (a.E <= 32) return go(k_scored_choose<16, 2>, 16);
+  if (a.E <= 64) return go(k_scored_choose<64, 1>, 4);
+  if (a.E <= 128) return go(k_scored_choose<64, 2>, 4);
+  return go(k_scored_choose<64, 4>, 4);
 }
 
 }  // namespace
@@ -404,11 +478,12 @@ hipError_t launch_route_scored(const moe_shape& s, const moe_routing& r, const v
   double* part = (double*)ws;
   for (int64_t base = 0; base < s.T; base += p.chunk) {
     const int64_t n = s.T - base < p.chunk ? s.T - base : p.chunk;
-    hipError_t err = s.dtype == MOE_BF16
-                         ? logits_any<bf16_t>(s, (const bf16_t*)x, (const bf16_t*)w_router, p, base,
-                                              n, part, st)
-                         : logits_any<float>(s, (const float*)x, (const float*)w_router, p, base, n,
-                                             part, st);
+    hipError_t err =
+        s.dtype == MOE_BF16
+            ? logits_any<bf16_t, Chunk8<bf16_t>>(s, x, w_router, p, base, n, part, st)
+        : s.d_model % 4 == 0
+            ? logits_any<float, Chunk8F4>(s, x, w_router, p, base, n, part, st)
+            : logits_any<float, Chunk8<float>>(s, x, w_router, p, base, n, part, st);
     if (err != hipSuccess) return err;
     ChooseArgs a{part, p.S, base, n, s.n_experts, s.top_k, r.score == MOE_SCORE_SIGMOID,
                  r.n_groups, r.topk_groups, r.group_score == MOE_GROUP_TOP_TWO, r.renormalize,

@@ -249,6 +249,26 @@ def test_masked_tokens_are_not_looked_at():
     assert np.all(none[0] == -1) and np.all(none[1] == 0)
 
 
+@pytest.mark.parametrize("T,d,E", [(70, 72, 20), (4200, 36, 40), (33, 35, 9)])
+def test_f32_arrays_on_4_bytes(T, d, E):
+    """fp32 x, W_r and the other arrays off 16 bytes give the bits of the aligned call."""
+    x, w, b, bias = [t.to(DEV) for t in make(T, d, E, "f32", seed=8)]
+    shape, r = B.make_shape(T, d, 8, E, 3, 0, B.MOE_F32), B.make_routing("sigmoid", renormalize=True)
+    mask = (torch.arange(T, device=DEV) % 5 > 0).to(torch.uint8)
+    ws = torch.empty(B.workspace_bytes_route_scored(shape), dtype=torch.uint8, device=DEV)
+    outs = []
+    for n in range(4):
+        o = [shifted(torch.full((T, 3), 7, dtype=torch.int32, device=DEV), n),
+             shifted(torch.full((T, 3), 7.0, device=DEV), n), shifted(torch.full((T, E), 7.0, device=DEV), n)]
+        B.moe_route_scored(shape, r, shifted(x, n), shifted(w, n), shifted(b, n), shifted(bias, n), o[0], o[1],
+                           logits=o[2], token_mask=shifted(mask, n), ws=ws)
+        outs.append(o)
+    z, noise = logits_ref(x.cpu(), w.cpu(), b.cpu())
+    z[mask.cpu().numpy() == 0] = 0.0
+    assert np.all(np.abs(outs[0][2].double().cpu().numpy() - z) <= U * np.abs(z) + noise)
+    assert all(torch.equal(p, q) for o in outs[1:] for p, q in zip(o, outs[0]))
+
+
 def test_more_tokens_than_a_chunk():
     """The workspace bounds how many tokens go through at a time; past that, chunks."""
     T, E, d, k = 40000, 256, 8, 8
