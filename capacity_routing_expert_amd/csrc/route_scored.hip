@@ -13,42 +13,86 @@
 //
 // Two launches.  k_scored_logits leaves partial logits (fp64, [split][token][expert]) of 16 or 32
 // tokens and 16 to 64 experts a block on v_mfma_f64_16x16x4f64; k_scored_choose adds the splits and
-// does the rest with 16 lanes a token.  Tokens go through both in chunks, which bounds the workspace.
-#include "route_chunks.h"
+// does the rest with a wave a token (16 lanes up to 32 experts).  Tokens go through both in chunks,
+// which bounds the workspace.
+#include <algorithm>
+
+#include "moe_internal.h"
 
 namespace moe {
 
 namespace {
 
-// 8 fp32 columns as two 16-byte loads (d % 4 == 0, arrays on 4 bytes)
-struct Chunk8F4 {
-  uint4 v[2];
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, bool ok, int64_t row, int c, int d) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int col = c * 8 + h * 4;
-      v[h] = buffer_load16(m, ok && col < d ? (uint32_t)((row * d + col) * 4) : kBufferOOR);
-    }
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+
+// 8 columns of a token or of an expert, as stored.  A load takes a byte offset of the lane (kBufferOOR:
+// zeros) and one of the wave, so that walking along d costs the vector ALU nothing: it and the fp64
+// matrix instructions take turns.  widen: columns 4 h .. 4 h + 3 in fp64, exactly.
+struct ChunkBf16 {  // d % 8 == 0
+  typedef bf16_t Elem;
+  uint4 v;
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
+                                       int, int) {
+    v = load16(m, lane_off, wave_off);
   }
-  __device__ __forceinline__ void widen(double* o) const {
+  static __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t m, uint32_t lane_off,
+                                                 uint32_t wave_off) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(m, (int)lane_off, (int)wave_off, 0);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
+    const uint32_t a = h ? v.z : v.x, b = h ? v.w : v.y;
+    o[0] = __uint_as_float(a << 16);
+    o[1] = __uint_as_float(a & 0xFFFF0000u);
+    o[2] = __uint_as_float(b << 16);
+    o[3] = __uint_as_float(b & 0xFFFF0000u);
+  }
+};
+struct ChunkF32x4 {  // two 16-byte loads: d % 4 == 0, arrays on 4 bytes
+  typedef float Elem;
+  uint4 v[2];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
+                                       int col, int d) {
+    v[0] = ChunkBf16::load16(m, lane_off, wave_off);
+    v[1] = ChunkBf16::load16(m, col + 4 < d ? lane_off + 16 : kBufferOOR, wave_off);
+  }
+  __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
+    o[0] = __uint_as_float(v[h].x);
+    o[1] = __uint_as_float(v[h].y);
+    o[2] = __uint_as_float(v[h].z);
+    o[3] = __uint_as_float(v[h].w);
+  }
+};
+struct ChunkF32 {  // any d
+  typedef float Elem;
+  float v[8];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
+                                       int col, int d) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      o[4 * h] = __uint_as_float(v[h].x);
-      o[4 * h + 1] = __uint_as_float(v[h].y);
-      o[4 * h + 2] = __uint_as_float(v[h].z);
-      o[4 * h + 3] = __uint_as_float(v[h].w);
-    }
+    for (int u = 0; u < 8; ++u)
+      v[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          m, (int)(col + u < d ? lane_off + 4 * u : kBufferOOR), (int)wave_off, 0));
+  }
+  __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = v[4 * h + u];
   }
 };
 
 // ---------------------------------------------------------------- partial logits
 // A block of WD x WE waves takes 16 R tokens and 16 EBG WE experts: wave (wd, we) takes expert tiles
 // we EBG .. of them and every (S WD)-th quad of 32 columns from quad split WD + wd on.  The waves of
-// one we are added in the order of wd, so equal calls give equal bits.  Lane layout of the operands
-// and results as in k_route_mfma.
-template <typename TIn, typename Chunk, int R, int EBG, int WD, int WE>
+// one we are added in the order of wd, so equal calls give equal bits.  Operands: lane l holds token or
+// expert l % 16 and 8 consecutive columns, 8 (l / 16) of its quad on; instruction s multiplies column s
+// of both, a permutation of the sum's order only.
+// Bound from some thousand tokens on: the fp64 matrix instructions (64 cycles each, 73 TFLOP/s with
+// nothing between) and the conversions, which they do not overlap with: T 65536, E 64, d 2048 281 us, 61
+// TFLOP/s; accumulators in AGPRs would halve the rate.  W_r converted to fp64 by a launch ahead and read
+// in the operands' order: 268 us there, but 73 + 5 against 75 at T 16384.
+template <typename Chunk, int R, int EBG, int WD, int WE>
 __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
-    const TIn* __restrict__ x, const TIn* __restrict__ w, int64_t T, int d, int E, int S,
+    const void* __restrict__ x, const void* __restrict__ w, int64_t T, int d, int E, int S,
     int64_t tok_base, int64_t n_tok, double* __restrict__ part) {
   constexpr int kPart = R * EBG * 256;
   __shared__ double lds[WD > 1 ? (WD - 1) * WE * kPart : 1];
@@ -59,9 +103,10 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
   const int64_t tok0 = (int64_t)blockIdx.x * (16 * R);  // within the chunk
   const int e0 = ((int)blockIdx.y * WE + we) * EBG * 16;
   const int split = blockIdx.z;
-  const int d8 = (d + 7) / 8, nq = (d8 + 3) / 4, stride = S * WD;
-  const __amdgpu_buffer_rsrc_t xs = buffer_rsrc(x, (uint32_t)(T * d * (int64_t)sizeof(TIn)));
-  const __amdgpu_buffer_rsrc_t ws = buffer_rsrc(w, (uint32_t)((int64_t)E * d * sizeof(TIn)));
+  constexpr uint32_t kSize = sizeof(typename Chunk::Elem);
+  const int nq = (d + 31) / 32, stride = S * WD;
+  const __amdgpu_buffer_rsrc_t xs = buffer_rsrc(x, (uint32_t)(T * d * kSize));
+  const __amdgpu_buffer_rsrc_t ws = buffer_rsrc(w, (uint32_t)((int64_t)E * d * kSize));
 
   f64x4_t acc[R][EBG];
 #pragma unroll
@@ -69,35 +114,45 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
 #pragma unroll
     for (int b = 0; b < EBG; ++b) acc[r][b] = f64x4_t{0.0, 0.0, 0.0, 0.0};
   Chunk xr[R], wr[EBG];
-  auto load = [&](int cq) {
-    const int c = cq * 4 + q;
+  uint32_t xo[R], wo[EBG];  // of the lane's columns in quad 0
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t t = tok0 + 16 * r + i;
-      xr[r].load(xs, cq < nq && t < n_tok, tok_base + t, c, d);
-    }
+  for (int r = 0; r < R; ++r) {
+    const int64_t t = tok0 + 16 * r + i;
+    xo[r] = t < n_tok ? (uint32_t)((tok_base + t) * d + q * 8) * kSize : kBufferOOR;
+  }
 #pragma unroll
-    for (int b = 0; b < EBG; ++b) {
-      const int e = e0 + 16 * b + i;
-      wr[b].load(ws, cq < nq && e < E, e, c, d);
-    }
+  for (int b = 0; b < EBG; ++b) {
+    const int e = e0 + 16 * b + i;
+    wo[b] = e < E ? (uint32_t)((int64_t)e * d + q * 8) * kSize : kBufferOOR;
+  }
+  auto load = [&](int cq) {  // columns past d, and whole quads past the last, read as zeros
+    const int col = cq * 32 + q * 8;
+    const uint32_t at = (uint32_t)cq * 32 * kSize;
+#pragma unroll
+    for (int r = 0; r < R; ++r) xr[r].load(xs, col < d ? xo[r] : kBufferOOR, at, col, d);
+#pragma unroll
+    for (int b = 0; b < EBG; ++b) wr[b].load(ws, col < d ? wo[b] : kBufferOOR, at, col, d);
   };
   int cq = split * WD + wd;
   load(cq);
   for (; cq < nq; cq += stride) {
-    double xa[R][8], wb[EBG][8];
+    // half a chunk at a time: 16 registers of widened operands less
 #pragma unroll
-    for (int r = 0; r < R; ++r) xr[r].widen(xa[r]);
+    for (int h = 0; h < 2; ++h) {
+      double xa[R][4], wb[EBG][4];
 #pragma unroll
-    for (int b = 0; b < EBG; ++b) wr[b].widen(wb[b]);
-    load(cq + stride);
+      for (int r = 0; r < R; ++r) xr[r].widen(h, xa[r]);
 #pragma unroll
-    for (int s8 = 0; s8 < 8; ++s8)
+      for (int b = 0; b < EBG; ++b) wr[b].widen(h, wb[b]);
+      if (h == 1) load(cq + stride);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int b = 0; b < EBG; ++b)
-          acc[r][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[r][s8], wb[b][s8], acc[r][b], 0, 0, 0);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int b = 0; b < EBG; ++b)
+            acc[r][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[r][s], wb[b][s], acc[r][b], 0, 0, 0);
+    }
   }
   if constexpr (WD > 1) {
     if (wd > 0) {
@@ -111,6 +166,7 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
     }
     __syncthreads();
     if (wd > 0) return;
+#pragma unroll 1  // all waves' tiles at once would take the registers of a second block on the CU
     for (int o = 1; o < WD; ++o) {
       const double* other = lds + ((o - 1) * WE + we) * kPart;
 #pragma unroll
@@ -137,6 +193,8 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
 }
 
 // ---------------------------------------------------------------- scores and choice
+constexpr int kMaxSplits = 8;
+
 struct ChooseArgs {
   const double* part;  // [S][n_tok][E]
   int S;
@@ -164,22 +222,60 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // one that choice c took.
 constexpr uint32_t kLeastKey = 0x00800000u;
 
+// e^x in fp64 for x from -1100 (0) to 700 (1e304), clamped there; NaN stays NaN.  Reduction by n ln 2 in
+// two parts and the Taylor series to the 13th power on |r| <= ln 2 / 2 (rest 4e-18): 23 operations
+// against some 60 of the general function, which a wave that has little to do waits for one by one.
+__device__ __forceinline__ double exp_clamped(double x) {
+  x = x < -1100.0 ? -1100.0 : x > 700.0 ? 700.0 : x;
+  const double n = rint(x * 1.4426950408889634);
+  double r = fma(n, -0.6931471805599453, x);
+  r = fma(n, -2.3190468138462996e-17, r);
+  double p = 1.0 / 6227020800.0;
+  constexpr double kInverse[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                                 1.0 / 40320.0,     1.0 / 5040.0,     1.0 / 720.0,     1.0 / 120.0,
+                                 1.0 / 24.0,        1.0 / 6.0,        0.5,             1.0,
+                                 1.0};
+#pragma unroll
+  for (int i = 0; i < 13; ++i) p = fma(p, r, kInverse[i]);
+  return ldexp(p, (int)n);
+}
+// 1 / d for finite d >= 1 (or NaN): two steps of Newton's from the instruction's estimate
+__device__ __forceinline__ double reciprocal(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = fma(r, fma(-d, r, 1.0), r);
+  return fma(r, fma(-d, r, 1.0), r);
+}
+
 // The lanes that hold a token: 16 (a DPP row, for up to 32 experts) or the whole wave.  sum and max in a
 // fixed order, every lane gets the result.
 template <int LPT>
 struct Lanes {
-  static __device__ __forceinline__ double partner(double v, int s) {
-    return __longlong_as_double((long long)xor_partner((uint64_t)__double_as_longlong(v), s));
+  template <int CTRL>
+  static __device__ __forceinline__ double moved(double v) {
+    return __longlong_as_double((long long)dpp64<CTRL>((uint64_t)__double_as_longlong(v)));
+  }
+  static __device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)(
+        ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane) << 32) |
+        (uint32_t)__builtin_amdgcn_readlane((int)u, lane)));
+  }
+  // quads, then mirrored halves of a row and mirrored rows, then the wave's four rows
+  template <typename Op>
+  static __device__ __forceinline__ double all(double v, Op op) {
+    v = op(v, moved<0xB1>(v));
+    v = op(v, moved<0x4E>(v));
+    v = op(v, moved<0x141>(v));
+    v = op(v, moved<0x140>(v));
+    if constexpr (LPT == 64)
+      v = op(op(lane_of(v, 0), lane_of(v, 16)), op(lane_of(v, 32), lane_of(v, 48)));
+    return v;
   }
   static __device__ __forceinline__ double sum(double v) {
-#pragma unroll
-    for (int s = 1; s < LPT; s <<= 1) v += partner(v, s);
-    return v;
+    return all(v, [](double a, double b) { return a + b; });
   }
   static __device__ __forceinline__ double max(double v) {  // leaves NaN out
-#pragma unroll
-    for (int s = 1; s < LPT; s <<= 1) v = fmax(v, partner(v, s));
-    return v;
+    return all(v, [](double a, double b) { return fmax(a, b); });
   }
   static __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
     auto take = [&](uint32_t o) { v = o > v ? o : v; };
@@ -249,16 +345,27 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
     z[i] = part[e];
     sb[i] = a.score_bias ? a.score_bias[e] : 0.0f;
   }
-  if (a.S > 1) {
-#pragma unroll 7
-    for (int s = 1; s < a.S; ++s)
+  float rb[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        z[i] += part[(int64_t)s * a.n_tok * E + (e0 + i < E ? e0 + i : E - 1)];
+  for (int i = 0; i < NV; ++i) rb[i] = a.b_router ? a.b_router[e0 + i < E ? e0 + i : E - 1] : 0.0f;
+  if (a.S > 1) {
+    // all splits' loads before the first sum: the compiler on its own waits for one after the other
+    double v[kMaxSplits - 1][NV];
+#pragma unroll
+    for (int s = 1; s < kMaxSplits; ++s) {
+      const double* from = part + (s < a.S ? (int64_t)s * a.n_tok * E : 0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[s - 1][i] = from[e0 + i < E ? e0 + i : E - 1];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 1; s < kMaxSplits; ++s)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) z[i] += s < a.S ? v[s - 1][i] : 0.0;
   }
   if (a.b_router)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] += (double)a.b_router[e0 + i < E ? e0 + i : E - 1];
+    for (int i = 0; i < NV; ++i) z[i] += (double)rb[i];
   if (there && a.logits)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -277,17 +384,18 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
   double p[NV], sum = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    p[i] = e0 + i < E ? exp(a.sigmoid ? -z[i] : z[i] - m) : 0.0;
+    p[i] = e0 + i < E ? exp_clamped(a.sigmoid ? -z[i] : z[i] - m) : 0.0;
     sum += p[i];
   }
+  double inv = 1.0;
   if (!a.sigmoid) {
     sum = W::sum(sum);
-    if (sum == 0.0) sum = 1.0;
+    inv = 1.0 / (sum == 0.0 ? 1.0 : sum);
   }
   uint32_t key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    p[i] = a.sigmoid ? 1.0 / (1.0 + p[i]) : p[i] / sum;
+    p[i] = a.sigmoid ? reciprocal(1.0 + p[i]) : p[i] * inv;
     const bool on = e0 + i < E && sb[i] != -INFINITY;
     // the bias is added also where there is none: a score is no -0
     key[i] = on ? order_key((float)p[i] + sb[i]) : 0u;
@@ -382,19 +490,20 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (chosen(i)) {
-          p[i] = exp(z[i] - m);
+          p[i] = exp_clamped(z[i] - m);
           total += p[i];
         }
       total = W::sum(total);
       if (total == 0.0) total = 1.0;
     }
   }
+  const double factor = a.scale / total;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (chosen(i)) {
       const int64_t at = tt * k + (key[i] - 1);
       a.ids[at] = e0 + i;
-      a.gates[at] = (float)(a.scale * (p[i] / total));
+      a.gates[at] = (float)(p[i] * factor);
     }
   for (int c = taken + l; c < k; c += LPT) {  // masked, or too few experts are on
     a.ids[tt * k + c] = -1;
@@ -406,48 +515,42 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
 struct Plan {
   int64_t chunk;  // tokens that go through the two launches at a time
   int S;          // splits of the columns
-  bool large;
+  bool large;     // 32 tokens x 32 experts a wave instead of 16 x 16
 };
 
-// At most 64 MiB of partial logits.  Short batches take 16 x 16 tiles and split the columns until
-// there are some hundred blocks; long ones 32 x 32 tiles, which widen each value for two products.
+// The large tiles convert each value for two products, and conversions and fp64 products take turns
+// (16 and 64 cycles); the small ones make more blocks.  us, small / large, bf16, both with the columns
+// split until there are 512 blocks: E 64, d 2048: T 1024 9.6 / 9.8, 2048 14.9 / 14.9, 4096 25.4 / 23.4,
+// 16384 89 / 75; E 256, d 4096, T 1024 45.9 / 40.5; T 256, E 64 4.8 / 8.6.  Without splits T 4096, E 64
+// takes 37.9.  At most 64 MiB of partial logits.
 Plan plan(const moe_shape& s) {
   Plan p;
-  p.large = s.T >= 4096;
-  const int nq = ((s.d_model + 7) / 8 + 3) / 4;
-  if (p.large) {
-    p.S = 1;
-    p.chunk = ((int64_t)64 << 20) / (8 * s.n_experts) / 32 * 32;
-  } else {
-    const int64_t tiles = (s.T + 15) / 16 * ((s.n_experts + 15) / 16);
-    const int most = (nq + 7) / 8;
-    p.S = (int)(512 / (tiles > 0 ? tiles : 1));
-    p.S = p.S < 1 ? 1 : p.S > 8 ? 8 : p.S;
-    p.S = p.S < most ? p.S : most;
-    p.chunk = 4096;
-  }
-  if (p.chunk > s.T) p.chunk = s.T;
+  const int64_t tiles = (s.T + 31) / 32 * ((s.n_experts + 63) / 64);
+  p.large = tiles >= 64;
+  const int64_t blocks = p.large ? tiles : (s.T + 15) / 16 * ((s.n_experts + 15) / 16);
+  const int64_t most = (s.d_model + 255) / 256;  // at least a quad of 32 columns for each of 8 waves
+  p.S = (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), most, kMaxSplits}));
+  p.chunk = std::min<int64_t>(s.T, ((int64_t)64 << 20) / (8 * s.n_experts * p.S) / 32 * 32);
   return p;
 }
 
-template <typename TIn, typename Chunk, int R, int EBG, int WD, int WE>
-hipError_t launch_logits(const moe_shape& s, const TIn* x, const TIn* w, const Plan& p,
+template <typename Chunk, int R, int EBG, int WD, int WE>
+hipError_t launch_logits(const moe_shape& s, const void* x, const void* w, const Plan& p,
                          int64_t base, int64_t n, double* part, hipStream_t st) {
   const dim3 grid((unsigned)((n + 16 * R - 1) / (16 * R)),
                   (unsigned)((s.n_experts + 16 * EBG * WE - 1) / (16 * EBG * WE)), (unsigned)p.S);
-  hipLaunchKernelGGL((k_scored_logits<TIn, Chunk, R, EBG, WD, WE>), grid, dim3(64 * WD * WE), 0, st, x, w,
+  hipLaunchKernelGGL((k_scored_logits<Chunk, R, EBG, WD, WE>), grid, dim3(64 * WD * WE), 0, st, x, w,
                      s.T, s.d_model, s.n_experts, p.S, base, n, part);
   return hipGetLastError();
 }
 
-template <typename TIn, typename Chunk>
+template <typename Chunk>
 hipError_t logits_any(const moe_shape& s, const void* x, const void* w, const Plan& p, int64_t base,
                       int64_t n, double* part, hipStream_t st) {
-  const TIn *xi = (const TIn*)x, *wi = (const TIn*)w;
-  if (!p.large) return launch_logits<TIn, Chunk, 1, 1, 8, 1>(s, xi, wi, p, base, n, part, st);
-  if (s.n_experts <= 16) return launch_logits<TIn, Chunk, 2, 1, 4, 1>(s, xi, wi, p, base, n, part, st);
-  if (s.n_experts <= 32) return launch_logits<TIn, Chunk, 2, 2, 4, 1>(s, xi, wi, p, base, n, part, st);
-  return launch_logits<TIn, Chunk, 2, 2, 4, 2>(s, xi, wi, p, base, n, part, st);
+  if (!p.large) return launch_logits<Chunk, 1, 1, 8, 1>(s, x, w, p, base, n, part, st);
+  if (s.n_experts <= 16) return launch_logits<Chunk, 2, 1, 4, 1>(s, x, w, p, base, n, part, st);
+  if (s.n_experts <= 32) return launch_logits<Chunk, 2, 2, 4, 1>(s, x, w, p, base, n, part, st);
+  return launch_logits<Chunk, 2, 2, 4, 2>(s, x, w, p, base, n, part, st);
 }
 
 hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
@@ -479,11 +582,9 @@ hipError_t launch_route_scored(const moe_shape& s, const moe_routing& r, const v
   for (int64_t base = 0; base < s.T; base += p.chunk) {
     const int64_t n = s.T - base < p.chunk ? s.T - base : p.chunk;
     hipError_t err =
-        s.dtype == MOE_BF16
-            ? logits_any<bf16_t, Chunk8<bf16_t>>(s, x, w_router, p, base, n, part, st)
-        : s.d_model % 4 == 0
-            ? logits_any<float, Chunk8F4>(s, x, w_router, p, base, n, part, st)
-            : logits_any<float, Chunk8<float>>(s, x, w_router, p, base, n, part, st);
+        s.dtype == MOE_BF16    ? logits_any<ChunkBf16>(s, x, w_router, p, base, n, part, st)
+        : s.d_model % 4 == 0 ? logits_any<ChunkF32x4>(s, x, w_router, p, base, n, part, st)
+                             : logits_any<ChunkF32>(s, x, w_router, p, base, n, part, st);
     if (err != hipSuccess) return err;
     ChooseArgs a{part, p.S, base, n, s.n_experts, s.top_k, r.score == MOE_SCORE_SIGMOID,
                  r.n_groups, r.topk_groups, r.group_score == MOE_GROUP_TOP_TWO, r.renormalize,
