@@ -159,12 +159,41 @@ __device__ __forceinline__ float wave_absmax(const float (&x)[4]) {
 }
 // Codes of x under `step`; a block whose step is not finite has no value left that is: codes 0 (or 1).
 template <int TOP>
-__device__ __forceinline__ int encode(float x, float step) {
-  const float y = step > 0.0f ? fabsf(x) / step : 0.0f;
-  const float c = floorf(sqrtf(y) + 0.5f);
-  int code = c >= 0.0f ? (int)fminf(c, (float)TOP) : 0;
+__device__ __forceinline__ int finish_code(float x, float c) {
+  const int code = c >= 0.0f ? (int)fminf(c, (float)TOP) : 0;
   if (TOP == 255) return x > 0.0f && code < 1 ? 1 : code;
   return x < 0.0f ? -code : code;
+}
+template <int TOP>
+__device__ __forceinline__ int encode(float x, float step) {
+  const float y = step > 0.0f ? fabsf(x) / step : 0.0f;
+  return finish_code<TOP>(x, floorf(sqrtf(y) + 0.5f));
+}
+// The codes of a lane's four values; exact(j) gives value j as the definition has it, x[j] may be a step
+// of fp32 off.  Away from the borders between codes the hardware's reciprocal and root are near enough:
+// x, the reciprocal and the product put |x| / step 2.5 steps off, its root 1.25 and one of its own,
+// 2.25 2^-23 of at most 255.5 or 2^-13.8, and the sums with 1/2 and the definition's own roundings less
+// than 2^-14 more.  A wave with a value within 2^-12 of a border (12 in 100) does that lane's values
+// over, and so does one whose step is too small or large for its reciprocal, or no number.
+template <int TOP, typename Exact>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], Exact exact, float step) {
+  const float inv = __builtin_amdgcn_rcpf(step);
+  bool near = !(step > 0x1p-80f && step < 0x1p100f);
+  int code[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float f = __builtin_amdgcn_sqrtf(fabsf(x[j]) * inv) + 0.5f, c = floorf(f);
+    near |= fabsf(f - c - 0.5f) > 0.5f - 0x1p-12f;
+    code[j] = finish_code<TOP>(x[j], c);
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) code[j] = encode<TOP>(exact(j), step);
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w |= ((uint32_t)code[j] & 0xFFu) << (8 * j);
+  return w;
 }
 
 // m and v of one element, each operation rounded
@@ -218,24 +247,26 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
       load4<float>((const float*)r.v, i, n, whole, vv);
     }
     float rv[4];
+    bool slow = false;  // roots that the instruction alone does not give to a step: of v below 2^-96
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       moments(gv[j] * c.grad_scale, a.beta1, a.beta2, mv[j], vv[j]);
-      rv[j] = sqrtf(vv[j]);
+      slow |= !Q8 || __float_as_uint(vv[j]) - 1u < 0x0F7FFFFFu;  // but 0 is fine
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rv[j] = slow ? sqrtf(vv[j]) : __builtin_amdgcn_sqrtf(vv[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       const float q = fmaf(-lr_wd, pv[j], pv[j]);
       pv[j] = q - c.rate * mv[j] / fmaf(rv[j], c.inv_root, a.eps);
     }
     store4(p, i, n, whole, pv);
     if (copy) store4(copy, i, n, whole, pv);
     if constexpr (Q8) {
-      // elements past the tensor's end are zeros
-      const float ms = wave_absmax(mv) / 16129.0f, vs = wave_absmax(rv) / 65025.0f;
-      uint32_t mc = 0, vc = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mc |= ((uint32_t)encode<127>(mv[j], ms) & 0xFFu) << (8 * j);
-        vc |= (uint32_t)encode<255>(rv[j], vs) << (8 * j);
-      }
+      // elements past the tensor's end are zeros; the largest root is the largest v's
+      const float ms = wave_absmax(mv) / 16129.0f, vs = sqrtf(wave_absmax(vv)) / 65025.0f;
+      const uint32_t mc = encode4<127>(mv, [&](int j) { return mv[j]; }, ms);
+      const uint32_t vc = encode4<255>(rv, [&](int j) { return sqrtf(vv[j]); }, vs);
       store_codes((uint8_t*)r.m, i, n, whole, mc);
       store_codes((uint8_t*)r.v, i, n, whole, vc);
       if ((threadIdx.x & 63) == 0) {
