@@ -126,26 +126,25 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, bo
 __device__ __forceinline__ void decode_m(uint32_t w, float step, float (&o)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = (int)(int8_t)(w >> (8 * j));
-    o[j] = (float)(c * (c < 0 ? -c : c)) * step;
+    const float c = (float)((int)(w << (24 - 8 * j)) >> 24);
+    o[j] = c * fabsf(c) * step;  // the square is exact
   }
 }
 __device__ __forceinline__ void decode_v(uint32_t w, float step, float (&o)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = (int)((w >> (8 * j)) & 0xFFu);
-    const float r = (float)(c * c) * step;
+    const float c = (float)((w >> (8 * j)) & 0xFFu), r = c * c * step;
     o[j] = r * r;
   }
 }
 
-// The largest of the wave's values, as the bit patterns of |x| order them: NaN above infinity
-// above all else.
+// The largest of the wave's |x|, as their bit patterns order them: NaN above infinity above all else.
+template <bool SIGNED>
 __device__ __forceinline__ float wave_absmax(const float (&x)[4]) {
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t u = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    const uint32_t u = SIGNED ? __float_as_uint(x[j]) & 0x7FFFFFFFu : __float_as_uint(x[j]);
     m = u > m ? u : m;
   }
   auto take = [&](uint32_t o) { m = o > m ? o : m; };
@@ -153,46 +152,50 @@ __device__ __forceinline__ float wave_absmax(const float (&x)[4]) {
   take(dpp32<0x4E>(m));
   take(dpp32<0x141>(m));
   take(dpp32<0x140>(m));
-  take((uint32_t)__shfl_xor((int)m, 16, 64));
-  take((uint32_t)__shfl_xor((int)m, 32, 64));
-  return __uint_as_float(m);
+  const uint32_t a = __builtin_amdgcn_readlane(m, 0), b = __builtin_amdgcn_readlane(m, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(m, 32), d = __builtin_amdgcn_readlane(m, 48);
+  const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
+  return __uint_as_float(ab > cd ? ab : cd);
 }
-// Codes of x under `step`; a block whose step is not finite has no value left that is: codes 0 (or 1).
-template <int TOP>
-__device__ __forceinline__ int finish_code(float x, float c) {
-  const int code = c >= 0.0f ? (int)fminf(c, (float)TOP) : 0;
-  if (TOP == 255) return x > 0.0f && code < 1 ? 1 : code;
-  return x < 0.0f ? -code : code;
-}
+// The code of x under `step`, by the definition; a block whose step is not finite has no value left that
+// is: codes 0 (or 1).
 template <int TOP>
 __device__ __forceinline__ int encode(float x, float step) {
   const float y = step > 0.0f ? fabsf(x) / step : 0.0f;
-  return finish_code<TOP>(x, floorf(sqrtf(y) + 0.5f));
+  const float c = floorf(sqrtf(y) + 0.5f);
+  const int code = c >= 0.0f ? (int)fminf(c, (float)TOP) : 0;
+  if (TOP == 255) return x > 0.0f && code < 1 ? 1 : code;
+  return x < 0.0f ? -code : code;
 }
 // The codes of a lane's four values; exact(j) gives value j as the definition has it, x[j] may be a step
 // of fp32 off.  Away from the borders between codes the hardware's reciprocal and root are near enough:
 // x, the reciprocal and the product put |x| / step 2.5 steps off, its root 1.25 and one of its own,
 // 2.25 2^-23 of at most 255.5 or 2^-13.8, and the sums with 1/2 and the definition's own roundings less
-// than 2^-14 more.  A wave with a value within 2^-12 of a border (12 in 100) does that lane's values
-// over, and so does one whose step is too small or large for its reciprocal, or no number.
+// than 2^-14 more.  A lane with a value within 2^-12 of a border (12 waves in 100 have one) does its
+// values over, and so do all where the step is too small or large for its reciprocal, or no number.
 template <int TOP, typename Exact>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], Exact exact, float step) {
   const float inv = __builtin_amdgcn_rcpf(step);
-  bool near = !(step > 0x1p-80f && step < 0x1p100f);
-  int code[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float f = __builtin_amdgcn_sqrtf(fabsf(x[j]) * inv) + 0.5f, c = floorf(f);
-    near |= fabsf(f - c - 0.5f) > 0.5f - 0x1p-12f;
-    code[j] = finish_code<TOP>(x[j], c);
-  }
-  if (near) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) code[j] = encode<TOP>(exact(j), step);
-  }
+  float edge = 0.0f;
   uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w |= ((uint32_t)code[j] & 0xFFu) << (8 * j);
+  for (int j = 0; j < 4; ++j) {
+    const float f = __builtin_amdgcn_sqrtf(fabsf(x[j]) * inv) + 0.5f;
+    edge = fmaxf(edge, fabsf(__builtin_amdgcn_fractf(f) - 0.5f));
+    const uint32_t c = (uint32_t)f, bits = __float_as_uint(x[j]);
+    if (TOP == 255) {  // x >= 0; not 0 where x is not
+      const uint32_t least = bits < 1u ? bits : 1u;
+      w |= (c < least ? least : c > 255u ? 255u : c) << (8 * j);
+    } else {
+      const uint32_t sign = (uint32_t)((int)bits >> 31);
+      w |= ((((c > 127u ? 127u : c) ^ sign) - sign) & 0xFFu) << (8 * j);
+    }
+  }
+  if (edge > 0.5f - 0x1p-12f || !(step > 0x1p-80f && step < 0x1p100f)) {
+    w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= ((uint32_t)encode<TOP>(exact(j), step) & 0xFFu) << (8 * j);
+  }
   return w;
 }
 
@@ -246,25 +249,40 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
       load4<float>((const float*)r.m, i, n, whole, mv);
       load4<float>((const float*)r.v, i, n, whole, vv);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) moments(gv[j] * c.grad_scale, a.beta1, a.beta2, mv[j], vv[j]);
     float rv[4];
-    bool slow = false;  // roots that the instruction alone does not give to a step: of v below 2^-96
+    if constexpr (Q8) {
+      // The kernel of 8 bits is short of instructions, not of bytes (122 an element with every root and
+      // quotient in full: 139 us for 37.8 million elements): roots and the quotient to a step of fp32,
+      // except roots of denormal numbers, which the instruction takes for zeros.
+      uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      moments(gv[j] * c.grad_scale, a.beta1, a.beta2, mv[j], vv[j]);
-      slow |= !Q8 || __float_as_uint(vv[j]) - 1u < 0x0F7FFFFFu;  // but 0 is fine
-    }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u = __float_as_uint(vv[j]) - 1u;  // 0 is fine
+        least = u < least ? u : least;
+        rv[j] = __builtin_amdgcn_sqrtf(vv[j]);
+      }
+      if (least < 0x007FFFFFu)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rv[j] = slow ? sqrtf(vv[j]) : __builtin_amdgcn_sqrtf(vv[j]);
+        for (int j = 0; j < 4; ++j) rv[j] = sqrtf(vv[j]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float q = fmaf(-lr_wd, pv[j], pv[j]);
-      pv[j] = q - c.rate * mv[j] / fmaf(rv[j], c.inv_root, a.eps);
+      for (int j = 0; j < 4; ++j) {
+        const float q = fmaf(-lr_wd, pv[j], pv[j]);
+        pv[j] = fmaf(-c.rate * mv[j], __builtin_amdgcn_rcpf(fmaf(rv[j], c.inv_root, a.eps)), q);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float q = fmaf(-lr_wd, pv[j], pv[j]);
+        pv[j] = q - c.rate * mv[j] / fmaf(sqrtf(vv[j]), c.inv_root, a.eps);
+      }
     }
     store4(p, i, n, whole, pv);
     if (copy) store4(copy, i, n, whole, pv);
     if constexpr (Q8) {
       // elements past the tensor's end are zeros; the largest root is the largest v's
-      const float ms = wave_absmax(mv) / 16129.0f, vs = sqrtf(wave_absmax(vv)) / 65025.0f;
+      const float ms = wave_absmax<true>(mv) / 16129.0f, vs = sqrtf(wave_absmax<false>(vv)) / 65025.0f;
       const uint32_t mc = encode4<127>(mv, [&](int j) { return mv[j]; }, ms);
       const uint32_t vc = encode4<255>(rv, [&](int j) { return sqrtf(vv[j]); }, vs);
       store_codes((uint8_t*)r.m, i, n, whole, mc);

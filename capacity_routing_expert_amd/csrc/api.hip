@@ -1,5 +1,6 @@
 // C interface of libmoe: argument checks, workspace layout and launch order.  The operations
 // and their sources are described in include/moe.h.
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -363,8 +364,8 @@ moe_status check_adamw(const moe_adamw_config* config, const moe_adamw_tensor* t
                 c.grad_dtype);
   if (!(c.beta1 >= 0.0f && c.beta1 < 1.0f) || !(c.beta2 >= 0.0f && c.beta2 < 1.0f))
     return fail(MOE_ERR_INVALID_ARGUMENT, "beta1 = %g, beta2 = %g not in [0, 1)", c.beta1, c.beta2);
-  if (!isfinite(c.eps) || !(c.eps > 0.0f))
-    return fail(MOE_ERR_INVALID_ARGUMENT, "eps = %g must be positive and finite", c.eps);
+  if (!isfinite(c.eps) || !(c.eps >= FLT_MIN))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "eps = %g must be positive, normal and finite", c.eps);
   if (c.dynamic) {
     if (!aligned(c.dynamic, 4)) return fail(MOE_ERR_UNSUPPORTED, "dynamic is not 4-byte aligned");
   } else {

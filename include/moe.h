@@ -676,7 +676,7 @@ typedef struct {
   int32_t state_bits;  /* 32 or 8 */
   float lr;            /* >= 0 */
   float beta1, beta2;  /* in [0, 1) */
-  float eps;           /* > 0 */
+  float eps;           /* > 0, no denormal number */
   float grad_scale;    /* finite */
   int64_t step;        /* number of this step, from 1 */
   const float* dynamic; /* NULL, or [4] on the device: lr, grad_scale, step, skip take the place of

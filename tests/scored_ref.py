@@ -193,7 +193,8 @@ def adamw(p, g, m, v, lr, beta1, beta2, eps, step, wd, grad_scale=1.0):
         up = lr * (m.astype(np.float64) / c1) / (np.sqrt(v.astype(np.float64) / c2) + eps)
         p64 = p.astype(np.float64)
         new = p64 - lr * wd * p64 - up
-        # update: the factor, its product with m, the root, its factor, their sum, the quotient (6
-        # roundings, 7 with slack for second order); p: lr wd, the decayed p, the difference
-        bound = U * (7 * np.abs(up) + (1 + lr * wd) * np.abs(p64) + np.abs(new)) + 2.0 ** -140
+        # update: in half steps of fp32, the factor 1, its product with m 1, the root 1 (2 at 8 bits, the
+        # hardware's own), its factor 1, their sum 1, the quotient 1 (2 at 8 bits: reciprocal), so at
+        # most 8, and 9 with the second order; p: lr wd, the decayed p, the difference
+        bound = U * (9 * np.abs(up) + (1 + lr * wd) * np.abs(p64) + np.abs(new)) + 2.0 ** -140
     return new, bound, m, v

@@ -193,7 +193,7 @@ def step(lib, c=None, ts=None, n=1):
 @pytest.mark.parametrize("kw,status,text", [
     (dict(state_bits=16), 1, "state_bits"), (dict(param_dtype=3), 2, "param_dtype"),
     (dict(grad_dtype=-1), 2, "grad_dtype"), (dict(beta1=1.0), 1, "beta1"), (dict(beta2=-0.1), 1, "beta2"),
-    (dict(beta1=float("nan")), 1, "beta1"), (dict(eps=0.0), 1, "eps"), (dict(eps=float("inf")), 1, "eps"),
+    (dict(beta1=float("nan")), 1, "beta1"), (dict(eps=0.0), 1, "eps"), (dict(eps=float("inf")), 1, "eps"), (dict(eps=1e-39), 1, "eps"),
     (dict(lr=-1.0), 1, "lr"), (dict(lr=float("nan")), 1, "lr"), (dict(grad_scale=float("inf")), 1, "grad"),
     (dict(step=0), 1, "step = 0"), (dict(dynamic=4098), 2, "dynamic"),
 ])
