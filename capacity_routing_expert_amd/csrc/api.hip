@@ -350,8 +350,8 @@ moe_status check_adamw_state(const moe_adamw_config& c, const moe_adamw_tensor& 
 
 moe_status check_adamw_n(const moe_adamw_tensor& t, int i) {
   if (t.n < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "tensors[%d].n = %lld < 0", i, (long long)t.n);
-  if (t.n >= ((int64_t)1 << 36))
-    return fail(MOE_ERR_UNSUPPORTED, "tensors[%d].n = %lld >= 2^36", i, (long long)t.n);
+  if (t.n > ((int64_t)1 << 33))
+    return fail(MOE_ERR_UNSUPPORTED, "tensors[%d].n = %lld > 2^33", i, (long long)t.n);
   return MOE_OK;
 }
 

@@ -78,10 +78,19 @@ __global__ __launch_bounds__(kThreads) void k_bias_update(const int32_t* __restr
   }
   __syncthreads();
   if (blocks > 0) {
-    for (int i = threadIdx.x; i < blocks * E; i += kThreads) {
-      const int c = part[i];
-      if (c) atomicAdd(&hist[i % E], c);
-    }
+    // EG threads a row of partial counts, kThreads / EG rows at a time, their loads together
+    int EG = 1;
+    while (EG < E) EG <<= 1;
+    const int at = threadIdx.x % EG, r0 = threadIdx.x / EG, rows = kThreads / EG;
+    if (at < E)
+      for (int b = r0; b < blocks; b += 16 * rows) {
+        int v[16], c = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = part[(b + j * rows < blocks ? b + j * rows : b) * E + at];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) c += b + j * rows < blocks ? v[j] : 0;
+        atomicAdd(&hist[(r0 & (kCopies - 1)) * (E + 1) + at], c);
+      }
   } else if (ids) {
     count_range(ids, mask, 0, n, E, k, hist);
   }

@@ -136,18 +136,29 @@ __global__ __launch_bounds__(256) void k_combine_back(const CombineBackArgs a) {
 hipError_t launch_combine_backward(const moe_shape& s, const void* dout, const float* gates,
                                    const int32_t* slot_of, const void* y, float* dgates, void* dy,
                                    hipStream_t st) {
-  const CombineBackArgs a{dout, gates, slot_of, y, dgates, dy, s.T, s.d_model, s.top_k};
-  const dim3 grid((unsigned)((s.T + 3) / 4));
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a);
-    return hipGetLastError();
-  };
-  if (s.dtype == MOE_BF16)
-    return dy ? go(k_combine_back<bf16_t, 8, true>) : go(k_combine_back<bf16_t, 8, false>);
-  const uintptr_t all = (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy;
-  if (s.d_model % 4 == 0 && all % 16 == 0)
-    return dy ? go(k_combine_back<float, 4, true>) : go(k_combine_back<float, 4, false>);
-  return dy ? go(k_combine_back<float, 1, true>) : go(k_combine_back<float, 1, false>);
+  const size_t size = s.dtype == MOE_BF16 ? 2 : 4, row = (size_t)s.d_model * size;
+  constexpr int64_t kTokens = 1 << 25;  // a launch: 64 threads each, and 2^32 are too many
+  for (int64_t t = 0; t < s.T; t += kTokens) {
+    const int64_t n = s.T - t < kTokens ? s.T - t : kTokens;
+    const CombineBackArgs a{(const char*)dout + t * row, gates ? gates + t * s.top_k : nullptr,
+                            slot_of + t * s.top_k, y, dgates ? dgates + t * s.top_k : nullptr, dy, n,
+                            s.d_model, s.top_k};
+    const dim3 grid((unsigned)((n + 3) / 4));
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a);
+      return hipGetLastError();
+    };
+    const uintptr_t all = (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy;
+    hipError_t err;
+    if (s.dtype == MOE_BF16)
+      err = dy ? go(k_combine_back<bf16_t, 8, true>) : go(k_combine_back<bf16_t, 8, false>);
+    else if (s.d_model % 4 == 0 && all % 16 == 0)
+      err = dy ? go(k_combine_back<float, 4, true>) : go(k_combine_back<float, 4, false>);
+    else
+      err = dy ? go(k_combine_back<float, 1, true>) : go(k_combine_back<float, 1, false>);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

@@ -185,20 +185,27 @@ hipError_t launch_route_scored_backward(const moe_shape& s, const moe_routing& r
                                         const float* logits, const int32_t* ids,
                                         const float* dgates, const float* add, const uint8_t* mask,
                                         float* dlogits, hipStream_t st) {
-  const ScoredBackArgs a{logits, ids, dgates, add, mask, dlogits, s.T, s.n_experts, s.top_k, r.scale};
   const uintptr_t all = (uintptr_t)logits | (uintptr_t)add | (uintptr_t)dlogits;
   const bool vec = s.n_experts % 4 == 0 && all % 16 == 0;
-  return with_router_row(s.n_experts, vec, [&](auto row) {
-    using Row = decltype(row);
-    const dim3 grid((unsigned)((s.T + 256 / Row::LPT - 1) / (256 / Row::LPT)));
-    auto go = [&](auto kern) {
-      hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a);
-      return hipGetLastError();
-    };
-    if (r.score == MOE_SCORE_SIGMOID)
-      return r.renormalize ? go(k_scored_back<Row, true, true>) : go(k_scored_back<Row, true, false>);
-    return r.renormalize ? go(k_scored_back<Row, false, true>) : go(k_scored_back<Row, false, false>);
-  });
+  constexpr int64_t kTokens = 1 << 27;  // a launch: up to 16 threads each, and 2^32 are too many
+  for (int64_t t = 0; t < s.T; t += kTokens) {
+    const int64_t n = s.T - t < kTokens ? s.T - t : kTokens, e = t * s.n_experts, c = t * s.top_k;
+    const ScoredBackArgs a{logits + e, ids + c, dgates + c, add ? add + e : nullptr,
+                           mask ? mask + t : nullptr, dlogits + e, n, s.n_experts, s.top_k, r.scale};
+    const hipError_t err = with_router_row(s.n_experts, vec, [&](auto row) {
+      using Row = decltype(row);
+      const dim3 grid((unsigned)((n + 256 / Row::LPT - 1) / (256 / Row::LPT)));
+      auto go = [&](auto kern) {
+        hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, a);
+        return hipGetLastError();
+      };
+      if (r.score == MOE_SCORE_SIGMOID)
+        return r.renormalize ? go(k_scored_back<Row, true, true>) : go(k_scored_back<Row, true, false>);
+      return r.renormalize ? go(k_scored_back<Row, false, true>) : go(k_scored_back<Row, false, false>);
+    });
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

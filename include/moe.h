@@ -693,7 +693,7 @@ moe_status moe_adamw_check(const moe_adamw_config* config, const moe_adamw_tenso
 
 /* One step.  `tensors` is a host array, not kept after the call; arrays need their element's alignment
  * (16-byte alignment, 8 for bf16 and 4 for codes, is faster).  The tensors must be apart
- * (moe_adamw_check).  n < 2^36 a tensor. */
+ * (moe_adamw_check).  A tensor has at most 2^33 elements. */
 moe_status moe_adamw_step(const moe_adamw_config* config, const moe_adamw_tensor* tensors,
                           int32_t n_tensors, moe_stream_t stream);
 

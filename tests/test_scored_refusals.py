@@ -209,7 +209,7 @@ def test_adamw_config_refusals(lib, kw, status, text):
     (dict(m_steps=at(5)), 32, 1, "steps with 32-bit"), (dict(m_steps=at(5)), 8, 1, "v_steps is NULL"),
     (dict(param=P(4098)), 32, 2, "4-byte"), (dict(m=P(4098)), 32, 2, "4-byte"),
     (dict(copy=P(4097)), 32, 2, "2-byte"), (dict(n=-1), 32, 1, "n = -1"),
-    (dict(n=1 << 36), 32, 2, "2^36"), (dict(weight_decay=-0.1), 32, 1, "weight_decay"),
+    (dict(n=(1 << 33) + 1), 32, 2, "2^33"), (dict(weight_decay=-0.1), 32, 1, "weight_decay"),
     (dict(weight_decay=float("nan")), 32, 1, "weight_decay"),
 ])
 def test_adamw_tensor_refusals(lib, kw, bits, status, text):
