@@ -275,8 +275,11 @@ def _w(shape: MoeShape, rows: int, cols: int) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream, dev: int | None = None) -> ctypes.c_void_p:
+    """The handle of `stream`, or of the current one (of device `dev`, if it has been looked up)."""
     if stream is None and _raw_stream is not None:
+        if dev is not None and dev >= 0:
+            return _raw_stream(dev)
         return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -600,10 +603,13 @@ def moe_pack_weights(shape, w, w_packed, stream=None):
            "moe_pack_weights")
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _device() -> int:
     """The current device (-1 without one): looked up once a call."""
     try:
-        return torch.cuda.current_device()
+        return _get_device()
     except (RuntimeError, AssertionError):
         return -1
 
@@ -615,7 +621,7 @@ def _cur(dev: int, t, name: str, dtype=None, numel: int = 0):
     if t is None:
         return None
     if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and
-            t.numel() >= numel and t.is_cuda and t.is_contiguous() and t.get_device() == dev):
+            t.get_device() == dev and t.numel() >= numel and t.is_contiguous() and dev >= 0):
         return t.data_ptr()
     _ptr(t, name, dtype, numel=numel)
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
@@ -820,7 +826,7 @@ def moe_route_scored(shape, routing, x, w_router, b_router, score_bias, topk_ids
         _cur(dev, topk_ids, "topk_ids", torch.int32, numel=T * k),
         _cur(dev, topk_gates, "topk_gates", f32, numel=T * k),
         _cur(dev, logits, "logits", f32, numel=T * E), _cur(dev, ws, "ws", torch.uint8),
-        ws.numel() if ws is not None else 0, _stream(stream)), "moe_route_scored")
+        ws.numel() if ws is not None else 0, _stream(stream, dev)), "moe_route_scored")
 
 
 def moe_route_scored_backward(shape, routing, logits, topk_ids, dgates, dlogits, dlogits_add=None,
@@ -835,7 +841,7 @@ def moe_route_scored_backward(shape, routing, logits, topk_ids, dgates, dlogits,
         _cur(dev, dgates, "dgates", f32, numel=T * k),
         _cur(dev, dlogits_add, "dlogits_add", f32, numel=T * E),
         _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
-        _cur(dev, dlogits, "dlogits", f32, numel=T * E), _stream(stream)),
+        _cur(dev, dlogits, "dlogits", f32, numel=T * E), _stream(stream, dev)),
         "moe_route_scored_backward")
 
 
@@ -851,7 +857,7 @@ def moe_combine_backward(shape, dout, topk_gates, slot_of, y_rows, dgates=None, 
         _cur(dev, topk_gates, "topk_gates", torch.float32, T * k),
         _cur(dev, slot_of, "slot_of", torch.int32, T * k), _cur(dev, y_rows, "y_rows", dt, rows * d),
         _cur(dev, dgates, "dgates", torch.float32, T * k),
-        _cur(dev, dy_rows, "dy_rows", dt, rows * d), _stream(stream)), "moe_combine_backward")
+        _cur(dev, dy_rows, "dy_rows", dt, rows * d), _stream(stream, dev)), "moe_combine_backward")
 
 
 def workspace_bytes_balance_bias(shape: MoeShape) -> int:
@@ -871,7 +877,7 @@ def moe_balance_bias(shape, rate, score_bias, expert_counts=None, topk_ids=None,
     _check(lib().moe_balance_bias(
         ctypes.byref(shape), ids, _cur(dev, token_mask, "token_mask", torch.uint8, numel=T),
         float(rate), bias, _cur(dev, expert_counts, "expert_counts", torch.int32, numel=E),
-        _cur(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0, _stream(stream)),
+        _cur(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0, _stream(stream, dev)),
         "moe_balance_bias")
 
 
@@ -960,13 +966,14 @@ def moe_adamw_step(tensors: AdamWTensors, lr, beta1, beta2, eps, step, grad_scal
     tensors.on(dev)
     c = tensors.config(lr, beta1, beta2, eps, step, grad_scale,
                        _cur(dev, dynamic, "dynamic", torch.float32, numel=4))
-    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.array, tensors.n, _stream(stream)),
+    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.array, tensors.n, _stream(stream, dev)),
            "moe_adamw_step")
 
 
 def moe_adamw_moments(tensors: AdamWTensors, m_out=None, v_out=None, stream=None):
     """The fp32 moments [n] each of all tensors: lists of outputs (or None, or None entries)."""
-    tensors.on(_device())
+    dev = _device()
+    tensors.on(dev)
     outs = []
     for name, x in (("m_out", m_out), ("v_out", v_out)):
         if x is not None and len(x) != tensors.n:
@@ -977,4 +984,4 @@ def moe_adamw_moments(tensors: AdamWTensors, m_out=None, v_out=None, stream=None
             for i, t in enumerate(x)]))
     c = tensors.config(0.0, 0.0, 0.0, 1.0, 1, 1.0, None)
     _check(lib().moe_adamw_moments(ctypes.byref(c), tensors.array, tensors.n, *outs,
-                                   _stream(stream)), "moe_adamw_moments")
+                                   _stream(stream, dev)), "moe_adamw_moments")

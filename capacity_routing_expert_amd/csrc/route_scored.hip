@@ -25,7 +25,9 @@ namespace {
 
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
-// 8 columns of a token or of an expert, as stored.  A load takes a byte offset of the lane (kBufferOOR:
+constexpr uint32_t kNowhere = 0x80000000u;  // past every array (below 2 GiB), also with some bytes added
+
+// 8 columns of a token or of an expert, as stored.  A load takes a byte offset of the lane (kNowhere:
 // zeros) and one of the wave, so that walking along d costs the vector ALU nothing: it and the fp64
 // matrix instructions take turns.  widen: columns 4 h .. 4 h + 3 in fp64, exactly.
 struct ChunkBf16 {  // d % 8 == 0
@@ -55,7 +57,7 @@ struct ChunkF32x4 {  // two 16-byte loads: d % 4 == 0, arrays on 4 bytes
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
                                        int col, int d) {
     v[0] = ChunkBf16::load16(m, lane_off, wave_off);
-    v[1] = ChunkBf16::load16(m, col + 4 < d ? lane_off + 16 : kBufferOOR, wave_off);
+    v[1] = ChunkBf16::load16(m, col + 4 < d ? lane_off + 16 : kNowhere, wave_off);
   }
   __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
     o[0] = __uint_as_float(v[h].x);
@@ -72,7 +74,7 @@ struct ChunkF32 {  // any d
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       v[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          m, (int)(col + u < d ? lane_off + 4 * u : kBufferOOR), (int)wave_off, 0));
+          m, (int)(col + u < d ? lane_off + 4 * u : kNowhere), (int)wave_off, 0));
   }
   __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
 #pragma unroll
@@ -118,20 +120,21 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t t = tok0 + 16 * r + i;
-    xo[r] = t < n_tok ? (uint32_t)((tok_base + t) * d + q * 8) * kSize : kBufferOOR;
+    xo[r] = t < n_tok ? (uint32_t)((tok_base + t) * d + q * 8) * kSize : kNowhere;
   }
 #pragma unroll
   for (int b = 0; b < EBG; ++b) {
     const int e = e0 + 16 * b + i;
-    wo[b] = e < E ? (uint32_t)((int64_t)e * d + q * 8) * kSize : kBufferOOR;
+    wo[b] = e < E ? (uint32_t)((int64_t)e * d + q * 8) * kSize : kNowhere;
   }
   auto load = [&](int cq) {  // columns past d, and whole quads past the last, read as zeros
     const int col = cq * 32 + q * 8;
-    const uint32_t at = (uint32_t)cq * 32 * kSize;
+    // within the first row, and so within the array, whose size the lanes' offsets are held against
+    const uint32_t at = cq < nq ? (uint32_t)cq * 32 * kSize : 0u;
 #pragma unroll
-    for (int r = 0; r < R; ++r) xr[r].load(xs, col < d ? xo[r] : kBufferOOR, at, col, d);
+    for (int r = 0; r < R; ++r) xr[r].load(xs, col < d ? xo[r] : kNowhere, at, col, d);
 #pragma unroll
-    for (int b = 0; b < EBG; ++b) wr[b].load(ws, col < d ? wo[b] : kBufferOOR, at, col, d);
+    for (int b = 0; b < EBG; ++b) wr[b].load(ws, col < d ? wo[b] : kNowhere, at, col, d);
   };
   int cq = split * WD + wd;
   load(cq);
