@@ -886,7 +886,9 @@ class AdamWTensors:
     """The tensors of one optimiser: lists of params, grads and moments (any shapes; entry i of every
     list has the elements of params[i], all contiguous and on one device), checked once.  m and v are
     fp32, or int8 and uint8 with m_steps and v_steps ([ceil(n / 256)] fp32 each); copies, bf16, are
-    written after each step; weight_decay is a number or one per tensor."""
+    written after each step; weight_decay is a number or one per tensor.  Their addresses are taken
+    here and in set_grads: a tensor whose storage is exchanged afterwards (`t.data = ...`) has to be
+    handed over again."""
 
     def __init__(self, params, grads, m, v, m_steps=None, v_steps=None, copies=None,
                  weight_decay=0.0):
@@ -906,7 +908,7 @@ class AdamWTensors:
         self.bits = 8 if quantized else 32
         self.param_dtype = self._one_dtype(params, "params")
         self.params, self.m, self.v = list(params), list(m), list(v)
-        self.m_steps, self.v_steps, self.copies = m_steps, v_steps, copies
+        self.others = [list(x) for x in (m_steps, v_steps, copies) if x is not None]  # kept alive
         self.array = (MoeAdamWTensor * max(n, 1))()
         self.n = n
         f32 = torch.float32

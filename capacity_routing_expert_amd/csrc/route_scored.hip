@@ -564,6 +564,10 @@ hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
   };
   if (a.E <= 16) return go(k_scored_choose<16, 1>, 16);
   if (a.E <= 32) return go(k_scored_choose<16, 2>, 16);
+  // A wave a token is sooner done, 16 lanes take fewer instructions.  us, wave / 16 lanes: E 64, T 64
+  // 3.5 / 4.8, 4096 4.7 / 5.3, 16384 11.0 / 10.1 (with 8 groups 16.1 / 12.1); E 40, top-8, T 65536 52.7
+  // / 31.4.  Above 64 experts 16 lanes hold too many each: E 128, T 16384 15.3 / 24.4.
+  if (a.E <= 64 && a.n_tok >= 8192) return go(k_scored_choose<16, 4>, 16);
   if (a.E <= 64) return go(k_scored_choose<64, 1>, 4);
   if (a.E <= 128) return go(k_scored_choose<64, 2>, 4);
   return go(k_scored_choose<64, 4>, 4);

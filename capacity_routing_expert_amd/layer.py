@@ -524,7 +524,9 @@ class AdamW:
             self.tensors = B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
                                           v_steps=self.v_steps, copies=self.copies,
                                           weight_decay=self.weight_decay)
-        elif any(a is not b for a, b in zip(grads, self.tensors.grads)) or len(grads) != self.tensors.n:
+        elif len(grads) != self.tensors.n or any(
+                g is not old or g.data_ptr() != (a.grad or 0)
+                for g, old, a in zip(grads, self.tensors.grads, self.tensors.array)):
             self.tensors.set_grads(grads)
         B.moe_adamw_step(self.tensors, self.lr, *self.betas, self.eps, self.steps + 1,
                          grad_scale=grad_scale, dynamic=dynamic)

@@ -10,6 +10,7 @@ import torch
 
 import scored_ref as S
 from capacity_routing_expert_amd import binding as B
+from capacity_routing_expert_amd import layer as L
 
 pytestmark = pytest.mark.gpu
 
@@ -167,6 +168,28 @@ def test_blocks_of_zeros_and_single_values():
     assert bool((v[5] == 255).all())
 
 
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_codes_at_their_borders(seed):
+    """Values within a few steps of fp32 of the border between two codes, where the kernel's short way
+    must not decide: with betas of 0, m is the gradient and v its square."""
+    rng = np.random.default_rng(seed)
+    blocks = []
+    for top in (127, 255):
+        for _ in range(400):
+            s = np.exp(rng.uniform(-25, 15))  # the squares stay normal numbers
+            c = rng.integers(0, top, 256)
+            x = ((c + 0.5) ** 2 * s).astype(np.float32)
+            x = (x.view(np.int32) + rng.integers(-6, 7, 256).astype(np.int32)).view(np.float32)
+            x[rng.integers(256)] = np.float32(top * top * s)
+            blocks.append(x * np.where(rng.random(256) < 0.5, -1, 1).astype(np.float32))
+    g = torch.from_numpy(np.concatenate(blocks).astype(np.float32))
+    c = Case([g.numel()], 8, seed=3, fresh=True)
+    c.g[0].copy_(g)
+    want = c.expect(1, beta1=0.0, beta2=0.0)
+    B.moe_adamw_step(c.tensors, step=1, **{**HYPER, "beta1": 0.0, "beta2": 0.0})
+    c.check(want)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_not_finite(bits, bad):
@@ -273,6 +296,20 @@ def test_set_grads_and_refused_lists():
         B.AdamWTensors([p], [torch.zeros(257, device=DEV)], [z()], [z()])
     with pytest.raises(ValueError, match="contiguous"):
         B.AdamWTensors([torch.zeros(256, 2, device=DEV)[:, 0]], [z()], [z()], [z()])
+
+
+def test_gradients_in_other_storage():
+    """A gradient tensor whose storage was exchanged is taken where it lies now."""
+    p = torch.zeros(512, device=DEV)
+    opt = L.AdamW([p], lr=0.5, betas=(0.0, 0.0), weight_decay=0.0)
+    g = torch.ones(512, device=DEV)
+    opt.step([g])
+    assert bool((p + 0.5).abs().max() < 1e-6)
+    g.data = torch.full((512,), -1.0, device=DEV)
+    opt.step([g])
+    assert bool(p.abs().max() < 1e-6)
+    m, v = opt.moments()
+    assert torch.equal(m[0], g) and torch.equal(v[0], g * g)
 
 
 def test_another_stream():

@@ -95,6 +95,8 @@ ROUTES = [
     (4099, 72, 24, 3, "bf16", dict(score="sigmoid", n_groups=8, topk_groups=3, renormalize=True)),
     (4097, 33, 60, 4, "f32", dict(n_groups=3, topk_groups=2, group_score="top2")),
     (4100, 40, 100, 4, "bf16", dict(score="sigmoid")),
+    (8200, 16, 64, 6, "bf16", dict(n_groups=8, topk_groups=3, group_score="top2", renormalize=True)),
+    (8193, 24, 39, 39, "bf16", dict(score="sigmoid", n_groups=3, topk_groups=3, renormalize=True)),
 ]
 
 
