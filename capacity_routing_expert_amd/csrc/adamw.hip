@@ -17,48 +17,59 @@
 // gradients whose size varies by e^(+-1) within a block; rounding at random, unbiased, adds its noise
 // every step and holds it within 8 %.
 //
-// Bound: memory, 28 bytes an element for fp32 moments and gradients, 14 to 18 for 8 bits.  The tensors'
-// addresses go along as kernel arguments, 48 to a launch; a block takes 1024 elements of one tensor, a
-// thread 4 neighbours, so that a wave has exactly the 256 that share a step.
+// Bound: memory, 28 bytes an element for fp32 moments and gradients, 14 to 18 for 8 bits: 268 million
+// elements with bf16 gradients 1148 us (6.1 TB/s), 37.8 million at 8 bits with copies 105 us (5.7 TB/s; with
+// each load behind the branch for odd tensors 115).  The tensors'
+// addresses go along as kernel arguments, 64 or 48 to a launch; a block takes 1024 elements of one
+// tensor, a thread 4 neighbours, so that a wave has exactly the 256 that share a step.
 #include <math.h>
 
-#include "moe_internal.h"
+#include <type_traits>
+
+#include "math_f64.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kTensors = 48;    // a launch
-constexpr int kChunk = 1024;    // elements a block (4096 and 2048: 1326 and 1317 us against 1269 for 268
-                                // million elements, 13.2 and 12.3 against 11.7 for 4.2 million)
+constexpr int kTensors32 = 64, kTensors8 = 48;  // a launch, whose arguments stay below 4 KiB
+constexpr int kChunk = 1024;    // elements a block (loops over 2048 and 4096 took 3 and 5 % longer)
 constexpr int64_t kMaxBlocks = 1 << 23;  // a launch: 2^32 threads are too many
 // From this many bytes on a pass, more than the last-level cache holds, 32-bit moments and what goes with
-// them are loaded past the caches (1185 us against 1269 for 268 million elements, but 13.1 against 11.7
-// where all of it stays in the cache from step to step).
+// them are loaded past the caches (1148 us against 1248 for 268 million elements, but 22.8 against 19.8 for
+// 4.2 million, where all of it stays in the cache from step to step).
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 constexpr int kQuantBlock = 256;
 static_assert(kChunk == 4 * 256, "a block's threads take 4 elements each");
 
-struct AdamRec {
+struct AdamRec32 {
   void* p;
   const void* g;
   void* m;
   void* v;
-  float* m_steps;
-  float* v_steps;
   bf16_t* copy;
   int64_t n;
   float wd;
   int vec;  // every array lies where 4 elements load at once
 };
+struct AdamRec8 : AdamRec32 {
+  float* m_steps;
+  float* v_steps;
+};
+template <typename Rec_, int N>
 struct AdamArgs {
-  AdamRec rec[kTensors];
-  int32_t start[kTensors];  // first block of each tensor
+  typedef Rec_ Rec;
+  static constexpr int kTensors = N;
+  Rec rec[N];
+  int32_t start[N];  // first chunk of each tensor
   int32_t count;
   float lr, beta1, beta2, eps, grad_scale, rate, inv_root;
   double log_beta1, log_beta2;
   const float* dynamic;
 };
+typedef AdamArgs<AdamRec32, kTensors32> AdamArgs32;
+typedef AdamArgs<AdamRec8, kTensors8> AdamArgs8;
+static_assert(sizeof(AdamArgs32) <= 4096 && sizeof(AdamArgs8) <= 4096, "kernel arguments");
 
 struct Rates {
   float lr, grad_scale, rate, inv_root;
@@ -66,9 +77,9 @@ struct Rates {
 
 // The 4 elements of a lane, as loaded.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-template <bool STREAM>
-__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, bool whole, float (&o)[4]) {
-  if (whole) {
+template <bool WHOLE, bool STREAM>
+__device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, float (&o)[4]) {
+  if constexpr (WHOLE) {
     const f32x4* at = reinterpret_cast<const f32x4*>(p + i);
     const f32x4 f = STREAM ? __builtin_nontemporal_load(at) : *at;
     o[0] = f[0], o[1] = f[1], o[2] = f[2], o[3] = f[3];
@@ -77,9 +88,9 @@ __device__ __forceinline__ void load4(const float* p, int64_t i, int64_t n, bool
     for (int j = 0; j < 4; ++j) o[j] = i + j < n ? p[i + j] : 0.0f;
   }
 }
-template <bool STREAM>
-__device__ __forceinline__ void load4(const bf16_t* p, int64_t i, int64_t n, bool whole, float (&o)[4]) {
-  if (whole) {
+template <bool WHOLE, bool STREAM>
+__device__ __forceinline__ void load4(const bf16_t* p, int64_t i, int64_t n, float (&o)[4]) {
+  if constexpr (WHOLE) {
     const uint64_t* at = reinterpret_cast<const uint64_t*>(p + i);
     const uint64_t f = STREAM ? __builtin_nontemporal_load(at) : *at;
     const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
@@ -92,9 +103,9 @@ __device__ __forceinline__ void load4(const bf16_t* p, int64_t i, int64_t n, boo
 }
 // Stores go past the caches: nothing of a step is read again before the next one (moments of 37.8
 // million elements 90 -> 63 us, the step on them 128 -> 124).
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, bool whole,
-                                       const float (&o)[4]) {
-  if (whole) {
+template <bool WHOLE>
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, const float (&o)[4]) {
+  if constexpr (WHOLE) {
     const f32x4 w = {o[0], o[1], o[2], o[3]};
     __builtin_nontemporal_store(w, reinterpret_cast<f32x4*>(p + i));
   } else {
@@ -103,10 +114,10 @@ __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, bool whol
       if (i + j < n) p[i + j] = o[j];
   }
 }
-__device__ __forceinline__ void store4(bf16_t* p, int64_t i, int64_t n, bool whole,
-                                       const float (&o)[4]) {
+template <bool WHOLE>
+__device__ __forceinline__ void store4(bf16_t* p, int64_t i, int64_t n, const float (&o)[4]) {
   const uint32_t a = pack_bf16x2(o[0], o[1]), b = pack_bf16x2(o[2], o[3]);
-  if (whole) {
+  if constexpr (WHOLE) {
     __builtin_nontemporal_store((uint64_t)b << 32 | a, reinterpret_cast<uint64_t*>(p + i));
   } else {
     const bf16_t w[4] = {(bf16_t)a, (bf16_t)(a >> 16), (bf16_t)b, (bf16_t)(b >> 16)};
@@ -116,16 +127,18 @@ __device__ __forceinline__ void store4(bf16_t* p, int64_t i, int64_t n, bool who
   }
 }
 // 4 codes in a dword, the first lowest
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n, bool whole) {
-  if (whole) return *reinterpret_cast<const uint32_t*>(p + i);
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if constexpr (WHOLE) return *reinterpret_cast<const uint32_t*>(p + i);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (i + j < n) w |= (uint32_t)p[i + j] << (8 * j);
   return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, bool whole, uint32_t w) {
-  if (whole) {
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, uint32_t w) {
+  if constexpr (WHOLE) {
     __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(p + i));
   } else {
 #pragma unroll
@@ -225,45 +238,39 @@ __device__ __forceinline__ int tensor_of(const int32_t* start, int count, int bl
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(before)) - 1);
 }
 
-template <typename P, typename G, bool Q8, bool STREAM>
-__global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
-  const int ti = tensor_of(a.start, a.count, (int)blockIdx.x);
-  const AdamRec& r = a.rec[ti];
-  const int64_t n = r.n, base = (int64_t)((int)blockIdx.x - a.start[ti]) * kChunk;
-  Rates c{a.lr, a.grad_scale, a.rate, a.inv_root};
-  if (a.dynamic) {
-    if (a.dynamic[3] != 0.0f) return;
-    c.lr = a.dynamic[0];
-    c.grad_scale = a.dynamic[1];
-    const double t = fmax((double)a.dynamic[2], 1.0);
-    c.rate = (float)((double)c.lr / -expm1(t * a.log_beta1));
-    c.inv_root = (float)(1.0 / sqrt(-expm1(t * a.log_beta2)));
-  }
-  const float lr_wd = c.lr * r.wd;
+// Four elements of a lane.  WHOLE: the chunk is inside the tensor and its arrays lie where 4 elements
+// load at once; decided once a chunk, so that no load waits behind a branch for the one before.
+template <bool WHOLE, typename P, typename G, bool Q8, bool STREAM, typename Args>
+__device__ __forceinline__ void adamw_lane(const Args& a, const typename Args::Rec& r, const Rates& c,
+                                           int64_t i, int64_t n) {
   P* p = (P*)r.p;
   const G* g = (const G*)r.g;
   bf16_t* copy = r.copy;
-  const bool whole = r.vec && base + kChunk <= n;
-  const int64_t i = base + (int64_t)threadIdx.x * 4;
-  if (!whole && base + (threadIdx.x & ~63) * 4 >= n) return;  // waves leave together
+  const float lr_wd = c.lr * r.wd;
   float pv[4], gv[4], mv[4], vv[4];
-  load4<STREAM>(p, i, n, whole, pv);
-  load4<STREAM>(g, i, n, whole, gv);
   const int64_t qb = i / kQuantBlock;
   if constexpr (Q8) {
-    decode_m(load_codes((const uint8_t*)r.m, i, n, whole), r.m_steps[qb], mv);
-    decode_v(load_codes((const uint8_t*)r.v, i, n, whole), r.v_steps[qb], vv);
+    const uint32_t mw = load_codes<WHOLE>((const uint8_t*)r.m, i, n);
+    const uint32_t vw = load_codes<WHOLE>((const uint8_t*)r.v, i, n);
+    const float ms = r.m_steps[qb], vs = r.v_steps[qb];
+    load4<WHOLE, STREAM>(p, i, n, pv);
+    load4<WHOLE, STREAM>(g, i, n, gv);
+    decode_m(mw, ms, mv);
+    decode_v(vw, vs, vv);
   } else {
-    load4<STREAM>((const float*)r.m, i, n, whole, mv);
-    load4<STREAM>((const float*)r.v, i, n, whole, vv);
+    load4<WHOLE, STREAM>(p, i, n, pv);
+    load4<WHOLE, STREAM>(g, i, n, gv);
+    load4<WHOLE, STREAM>((const float*)r.m, i, n, mv);
+    load4<WHOLE, STREAM>((const float*)r.v, i, n, vv);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) moments(gv[j] * c.grad_scale, a.beta1, a.beta2, mv[j], vv[j]);
   float rv[4];
   if constexpr (Q8) {
-    // The kernel of 8 bits is short of instructions, not of bytes (122 an element with every root and
-    // quotient in full: 139 us for 37.8 million elements): roots and the quotient to a step of fp32,
-    // except roots of denormal numbers, which the instruction takes for zeros.
+    // The kernel of 8 bits is short of instructions before it is of bytes (122 an element with every root
+    // and quotient in full: 139 us against 128 for 37.8 million elements, before its stores and loads
+    // were what they are): roots and the quotient to a step of fp32, except roots of denormal
+    // numbers, which the instruction takes for zeros.
     uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -286,23 +293,61 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
       pv[j] = q - c.rate * mv[j] / fmaf(sqrtf(vv[j]), c.inv_root, a.eps);
     }
   }
-  store4(p, i, n, whole, pv);
-  if (copy) store4(copy, i, n, whole, pv);
+  store4<WHOLE>(p, i, n, pv);
+  if (copy) store4<WHOLE>(copy, i, n, pv);
   if constexpr (Q8) {
     // elements past the tensor's end are zeros; the largest root is the largest v's
     const float ms = wave_absmax<true>(mv) / 16129.0f, vs = sqrtf(wave_absmax<false>(vv)) / 65025.0f;
     const uint32_t mc = encode4<127>(mv, [&](int j) { return mv[j]; }, ms);
     const uint32_t vc = encode4<255>(rv, [&](int j) { return sqrtf(vv[j]); }, vs);
-    store_codes((uint8_t*)r.m, i, n, whole, mc);
-    store_codes((uint8_t*)r.v, i, n, whole, vc);
+    store_codes<WHOLE>((uint8_t*)r.m, i, n, mc);
+    store_codes<WHOLE>((uint8_t*)r.v, i, n, vc);
     if ((threadIdx.x & 63) == 0) {
       r.m_steps[qb] = ms;
       r.v_steps[qb] = vs;
     }
   } else {
-    store4((float*)r.m, i, n, whole, mv);
-    store4((float*)r.v, i, n, whole, vv);
+    store4<WHOLE>((float*)r.m, i, n, mv);
+    store4<WHOLE>((float*)r.v, i, n, vv);
   }
+}
+
+// One chunk of kChunk elements.
+template <typename P, typename G, bool Q8, bool STREAM, typename Args>
+__device__ __forceinline__ void adamw_chunk(const Args& a, const Rates& c, int chunk) {
+  const int ti = tensor_of(a.start, a.count, chunk);
+  const typename Args::Rec& r = a.rec[ti];
+  const int64_t n = r.n, base = (int64_t)(chunk - a.start[ti]) * kChunk;
+  const int64_t i = base + (int64_t)threadIdx.x * 4;
+  if (r.vec && base + kChunk <= n)
+    adamw_lane<true, P, G, Q8, STREAM>(a, r, c, i, n);
+  else if (base + (threadIdx.x & ~63) * 4 < n)  // waves that hold nothing leave together
+    adamw_lane<false, P, G, Q8, STREAM>(a, r, c, i, n);
+}
+
+// A chunk a block.
+template <typename P, typename G, bool Q8, bool STREAM, typename Args>
+__global__ __launch_bounds__(256) void k_adamw(const Args a) {
+  adamw_chunk<P, G, Q8, STREAM>(a, Rates{a.lr, a.grad_scale, a.rate, a.inv_root}, (int)blockIdx.x);
+}
+
+// The same with rates from the device.  A correction 1 - beta^t is 1 - e^y in fp64, y = t log beta: as
+// near as 2^-53 / |y|, and |y| is 2^-24 at least.  All waves form both (some 70 instructions; the general
+// functions, 200, in as many blocks as run at once with several chunks each: 137 us against 113 for 37.8
+// million elements at 8 bits, 1459 against 1244 for 268 million at 32).
+template <typename P, typename G, bool Q8, bool STREAM, typename Args>
+__global__ __launch_bounds__(256) void k_adamw_dynamic(const Args a) {
+  if (a.dynamic[3] != 0.0f) return;
+  const double t = fmax((double)a.dynamic[2], 1.0);
+  const double c1 = 1.0 - exp_clamped(t * a.log_beta1), c2 = 1.0 - exp_clamped(t * a.log_beta2);
+  double root = __builtin_amdgcn_rsq(c2);
+  root = root * fma(-0.5 * c2 * root, root, 1.5);
+  Rates c;
+  c.lr = a.dynamic[0];
+  c.grad_scale = a.dynamic[1];
+  c.rate = (float)((double)c.lr / c1);
+  c.inv_root = (float)root;
+  adamw_chunk<P, G, Q8, STREAM>(a, c, (int)blockIdx.x);
 }
 
 struct MomentRec {
@@ -316,29 +361,41 @@ struct MomentRec {
   int vec;
 };
 struct MomentArgs {
+  typedef MomentRec Rec;
+  static constexpr int kTensors = kTensors8;
   MomentRec rec[kTensors];
   int32_t start[kTensors];
   int32_t count;
 };
+static_assert(sizeof(MomentArgs) <= 4096, "kernel arguments");
+
+template <bool WHOLE, bool Q8>
+__device__ __forceinline__ void moments_lane(const MomentRec& r, int64_t i, int64_t n) {
+  float mv[4], vv[4];
+  if constexpr (Q8) {
+    const uint32_t mw = load_codes<WHOLE>((const uint8_t*)r.m, i, n);
+    const uint32_t vw = load_codes<WHOLE>((const uint8_t*)r.v, i, n);
+    const float ms = r.m_steps[i / kQuantBlock], vs = r.v_steps[i / kQuantBlock];
+    decode_m(mw, ms, mv);
+    decode_v(vw, vs, vv);
+  } else {
+    load4<WHOLE, false>((const float*)r.m, i, n, mv);
+    load4<WHOLE, false>((const float*)r.v, i, n, vv);
+  }
+  if (r.m_out) store4<WHOLE>(r.m_out, i, n, mv);
+  if (r.v_out) store4<WHOLE>(r.v_out, i, n, vv);
+}
 
 template <bool Q8>
 __global__ __launch_bounds__(256) void k_adamw_moments(const MomentArgs a) {
   const int ti = tensor_of(a.start, a.count, (int)blockIdx.x);
   const MomentRec& r = a.rec[ti];
   const int64_t n = r.n, base = (int64_t)((int)blockIdx.x - a.start[ti]) * kChunk;
-  const bool whole = r.vec && base + kChunk <= n;
   const int64_t i = base + (int64_t)threadIdx.x * 4;
-  if (i >= n) return;
-  float mv[4], vv[4];
-  if constexpr (Q8) {
-    decode_m(load_codes((const uint8_t*)r.m, i, n, whole), r.m_steps[i / kQuantBlock], mv);
-    decode_v(load_codes((const uint8_t*)r.v, i, n, whole), r.v_steps[i / kQuantBlock], vv);
-  } else {
-    load4<false>((const float*)r.m, i, n, whole, mv);
-    load4<false>((const float*)r.v, i, n, whole, vv);
-  }
-  if (r.m_out) store4(r.m_out, i, n, whole, mv);
-  if (r.v_out) store4(r.v_out, i, n, whole, vv);
+  if (r.vec && base + kChunk <= n)
+    moments_lane<true, Q8>(r, i, n);
+  else if (i < n)
+    moments_lane<false, Q8>(r, i, n);
 }
 
 bool aligned_to(size_t a, std::initializer_list<const void*> ps) {
@@ -355,7 +412,7 @@ hipError_t for_launches(Args& args, const moe_adamw_tensor* ts, int n, Fill fill
   int64_t blocks = 0;
   for (int i = 0; i < n; ++i) {
     if (ts[i].n == 0) continue;
-    if (slot == kTensors || (slot && blocks + (ts[i].n + kChunk - 1) / kChunk > kMaxBlocks)) {
+    if (slot == Args::kTensors || (slot && blocks + (ts[i].n + kChunk - 1) / kChunk > kMaxBlocks)) {
       args.count = slot;
       if (hipError_t err = go(args, blocks); err != hipSuccess) return err;
       slot = 0;
@@ -374,39 +431,45 @@ hipError_t for_launches(Args& args, const moe_adamw_tensor* ts, int n, Fill fill
 
 hipError_t launch_adamw(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,
                         hipStream_t st) {
-  AdamArgs args;
-  args.lr = c.lr;
-  args.beta1 = c.beta1;
-  args.beta2 = c.beta2;
-  args.eps = c.eps;
-  args.grad_scale = c.grad_scale;
-  args.log_beta1 = log((double)c.beta1);
-  args.log_beta2 = log((double)c.beta2);
-  args.dynamic = c.dynamic;
-  const double t = (double)(c.step < 1 ? 1 : c.step);
-  args.rate = (float)((double)c.lr / -expm1(t * args.log_beta1));
-  args.inv_root = (float)(1.0 / sqrt(-expm1(t * args.log_beta2)));
   const bool p16 = c.param_dtype == MOE_BF16, g16 = c.grad_dtype == MOE_BF16, q8 = c.state_bits == 8;
-  auto fill = [&](AdamRec& r, int i) {
-    const moe_adamw_tensor& x = ts[i];
-    r = AdamRec{x.param, x.grad, x.m, x.v, x.m_steps, x.v_steps, (bf16_t*)x.copy, x.n, x.weight_decay, 0};
-    r.vec = aligned_to(p16 ? 8 : 16, {x.param}) && aligned_to(g16 ? 8 : 16, {x.grad}) &&
-            aligned_to(q8 ? 4 : 16, {x.m, x.v}) && aligned_to(8, {x.copy});
-  };
-  auto launch = [&](auto kern) {
-    return for_launches(args, ts, n, fill, [&](const AdamArgs& a, int64_t blocks) {
-      hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+  int64_t bytes = 0;
+  for (int i = 0; i < n; ++i) bytes += ts[i].n * (16 + (p16 ? 4 : 8) + (g16 ? 2 : 4) + (ts[i].copy ? 2 : 0));
+  auto launch = [&](auto args, auto kern, auto dynamic_kern) {
+    typedef typename decltype(args)::Rec Rec;
+    args.lr = c.lr;
+    args.beta1 = c.beta1;
+    args.beta2 = c.beta2;
+    args.eps = c.eps;
+    args.grad_scale = c.grad_scale;
+    args.log_beta1 = log((double)c.beta1);
+    args.log_beta2 = log((double)c.beta2);
+    args.dynamic = c.dynamic;
+    const double t = (double)(c.step < 1 ? 1 : c.step);
+    args.rate = (float)((double)c.lr / -expm1(t * args.log_beta1));
+    args.inv_root = (float)(1.0 / sqrt(-expm1(t * args.log_beta2)));
+    auto fill = [&](Rec& r, int i) {
+      const moe_adamw_tensor& x = ts[i];
+      r.p = x.param, r.g = x.grad, r.m = x.m, r.v = x.v, r.copy = (bf16_t*)x.copy;
+      r.n = x.n, r.wd = x.weight_decay;
+      r.vec = aligned_to(p16 ? 8 : 16, {x.param}) && aligned_to(g16 ? 8 : 16, {x.grad}) &&
+              aligned_to(q8 ? 4 : 16, {x.m, x.v}) && aligned_to(8, {x.copy});
+      if constexpr (std::is_same<Rec, AdamRec8>::value) r.m_steps = x.m_steps, r.v_steps = x.v_steps;
+    };
+    return for_launches(args, ts, n, fill, [&](const auto& a, int64_t blocks) {
+      hipLaunchKernelGGL(c.dynamic ? dynamic_kern : kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
       return hipGetLastError();
     });
   };
-  int64_t bytes = 0;
-  for (int i = 0; i < n; ++i) bytes += ts[i].n * (16 + (p16 ? 4 : 8) + (g16 ? 2 : 4) + (ts[i].copy ? 2 : 0));
   auto types = [&](auto p, auto g) {
     using P = decltype(p);
     using G = decltype(g);
-    return q8                    ? launch(k_adamw<P, G, true, false>)
-           : bytes > kStreamBytes ? launch(k_adamw<P, G, false, true>)
-                                  : launch(k_adamw<P, G, false, false>);
+    if (q8)
+      return launch(AdamArgs8{}, k_adamw<P, G, true, false, AdamArgs8>,
+                    k_adamw_dynamic<P, G, true, false, AdamArgs8>);
+    return bytes > kStreamBytes ? launch(AdamArgs32{}, k_adamw<P, G, false, true, AdamArgs32>,
+                                         k_adamw_dynamic<P, G, false, true, AdamArgs32>)
+                                : launch(AdamArgs32{}, k_adamw<P, G, false, false, AdamArgs32>,
+                                         k_adamw_dynamic<P, G, false, false, AdamArgs32>);
   };
   if (p16) return g16 ? types(bf16_t{}, bf16_t{}) : types(bf16_t{}, float{});
   return g16 ? types(float{}, bf16_t{}) : types(float{}, float{});
