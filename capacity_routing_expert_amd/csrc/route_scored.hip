@@ -66,19 +66,29 @@ struct ChunkF32x4 {  // two 16-byte loads: d % 4 == 0, arrays on 4 bytes
     o[3] = __uint_as_float(v[h].w);
   }
 };
-struct ChunkF32 {  // any d
+struct ChunkF32 {  // any d: as ChunkF32x4 but where the quad (columns col0 to col0 + 31) passes d
   typedef float Elem;
-  float v[8];
+  uint4 v[2];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
                                        int col, int d) {
+    if (__builtin_amdgcn_readfirstlane(col) + 32 <= d) {  // lane 0 has the quad's first columns
+      v[0] = ChunkBf16::load16(m, lane_off, wave_off);
+      v[1] = ChunkBf16::load16(m, lane_off + 16, wave_off);
+      return;
+    }
+    uint32_t w[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      v[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          m, (int)(col + u < d ? lane_off + 4 * u : kNowhere), (int)wave_off, 0));
+      w[u] = __builtin_amdgcn_raw_buffer_load_b32(
+          m, (int)(col + u < d ? lane_off + 4 * u : kNowhere), (int)wave_off, 0);
+    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
   __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) o[u] = v[4 * h + u];
+    o[0] = __uint_as_float(v[h].x);
+    o[1] = __uint_as_float(v[h].y);
+    o[2] = __uint_as_float(v[h].z);
+    o[3] = __uint_as_float(v[h].w);
   }
 };
 

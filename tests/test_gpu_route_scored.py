@@ -395,6 +395,22 @@ def test_backward_of_odd_choices(score, renormalize):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("E,k", [(96, 6), (100, 16), (256, 8), (256, 17), (131, 5)])
+def test_backward_of_experts_held_twice(score, renormalize, E, k):
+    """Among many experts: tokens that hold one twice, three times or only one beside tokens that do not,
+    and choices that are none."""
+    z, ids, dg, add, _ = back_inputs(70, E, k, seed=E + k)
+    for t in range(0, 70, 3):
+        ids[t, 1:1 + t % 4] = ids[t, 0]
+    ids[6] = ids[6, 0]
+    ids[7, 2], ids[8] = -1, -1
+    got = back(z, ids, dg, score, renormalize, 1.5, add)
+    compare(got, z, ids, dg, score, renormalize, 1.5, add)
+    assert torch.equal(back(z, ids, dg, score, renormalize, 1.5, add), got)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_backward_at_the_ends_of_fp32(score):
     """Renormalised gates of scores that fp32 loses still have their gradients; rows whose chosen
     scores are all zero have none."""
