@@ -29,12 +29,12 @@ constexpr uint32_t kNowhere = 0x80000000u;  // past every array (below 2 GiB), a
 
 // 8 columns of a token or of an expert, as stored.  A load takes a byte offset of the lane (kNowhere:
 // zeros) and one of the wave, so that walking along d costs the vector ALU nothing: it and the fp64
-// matrix instructions take turns.  widen: columns 4 h .. 4 h + 3 in fp64, exactly.
+// matrix instructions take turns.  inside: all of the wave's columns are below d.  widen: columns 4 h .. 4 h + 3 in fp64, exactly.
 struct ChunkBf16 {  // d % 8 == 0
   typedef bf16_t Elem;
   uint4 v;
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
-                                       int, int) {
+                                       bool, int, int) {
     v = load16(m, lane_off, wave_off);
   }
   static __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t m, uint32_t lane_off,
@@ -55,8 +55,9 @@ struct ChunkF32x4 {  // two 16-byte loads: d % 4 == 0, arrays on 4 bytes
   typedef float Elem;
   uint4 v[2];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
-                                       int col, int d) {
+                                       bool inside, int col, int d) {
     v[0] = ChunkBf16::load16(m, lane_off, wave_off);
+    (void)inside;
     v[1] = ChunkBf16::load16(m, col + 4 < d ? lane_off + 16 : kNowhere, wave_off);
   }
   __device__ __forceinline__ void widen(int h, double (&o)[4]) const {
@@ -66,12 +67,12 @@ struct ChunkF32x4 {  // two 16-byte loads: d % 4 == 0, arrays on 4 bytes
     o[3] = __uint_as_float(v[h].w);
   }
 };
-struct ChunkF32 {  // any d: as ChunkF32x4 but where the quad (columns col0 to col0 + 31) passes d
+struct ChunkF32 {  // any d: as ChunkF32x4 where all of the wave's columns are inside
   typedef float Elem;
   uint4 v[2];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t m, uint32_t lane_off, uint32_t wave_off,
-                                       int col, int d) {
-    if (__builtin_amdgcn_readfirstlane(col) + 32 <= d) {  // lane 0 has the quad's first columns
+                                       bool inside, int col, int d) {
+    if (inside) {
       v[0] = ChunkBf16::load16(m, lane_off, wave_off);
       v[1] = ChunkBf16::load16(m, lane_off + 16, wave_off);
       return;
@@ -142,9 +143,11 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
     // within the first row, and so within the array, whose size the lanes' offsets are held against
     const uint32_t at = cq < nq ? (uint32_t)cq * 32 * kSize : 0u;
 #pragma unroll
-    for (int r = 0; r < R; ++r) xr[r].load(xs, col < d ? xo[r] : kNowhere, at, col, d);
+    for (int r = 0; r < R; ++r)
+      xr[r].load(xs, col < d ? xo[r] : kNowhere, at, cq * 32 + 32 <= d, col, d);
 #pragma unroll
-    for (int b = 0; b < EBG; ++b) wr[b].load(ws, col < d ? wo[b] : kNowhere, at, col, d);
+    for (int b = 0; b < EBG; ++b)
+      wr[b].load(ws, col < d ? wo[b] : kNowhere, at, cq * 32 + 32 <= d, col, d);
   };
   int cq = split * WD + wd;
   load(cq);
@@ -203,6 +206,97 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
         if (e < E && t < n_tok) out[t * E + e] = acc[r][b][j];
       }
     }
+}
+
+// ---------------------------------------------------------------- partial logits, up to 8 experts
+// With 8 experts half of a 16 x 16 tile is empty.  v_mfma_f64_4x4x4f64 makes four 4 x 4 x 4 products: lane
+// 16 g + 4 b + r holds row r of block b's A operand and column r of its B operand at step g, and
+// receives row g, column r of its result.  The four blocks take four slices of 128 columns, so no two
+// lanes load or convert the same values: lane (g, b, r) has 8 columns, 8 (4 b + g) on, of token 4 tg + r
+// and of expert 4 eg + r.  A block of WD waves takes 16 tokens, wave wd every (S WD)-th 128 columns; the
+// slices are added by lane moves, the waves in their order.  Whole calls against 16 x 16 tiles, us: E 8,
+// T 32768, d 4096 67.8 / 87.7 (268 MB: 4.0 TB/s), T 16384, d 2048 22.9 / 26.7, T 64 no difference.
+template <typename Chunk, int WD>
+__global__ __launch_bounds__(64 * WD) void k_scored_logits_few(
+    const void* __restrict__ x, const void* __restrict__ w, int64_t T, int d, int E, int S,
+    int64_t tok_base, int64_t n_tok, double* __restrict__ part) {
+  __shared__ double lds[WD - 1][8][64];
+  const int lane = threadIdx.x & 63;
+  const int wd = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, b = (lane >> 2) & 3, r = lane & 3;
+  const int64_t tok0 = (int64_t)blockIdx.x * 16;  // within the chunk
+  const int split = blockIdx.y;
+  constexpr uint32_t kSize = sizeof(typename Chunk::Elem);
+  const int nq = (d + 127) / 128, stride = S * WD;
+  const __amdgpu_buffer_rsrc_t xs = buffer_rsrc(x, (uint32_t)(T * d * kSize));
+  const __amdgpu_buffer_rsrc_t ws = buffer_rsrc(w, (uint32_t)((int64_t)E * d * kSize));
+  double acc[4][2];
+#pragma unroll
+  for (int tg = 0; tg < 4; ++tg) acc[tg][0] = acc[tg][1] = 0.0;
+  Chunk xr[4], wr[2];
+  uint32_t xo[4], wo[2];
+#pragma unroll
+  for (int tg = 0; tg < 4; ++tg) {
+    const int64_t t = tok0 + 4 * tg + r;
+    xo[tg] = t < n_tok ? (uint32_t)((tok_base + t) * d + (4 * b + g) * 8) * kSize : kNowhere;
+  }
+#pragma unroll
+  for (int eg = 0; eg < 2; ++eg)
+    wo[eg] = 4 * eg + r < E ? (uint32_t)((int64_t)(4 * eg + r) * d + (4 * b + g) * 8) * kSize : kNowhere;
+  auto load = [&](int cq) {
+    const int col = cq * 128 + (4 * b + g) * 8;
+    const bool inside = cq * 128 + 128 <= d;
+    const uint32_t at = cq < nq ? (uint32_t)cq * 128 * kSize : 0u;  // within the first row
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg) xr[tg].load(xs, col < d ? xo[tg] : kNowhere, at, inside, col, d);
+#pragma unroll
+    for (int eg = 0; eg < 2; ++eg) wr[eg].load(ws, col < d ? wo[eg] : kNowhere, at, inside, col, d);
+  };
+  int cq = split * WD + wd;
+  load(cq);
+  for (; cq < nq; cq += stride) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      double xa[4][4], wb[2][4];
+#pragma unroll
+      for (int tg = 0; tg < 4; ++tg) xr[tg].widen(h, xa[tg]);
+      wr[0].widen(h, wb[0]);
+      wr[1].widen(h, wb[1]);
+      if (h == 1) load(cq + stride);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int tg = 0; tg < 4; ++tg)
+#pragma unroll
+          for (int eg = 0; eg < 2; ++eg)
+            acc[tg][eg] = __builtin_amdgcn_mfma_f64_4x4x4f64(xa[tg][s], wb[eg][s], acc[tg][eg], 0, 0, 0);
+    }
+  }
+  auto moved = [](double v, int s) {
+    return __longlong_as_double((long long)xor_partner((uint64_t)__double_as_longlong(v), s));
+  };
+#pragma unroll
+  for (int tg = 0; tg < 4; ++tg)
+#pragma unroll
+    for (int eg = 0; eg < 2; ++eg) {
+      acc[tg][eg] += moved(acc[tg][eg], 4);
+      acc[tg][eg] += moved(acc[tg][eg], 8);
+      if (wd > 0) lds[wd - 1][tg * 2 + eg][lane] = acc[tg][eg];
+    }
+  __syncthreads();
+  if (wd > 0) return;
+  double* out = part + (int64_t)split * n_tok * E;
+  const int64_t t = tok0 + 4 * b + g;  // lane (g, b, r) stores token 4 b + g, experts r and 4 + r
+#pragma unroll
+  for (int eg = 0; eg < 2; ++eg) {
+    double v = 0.0;
+#pragma unroll
+    for (int tg = 0; tg < 4; ++tg)
+      if (tg == b) v = acc[tg][eg];
+#pragma unroll
+    for (int o = 1; o < WD; ++o) v += lds[o - 1][b * 2 + eg][lane];
+    if (4 * eg + r < E && t < n_tok) out[t * E + 4 * eg + r] = v;
+  }
 }
 
 // ---------------------------------------------------------------- scores and choice
@@ -504,6 +598,7 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
 struct Plan {
   int64_t chunk;  // tokens that go through the two launches at a time
   int S;          // splits of the columns
+  bool few;       // up to 8 experts
   bool large;     // 32 tokens x 32 experts a wave instead of 16 x 16
 };
 
@@ -515,9 +610,11 @@ struct Plan {
 Plan plan(const moe_shape& s) {
   Plan p;
   const int64_t tiles = (s.T + 31) / 32 * ((s.n_experts + 63) / 64);
-  p.large = tiles >= 64;
+  p.few = s.n_experts <= 8;
+  p.large = !p.few && tiles >= 64;
   const int64_t blocks = p.large ? tiles : (s.T + 15) / 16 * ((s.n_experts + 15) / 16);
-  const int64_t most = (s.d_model + 255) / 256;  // at least a quad of 32 columns for each of 8 waves
+  // at least 32 columns for each of 8 waves, or 128 for each of 4
+  const int64_t most = p.few ? (s.d_model + 511) / 512 : (s.d_model + 255) / 256;
   p.S = (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), most, kMaxSplits}));
   p.chunk = std::min<int64_t>(s.T, ((int64_t)64 << 20) / (8 * s.n_experts * p.S) / 32 * 32);
   return p;
@@ -536,6 +633,12 @@ hipError_t launch_logits(const moe_shape& s, const void* x, const void* w, const
 template <typename Chunk>
 hipError_t logits_any(const moe_shape& s, const void* x, const void* w, const Plan& p, int64_t base,
                       int64_t n, double* part, hipStream_t st) {
+  if (p.few) {
+    constexpr int WD = 4;
+    hipLaunchKernelGGL((k_scored_logits_few<Chunk, WD>), dim3((unsigned)((n + 15) / 16), (unsigned)p.S),
+                       dim3(64 * WD), 0, st, x, w, s.T, s.d_model, s.n_experts, p.S, base, n, part);
+    return hipGetLastError();
+  }
   if (!p.large) return launch_logits<Chunk, 1, 1, 8, 1>(s, x, w, p, base, n, part, st);
   if (s.n_experts <= 16) return launch_logits<Chunk, 2, 1, 4, 1>(s, x, w, p, base, n, part, st);
   if (s.n_experts <= 32) return launch_logits<Chunk, 2, 2, 4, 1>(s, x, w, p, base, n, part, st);
