@@ -12,9 +12,9 @@
 // every machine.  A gate is rounded once.
 //
 // Two launches.  k_scored_logits leaves partial logits (fp64, [split][token][expert]) of 16 or 32
-// tokens and 16 to 64 experts a block on v_mfma_f64_16x16x4f64; k_scored_choose adds the splits and
-// does the rest with a wave a token (16 lanes up to 32 experts).  Tokens go through both in chunks,
-// which bounds the workspace.
+// tokens and 16 to 64 experts a block on v_mfma_f64_16x16x4f64, k_scored_logits_few those of up to 8
+// experts on v_mfma_f64_4x4x4f64; k_scored_choose adds the splits and does the rest with a wave or 16
+// lanes a token.  Tokens go through both in chunks, which bounds the workspace.
 #include <algorithm>
 
 #include "math_f64.h"
@@ -329,13 +329,21 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // one that choice c took.
 constexpr uint32_t kLeastKey = 0x00800000u;
 
-// The lanes that hold a token: 16 (a DPP row, for up to 32 experts) or the whole wave.  sum and max in a
+// The lanes that hold a token: 16 (a DPP row, see launch_choose) or the whole wave.  sum and max in a
 // fixed order, every lane gets the result.
 template <int LPT>
 struct Lanes {
+  // the lane move of dpp32, from whose zeros for lanes without a partner (there are none) the compiler
+  // makes one instruction of a move and a maximum
+  template <int CTRL>
+  static __device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+  }
   template <int CTRL>
   static __device__ __forceinline__ double moved(double v) {
-    return __longlong_as_double((long long)dpp64<CTRL>((uint64_t)__double_as_longlong(v)));
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)moved<CTRL>((uint32_t)(u >> 32)) << 32 |
+                                            moved<CTRL>((uint32_t)u)));
   }
   static __device__ __forceinline__ double lane_of(double v, int lane) {
     const uint64_t u = (uint64_t)__double_as_longlong(v);
@@ -362,10 +370,10 @@ struct Lanes {
   }
   static __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
     auto take = [&](uint32_t o) { v = o > v ? o : v; };
-    take(dpp32<0xB1>(v));
-    take(dpp32<0x4E>(v));
-    take(dpp32<0x141>(v));
-    take(dpp32<0x140>(v));
+    take(moved<0xB1>(v));
+    take(moved<0x4E>(v));
+    take(moved<0x141>(v));
+    take(moved<0x140>(v));
     return v;
   }
   // the largest key of the token's lanes, and the lowest lane (of LPT) that has it
@@ -654,8 +662,8 @@ hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
   if (a.E <= 16) return go(k_scored_choose<16, 1>, 16);
   if (a.E <= 32) return go(k_scored_choose<16, 2>, 16);
   // A wave a token is sooner done, 16 lanes take fewer instructions.  us, wave / 16 lanes: E 64, T 64
-  // 3.5 / 4.8, 4096 4.7 / 5.3, 16384 11.0 / 10.1 (with 8 groups 16.1 / 12.1); E 40, top-8, T 65536 52.7
-  // / 31.4.  Above 64 experts 16 lanes hold too many each: E 128, T 16384 15.3 / 24.4.
+  // 3.9 / 4.8, 4096 4.5 / 5.2, 16384 10.3 / 9.9 (with 8 groups 13.5 / 11.9); E 40, top-8, T 65536 42.2
+  // / 25.5.  Above 64 experts 16 lanes hold too many each: E 128, T 16384 14.4 / 24.4.
   if (a.E <= 64 && a.n_tok >= 8192) return go(k_scored_choose<16, 4>, 16);
   if (a.E <= 64) return go(k_scored_choose<64, 1>, 4);
   if (a.E <= 128) return go(k_scored_choose<64, 2>, 4);
