@@ -1446,12 +1446,17 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const 
     if (rows > 0) MOE_TRY(check_data_ptr(s, y_rows, "y_rows"));
     if (overlap(dgates, choices, topk_gates, choices) || overlap(dgates, choices, slot_of, choices))
       return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps topk_gates or slot_of");
+    if (overlap(dgates, choices, dout, (size_t)s.T * row) || overlap(dgates, choices, y_rows, rows))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps dout or y_rows");
   }
   if (dy_rows) {
     MOE_TRY(check_data_ptr(s, dy_rows, "dy_rows"));
     MOE_TRY(check_ptr(topk_gates, 4, "topk_gates"));
     if (overlap(dy_rows, rows, dout, (size_t)s.T * row))
       return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps dout");
+    if (overlap(dy_rows, rows, topk_gates, choices) || overlap(dy_rows, rows, slot_of, choices) ||
+        overlap(dy_rows, rows, dgates, choices))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps topk_gates, slot_of or dgates");
     if (dgates && dy_rows != y_rows && overlap(dy_rows, rows, y_rows, rows))
       return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps y_rows without being it");
   }

@@ -619,7 +619,7 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* 
  *   y_rows     [rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates
  *   dgates     [T, k] fp32 out or NULL
  *   dy_rows    [rows, d_model] dtype out or NULL; rows that no slot names are left as they are.  May be
- *              y_rows itself, must not overlap it otherwise, nor dout
+ *              y_rows itself, must not overlap it otherwise; outputs overlap nothing else
  * At least one output is given.  Products are summed in fp32 in a fixed order: equal calls give equal
  * bits.  T == 0 enqueues nothing. */
 moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const float* topk_gates,

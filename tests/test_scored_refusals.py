@@ -129,6 +129,9 @@ def comb(lib, s=None, **kw):
     (dict(dy=P(4104)), 2, "16-byte"), (dict(dgates=P(4097)), 2, "aligned"),
     (dict(dgates=at(1)), 1, "dgates overlaps"), (dict(dy=at(0)), 1, "dy_rows overlaps dout"),
     (dict(dy=P(at(3).value + 16)), 1, "dy_rows overlaps y_rows"),
+    (dict(dgates=at(0)), 1, "dgates overlaps dout"), (dict(dgates=at(3)), 1, "dgates overlaps dout or y"),
+    (dict(dy=at(1)), 1, "dy_rows overlaps topk_gates"), (dict(dy=at(2)), 1, "slot_of or dgates"),
+    (dict(dgates=at(5)), 1, "slot_of or dgates"),
 ])
 def test_combine_backward_refusals(lib, kw, status, text):
     assert comb(lib, **kw) == status
