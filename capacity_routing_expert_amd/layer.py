@@ -502,7 +502,8 @@ def balance_bias(ids: torch.Tensor, score_bias: torch.Tensor, rate: float,
 class AdamW:
     """AdamW over a list of tensors, all fp32 or all bf16, with moments of 32 or 8 bits that start at
     zero.  copies: bf16 tensors (or None entries) that receive the new fp32 params, for the forward
-    pass."""
+    pass.  Params, gradients and copies are taken where they lie at each step; a saved state is copied
+    into m, v and the steps."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, copies=None):
@@ -520,12 +521,16 @@ class AdamW:
     def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
         """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
         takes their places, for a captured step."""
-        if self.tensors is None:
+        at = lambda t, old: (0 if t is None else t.data_ptr()) == (old or 0)
+        copies = self.copies or [None] * len(self.params)
+        if self.tensors is None or not all(
+                at(p, a.param) and at(c, a.copy)
+                for p, c, a in zip(self.params, copies, self.tensors.array)):
             self.tensors = B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
                                           v_steps=self.v_steps, copies=self.copies,
                                           weight_decay=self.weight_decay)
         elif len(grads) != self.tensors.n or any(
-                g is not old or g.data_ptr() != (a.grad or 0)
+                g is not old or not at(g, a.grad)
                 for g, old, a in zip(grads, self.tensors.grads, self.tensors.array)):
             self.tensors.set_grads(grads)
         B.moe_adamw_step(self.tensors, self.lr, *self.betas, self.eps, self.steps + 1,

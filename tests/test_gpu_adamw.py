@@ -312,6 +312,25 @@ def test_gradients_in_other_storage():
     assert torch.equal(m[0], g) and torch.equal(v[0], g * g)
 
 
+def test_params_and_copies_are_taken_where_they_lie():
+    """So are a param and a copy; what they held before stays as it was left."""
+    p, c = torch.zeros(512, device=DEV), torch.zeros(512, dtype=torch.bfloat16, device=DEV)
+    opt = L.AdamW([p], lr=0.5, betas=(0.0, 0.0), weight_decay=0.0, copies=[c])
+    g = torch.ones(512, device=DEV)
+    opt.step([g])
+    old = [p.data, c.data]
+    left = [t.clone() for t in old]
+    p.data = torch.full((512,), 8.0, device=DEV)
+    opt.step([g])
+    assert bool((p - 7.5).abs().max() < 1e-5) and bool((c == 7.5).all())
+    assert torch.equal(old[0], left[0])
+    left[1].copy_(c)
+    c.data = torch.zeros_like(c)
+    opt.step([g])
+    assert bool((p - 7.0).abs().max() < 1e-5) and bool((c == 7.0).all())
+    assert torch.equal(old[1], left[1]) and opt.steps == 3
+
+
 def test_another_stream():
     c, d = Case([100000], 8, seed=10), Case([100000], 8, seed=10)
     B.moe_adamw_step(c.tensors, step=1, **HYPER)
