@@ -12,10 +12,11 @@
 // every machine.  A gate is rounded once.
 //
 // Two launches.  k_scored_logits leaves partial logits (fp64, [split][token][expert]) of 16 or 32
-// tokens and 16 to 64 experts a block on v_mfma_f64_16x16x4f64, k_scored_logits_few those of up to 8
+// tokens and 16 or 32 experts a block on v_mfma_f64_16x16x4f64, k_scored_logits_few those of up to 8
 // experts on v_mfma_f64_4x4x4f64; k_scored_choose adds the splits and does the rest with a wave or 16
 // lanes a token.  Tokens go through both in chunks, which bounds the workspace.
 #include <algorithm>
+#include <type_traits>
 
 #include "math_f64.h"
 
@@ -29,7 +30,8 @@ constexpr uint32_t kNowhere = 0x80000000u;  // past every array (below 2 GiB), a
 
 // 8 columns of a token or of an expert, as stored.  A load takes a byte offset of the lane (kNowhere:
 // zeros) and one of the wave, so that walking along d costs the vector ALU nothing: it and the fp64
-// matrix instructions take turns.  inside: all of the wave's columns are below d.  widen: columns 4 h .. 4 h + 3 in fp64, exactly.
+// matrix instructions take turns.  inside: all of the wave's columns are below d.  widen: columns
+// 4 h .. 4 h + 3 in fp64, exactly.
 struct ChunkBf16 {  // d % 8 == 0
   typedef bf16_t Elem;
   uint4 v;
@@ -94,27 +96,27 @@ struct ChunkF32 {  // any d: as ChunkF32x4 where all of the wave's columns are i
 };
 
 // ---------------------------------------------------------------- partial logits
-// A block of WD x WE waves takes 16 R tokens and 16 EBG WE experts: wave (wd, we) takes expert tiles
-// we EBG .. of them and every (S WD)-th quad of 32 columns from quad split WD + wd on.  The waves of
-// one we are added in the order of wd, so equal calls give equal bits.  Operands: lane l holds token or
-// expert l % 16 and 8 consecutive columns, 8 (l / 16) of its quad on; instruction s multiplies column s
-// of both, a permutation of the sum's order only.
+// A block of WD waves takes 16 R tokens and 16 EBG experts: wave wd every (S WD)-th quad of 32 columns
+// from quad split WD + wd on.  The waves are added in the order of wd, so equal calls give equal bits.
+// Operands: lane l holds token or expert l % 16 and 8 consecutive columns, 8 (l / 16) of its quad on;
+// instruction s multiplies column s of both, a permutation of the sum's order only.
 // Bound from some thousand tokens on: the fp64 matrix instructions (64 cycles each, 73 TFLOP/s with
 // nothing between) and the conversions, which they do not overlap with: T 65536, E 64, d 2048 281 us, 61
-// TFLOP/s; accumulators in AGPRs would halve the rate.  W_r converted to fp64 by a launch ahead and read
-// in the operands' order: 268 us there, but 73 + 5 against 75 at T 16384.
-template <typename Chunk, int R, int EBG, int WD, int WE>
-__global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
+// TFLOP/s; accumulators in AGPRs would halve the rate.  Two rows of waves for 64 experts a block took as
+// long, and 137 against 90 us for E 80 at T 16384, where they leave half of each last block idle.  W_r
+// converted to fp64 by a launch ahead and read in the operands' order: 268 us at T 65536, but 73 + 5
+// against 75 at T 16384.
+template <typename Chunk, int R, int EBG, int WD>
+__global__ __launch_bounds__(64 * WD) void k_scored_logits(
     const void* __restrict__ x, const void* __restrict__ w, int64_t T, int d, int E, int S,
     int64_t tok_base, int64_t n_tok, double* __restrict__ part) {
   constexpr int kPart = R * EBG * 256;
-  __shared__ double lds[WD > 1 ? (WD - 1) * WE * kPart : 1];
+  __shared__ double lds[WD > 1 ? (WD - 1) * kPart : 1];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int we = wave % WE, wd = wave / WE;
+  const int wd = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, q = lane >> 4;
   const int64_t tok0 = (int64_t)blockIdx.x * (16 * R);  // within the chunk
-  const int e0 = ((int)blockIdx.y * WE + we) * EBG * 16;
+  const int e0 = (int)blockIdx.y * EBG * 16;
   const int split = blockIdx.z;
   constexpr uint32_t kSize = sizeof(typename Chunk::Elem);
   const int nq = (d + 31) / 32, stride = S * WD;
@@ -138,41 +140,49 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
     const int e = e0 + 16 * b + i;
     wo[b] = e < E ? (uint32_t)((int64_t)e * d + q * 8) * kSize : kNowhere;
   }
-  auto load = [&](int cq) {  // columns past d, and whole quads past the last, read as zeros
-    const int col = cq * 32 + q * 8;
-    // within the first row, and so within the array, whose size the lanes' offsets are held against
-    const uint32_t at = cq < nq ? (uint32_t)cq * 32 * kSize : 0u;
+  // The wave's first NB tiles of experts: a tile that is past E is zeros.
+  auto walk = [&](auto tiles) {
+    constexpr int NB = decltype(tiles)::value;
+    auto load = [&](int cq) {  // columns past d, and whole quads past the last, read as zeros
+      const int col = cq * 32 + q * 8;
+      // within the first row, and so within the array, whose size the lanes' offsets are held against
+      const uint32_t at = cq < nq ? (uint32_t)cq * 32 * kSize : 0u;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      xr[r].load(xs, col < d ? xo[r] : kNowhere, at, cq * 32 + 32 <= d, col, d);
+      for (int r = 0; r < R; ++r)
+        xr[r].load(xs, col < d ? xo[r] : kNowhere, at, cq * 32 + 32 <= d, col, d);
 #pragma unroll
-    for (int b = 0; b < EBG; ++b)
-      wr[b].load(ws, col < d ? wo[b] : kNowhere, at, cq * 32 + 32 <= d, col, d);
-  };
-  int cq = split * WD + wd;
-  load(cq);
-  for (; cq < nq; cq += stride) {
-    // half a chunk at a time: 16 registers of widened operands less
+      for (int b = 0; b < NB; ++b)
+        wr[b].load(ws, col < d ? wo[b] : kNowhere, at, cq * 32 + 32 <= d, col, d);
+    };
+    int cq = split * WD + wd;
+    load(cq);
+    for (; cq < nq; cq += stride) {
+      // half a chunk at a time: 16 registers of widened operands less
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      double xa[R][4], wb[EBG][4];
+      for (int h = 0; h < 2; ++h) {
+        double xa[R][4], wb[NB][4];
 #pragma unroll
-      for (int r = 0; r < R; ++r) xr[r].widen(h, xa[r]);
+        for (int r = 0; r < R; ++r) xr[r].widen(h, xa[r]);
 #pragma unroll
-      for (int b = 0; b < EBG; ++b) wr[b].widen(h, wb[b]);
-      if (h == 1) load(cq + stride);
+        for (int b = 0; b < NB; ++b) wr[b].widen(h, wb[b]);
+        if (h == 1) load(cq + stride);
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int b = 0; b < EBG; ++b)
-            acc[r][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[r][s], wb[b][s], acc[r][b], 0, 0, 0);
+            for (int b = 0; b < NB; ++b)
+              acc[r][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[r][s], wb[b][s], acc[r][b], 0, 0, 0);
+      }
     }
-  }
+  };
+  if (EBG == 1 || e0 + 16 < E)
+    walk(std::integral_constant<int, EBG>{});
+  else
+    walk(std::integral_constant<int, 1>{});
   if constexpr (WD > 1) {
     if (wd > 0) {
-      double* mine = lds + ((wd - 1) * WE + we) * kPart;
+      double* mine = lds + (wd - 1) * kPart;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(64 * WD * WE) void k_scored_logits(
     if (wd > 0) return;
 #pragma unroll 1  // all waves' tiles at once would take the registers of a second block on the CU
     for (int o = 1; o < WD; ++o) {
-      const double* other = lds + ((o - 1) * WE + we) * kPart;
+      const double* other = lds + (o - 1) * kPart;
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -607,33 +617,62 @@ struct Plan {
   int64_t chunk;  // tokens that go through the two launches at a time
   int S;          // splits of the columns
   bool few;       // up to 8 experts
-  bool large;     // 32 tokens x 32 experts a wave instead of 16 x 16
+  bool large;     // blocks of 32 tokens x 32 (16) experts instead of 16 x 16
 };
 
-// The large tiles convert each value for two products, and conversions and fp64 products take turns
-// (16 and 64 cycles); the small ones make more blocks.  us, small / large, bf16, both with the columns
-// split until there are 512 blocks: E 64, d 2048: T 1024 9.6 / 9.8, 2048 14.9 / 14.9, 4096 25.4 / 23.4,
-// 16384 89 / 75; E 256, d 4096, T 1024 45.9 / 40.5; T 256, E 64 4.8 / 8.6.  Without splits T 4096, E 64
-// takes 37.9.  At most 64 MiB of partial logits.
+// Large tiles convert each value for two products, and conversions and fp64 products take turns (12
+// and 64 cycles); small tiles and split columns spread more evenly over the CUs.  The least of
+//   (16 x 16 tiles on the CU with most) * (columns of a block) * (us a tile and column)
+// with 15 % more where that is one block alone, 2 us for the longer start and end of a large block, and
+// the partial logits of each split, written and read.  us measured, large tiles and small ones with
+// the splits in brackets, bf16, d 2048: T 16384, E 64 74 (1) and 84 (1); T 16400 89 (1), 78 (3) and 86 (1);
+// T 2048, E 160 37 (1), 28 (4) and 27 (1); T 4096, E 160 55 (1), 48 (2) and 53 (1); T 250, E 64 21 (1),
+// 8.2 (4) and 8.9 (1), 4.4 (4).  At most 64 MiB of partial logits.
 Plan plan(const moe_shape& s) {
-  Plan p;
-  const int64_t tiles = (s.T + 31) / 32 * ((s.n_experts + 63) / 64);
-  p.few = s.n_experts <= 8;
-  p.large = !p.few && tiles >= 64;
-  const int64_t blocks = p.large ? tiles : (s.T + 15) / 16 * ((s.n_experts + 15) / 16);
-  // at least 32 columns for each of 8 waves, or 128 for each of 4
-  const int64_t most = p.few ? (s.d_model + 511) / 512 : (s.d_model + 255) / 256;
-  p.S = (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), most, kMaxSplits}));
-  p.chunk = std::min<int64_t>(s.T, ((int64_t)64 << 20) / (8 * s.n_experts * p.S) / 32 * 32);
+  constexpr int64_t kBytes = (int64_t)64 << 20;
+  constexpr int kCUs = 256;
+  Plan p{0, 1, s.n_experts <= 8, false};
+  const int64_t tokens16 = (s.T + 15) / 16, tokens32 = (s.T + 31) / 32;
+  if (p.few) {  // at least 128 columns for each of 4 waves
+    const int64_t most = (s.d_model + 511) / 512;
+    p.S = (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(tokens16, 1), most, kMaxSplits}));
+  } else {
+    const int quads = (s.d_model + 31) / 32, E16 = (s.n_experts + 15) / 16;
+    const double split_us = 0.1 + (double)(s.T * s.n_experts * 8) * 1e-7;
+    double least = INFINITY;
+    for (int large = 0; large < 2; ++large) {
+      const int waves = large ? 4 : 8;
+      const double us = !large ? 2.45e-3 : E16 == 1 ? 2.3e-3 : 2.15e-3;
+      const int most = std::min((quads + waves - 1) / waves, kMaxSplits);
+      for (int S = 1; S <= most; ++S) {
+        if (S > 1 && s.T * s.n_experts * 8 * S > kBytes) break;
+        int64_t tiles, block = 1;  // on the CU with most, and in a block
+        if (!large) {
+          tiles = (tokens16 * E16 * S + kCUs - 1) / kCUs;
+        } else if (E16 % 2 == 0) {
+          block = 4;
+          tiles = 4 * ((tokens32 * (E16 / 2) * S + kCUs - 1) / kCUs);
+        } else {  // the last block of each 32 tokens has half the experts
+          block = E16 > 1 ? 4 : 2;
+          tiles = std::max<int64_t>(block, 2 * ((tokens32 * E16 * S + kCUs - 1) / kCUs));
+        }
+        const int columns = 32 * waves * ((quads + S * waves - 1) / (S * waves));
+        const double cost = (double)tiles * columns * us * (tiles == block ? 1.15 : 1.0) +
+                            (S - 1) * split_us + (large ? 2.0 : 0.0);
+        if (cost < least) least = cost, p.S = S, p.large = large != 0;
+      }
+    }
+  }
+  p.chunk = std::min<int64_t>(s.T, kBytes / (8 * s.n_experts * p.S) / 32 * 32);
   return p;
 }
 
-template <typename Chunk, int R, int EBG, int WD, int WE>
+template <typename Chunk, int R, int EBG, int WD>
 hipError_t launch_logits(const moe_shape& s, const void* x, const void* w, const Plan& p,
                          int64_t base, int64_t n, double* part, hipStream_t st) {
   const dim3 grid((unsigned)((n + 16 * R - 1) / (16 * R)),
-                  (unsigned)((s.n_experts + 16 * EBG * WE - 1) / (16 * EBG * WE)), (unsigned)p.S);
-  hipLaunchKernelGGL((k_scored_logits<Chunk, R, EBG, WD, WE>), grid, dim3(64 * WD * WE), 0, st, x, w,
+                  (unsigned)((s.n_experts + 16 * EBG - 1) / (16 * EBG)), (unsigned)p.S);
+  hipLaunchKernelGGL((k_scored_logits<Chunk, R, EBG, WD>), grid, dim3(64 * WD), 0, st, x, w,
                      s.T, s.d_model, s.n_experts, p.S, base, n, part);
   return hipGetLastError();
 }
@@ -647,10 +686,9 @@ hipError_t logits_any(const moe_shape& s, const void* x, const void* w, const Pl
                        dim3(64 * WD), 0, st, x, w, s.T, s.d_model, s.n_experts, p.S, base, n, part);
     return hipGetLastError();
   }
-  if (!p.large) return launch_logits<Chunk, 1, 1, 8, 1>(s, x, w, p, base, n, part, st);
-  if (s.n_experts <= 16) return launch_logits<Chunk, 2, 1, 4, 1>(s, x, w, p, base, n, part, st);
-  if (s.n_experts <= 32) return launch_logits<Chunk, 2, 2, 4, 1>(s, x, w, p, base, n, part, st);
-  return launch_logits<Chunk, 2, 2, 4, 2>(s, x, w, p, base, n, part, st);
+  if (!p.large) return launch_logits<Chunk, 1, 1, 8>(s, x, w, p, base, n, part, st);
+  if (s.n_experts <= 16) return launch_logits<Chunk, 2, 1, 4>(s, x, w, p, base, n, part, st);
+  return launch_logits<Chunk, 2, 2, 4>(s, x, w, p, base, n, part, st);
 }
 
 hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {

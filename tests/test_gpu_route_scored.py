@@ -97,6 +97,17 @@ ROUTES = [
     (4100, 40, 100, 4, "bf16", dict(score="sigmoid")),
     (8200, 16, 64, 6, "bf16", dict(n_groups=8, topk_groups=3, group_score="top2", renormalize=True)),
     (8193, 24, 39, 39, "bf16", dict(score="sigmoid", n_groups=3, topk_groups=3, renormalize=True)),
+    # large tiles of 16 and 32 experts, with and without splits, whose last one holds 16 experts or fewer
+    (40001, 520, 12, 2, "bf16", dict(renormalize=True)),
+    (40003, 136, 15, 3, "f32", dict(score="sigmoid", n_groups=5, topk_groups=2)),
+    (40003, 270, 28, 4, "f32", dict(score="sigmoid", renormalize=True)),
+    (4300, 1032, 33, 2, "bf16", dict(n_groups=11, topk_groups=4, group_score="top2")),
+    (9001, 264, 64, 6, "bf16", dict(score="sigmoid", n_groups=8, topk_groups=4, group_score="top2")),
+    (9000, 268, 72, 4, "f32", dict(renormalize=True)),
+    (9001, 264, 80, 8, "bf16", dict(score="sigmoid", renormalize=True, scale=2.5)),
+    (5000, 801, 100, 4, "f32", dict(n_groups=5, topk_groups=3)),
+    # logits of more than 64 MiB: the tokens in two parts
+    (34001, 16, 250, 5, "f32", dict(n_groups=10, topk_groups=3)),
 ]
 
 
