@@ -645,7 +645,7 @@ Plan plan(const moe_shape& s) {
       const double us = !large ? 2.45e-3 : E16 == 1 ? 2.3e-3 : 2.15e-3;
       const int most = std::min((quads + waves - 1) / waves, kMaxSplits);
       for (int S = 1; S <= most; ++S) {
-        if (S > 1 && s.T * s.n_experts * 8 * S > kBytes) break;
+        if (S > 1 && tokens32 * 32 * s.n_experts * 8 * S > kBytes) break;  // one part of tokens
         int64_t tiles, block = 1;  // on the CU with most, and in a block
         if (!large) {
           tiles = (tokens16 * E16 * S + kCUs - 1) / kCUs;

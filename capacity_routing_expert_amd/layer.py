@@ -516,23 +516,20 @@ class AdamW:
         self.m, self.v = like(torch.int8 if q else torch.float32), like(torch.uint8 if q else torch.float32)
         self.m_steps, self.v_steps = (steps(), steps()) if q else (None, None)
         self.params, self.copies, self.weight_decay = list(params), copies, weight_decay
-        self.tensors = None
+        self.tensors = self.here = self.grads_at = None
 
     def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
         """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
         takes their places, for a captured step."""
-        at = lambda t, old: (0 if t is None else t.data_ptr()) == (old or 0)
-        copies = self.copies or [None] * len(self.params)
-        if self.tensors is None or not all(
-                at(p, a.param) and at(c, a.copy)
-                for p, c, a in zip(self.params, copies, self.tensors.array)):
+        where = lambda ts: [0 if t is None else t.data_ptr() for t in ts]
+        here, grads_at = where(self.params) + where(self.copies or []), where(grads)
+        if self.tensors is None or here != self.here:
             self.tensors = B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
                                           v_steps=self.v_steps, copies=self.copies,
                                           weight_decay=self.weight_decay)
-        elif len(grads) != self.tensors.n or any(
-                g is not old or not at(g, a.grad)
-                for g, old, a in zip(grads, self.tensors.grads, self.tensors.array)):
+        elif grads_at != self.grads_at or any(g is not old for g, old in zip(grads, self.tensors.grads)):
             self.tensors.set_grads(grads)
+        self.here, self.grads_at = here, grads_at
         B.moe_adamw_step(self.tensors, self.lr, *self.betas, self.eps, self.steps + 1,
                          grad_scale=grad_scale, dynamic=dynamic)
         self.steps += 1
