@@ -620,6 +620,9 @@ struct Plan {
   bool large;     // blocks of 32 tokens x 32 (16) experts instead of 16 x 16
 };
 
+constexpr int64_t kPartBytes = (int64_t)64 << 20;  // of partial logits at most
+int most_splits(int d, int columns) { return (d + columns - 1) / columns; }
+
 // Large tiles convert each value for two products, and conversions and fp64 products take turns (12
 // and 64 cycles); small tiles and split columns spread more evenly over the CUs.  The least of
 //   (16 x 16 tiles on the CU with most) * (columns of a block) * (us a tile and column)
@@ -627,14 +630,13 @@ struct Plan {
 // the partial logits of each split, written and read.  us measured, large tiles and small ones with
 // the splits in brackets, bf16, d 2048: T 16384, E 64 74 (1) and 84 (1); T 16400 89 (1), 78 (3) and 86 (1);
 // T 2048, E 160 37 (1), 28 (4) and 27 (1); T 4096, E 160 55 (1), 48 (2) and 53 (1); T 250, E 64 21 (1),
-// 8.2 (4) and 8.9 (1), 4.4 (4).  At most 64 MiB of partial logits.
+// 8.2 (4) and 8.9 (1), 4.4 (4).
 Plan plan(const moe_shape& s) {
-  constexpr int64_t kBytes = (int64_t)64 << 20;
   constexpr int kCUs = 256;
   Plan p{0, 1, s.n_experts <= 8, false};
   const int64_t tokens16 = (s.T + 15) / 16, tokens32 = (s.T + 31) / 32;
   if (p.few) {  // at least 128 columns for each of 4 waves
-    const int64_t most = (s.d_model + 511) / 512;
+    const int64_t most = most_splits(s.d_model, 512);
     p.S = (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(tokens16, 1), most, kMaxSplits}));
   } else {
     const int quads = (s.d_model + 31) / 32, E16 = (s.n_experts + 15) / 16;
@@ -643,9 +645,9 @@ Plan plan(const moe_shape& s) {
     for (int large = 0; large < 2; ++large) {
       const int waves = large ? 4 : 8;
       const double us = !large ? 2.45e-3 : E16 == 1 ? 2.3e-3 : 2.15e-3;
-      const int most = std::min((quads + waves - 1) / waves, kMaxSplits);
+      const int most = std::min(most_splits(s.d_model, 32 * waves), kMaxSplits);
       for (int S = 1; S <= most; ++S) {
-        if (S > 1 && tokens32 * 32 * s.n_experts * 8 * S > kBytes) break;  // one part of tokens
+        if (S > 1 && tokens32 * 32 * s.n_experts * 8 * S > kPartBytes) break;  // one part of tokens
         int64_t tiles, block = 1;  // on the CU with most, and in a block
         if (!large) {
           tiles = (tokens16 * E16 * S + kCUs - 1) / kCUs;
@@ -663,7 +665,7 @@ Plan plan(const moe_shape& s) {
       }
     }
   }
-  p.chunk = std::min<int64_t>(s.T, kBytes / (8 * s.n_experts * p.S) / 32 * 32);
+  p.chunk = std::min<int64_t>(s.T, kPartBytes / (8 * s.n_experts * p.S) / 32 * 32);
   return p;
 }
 
@@ -710,9 +712,10 @@ hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// For as many splits as the columns allow, so that no smaller batch of the same kind takes more.
 size_t route_scored_ws_bytes(const moe_shape& s) {
-  const Plan p = plan(s);
-  return ((size_t)p.S * p.chunk * s.n_experts * 8 + 255) & ~(size_t)255;
+  const int most = std::min(most_splits(s.d_model, s.n_experts <= 8 ? 512 : 128), kMaxSplits);
+  return ((size_t)std::min<int64_t>(kPartBytes, s.T * s.n_experts * 8 * most) + 255) & ~(size_t)255;
 }
 
 hipError_t launch_route_scored(const moe_shape& s, const moe_routing& r, const void* x,

@@ -561,7 +561,8 @@ typedef struct {
   float scale;         /* factor of the gates */
 } moe_routing;
 
-/* Workspace bytes for moe_route_scored (at most 64 MiB); 0 for an invalid shape. */
+/* Workspace bytes for moe_route_scored (at most 64 MiB; no less for a larger T, so that one for the
+ * largest batch serves all); 0 for an invalid shape. */
 size_t moe_workspace_bytes_route_scored(const moe_shape* shape);
 
 /* moe_route with other scores.  With l = W_r x + b_r and s the scores of l, an expert is chosen by
@@ -626,7 +627,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const 
                                 const int32_t* slot_of, const void* y_rows, float* dgates,
                                 void* dy_rows, moe_stream_t stream);
 
-/* Workspace bytes for moe_balance_bias; 0 for an invalid shape, and where it needs none. */
+/* Workspace bytes for moe_balance_bias (no less for a larger T); 0 for an invalid shape, and where it
+ * needs none. */
 size_t moe_workspace_bytes_balance_bias(const moe_shape* shape);
 
 /* Update of the selection bias after a batch: with c_e assignments to expert e, over the n experts

@@ -114,6 +114,17 @@ def test_workspaces_are_bounded(lib):
             assert B.workspace_bytes_route_scored(s) % 256 == 0
 
 
+@pytest.mark.parametrize("E", [1, 8, 9, 48, 64, 250])
+@pytest.mark.parametrize("d", [8, 136, 1000, 2048, 8192])
+def test_a_workspace_serves_smaller_batches(lib, E, d):
+    last = [0, 0]
+    for T in sorted({*range(1, 700, 9), *range(700, 70000, 613), 2047, 2048, 16384, 16385, 16400}):
+        now = [B.workspace_bytes_route_scored(shape(T=T, n_experts=E, top_k=1, d_model=d)),
+               B.workspace_bytes_balance_bias(shape(T=T, n_experts=E, top_k=1, d_model=d))]
+        assert now[0] >= last[0] and now[1] >= last[1], T
+        last = now
+
+
 def comb(lib, s=None, **kw):
     a = dict(dout=at(0), gates=at(1), slots=at(2), y=at(3), dgates=at(4), dy=at(5))
     a.update(kw)
