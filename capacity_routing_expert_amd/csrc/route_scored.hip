@@ -578,9 +578,12 @@ __global__ __launch_bounds__(256) void k_scored_choose(const ChooseArgs a) {
     for (int i = 0; i < NV; ++i)
       if (chosen(i)) total += p[i];
     total = W::sum(total);
-    // Scores that the range of fp64 has lost, or nearly: e^l instead, from the largest chosen logit
-    // (1 + e^l is 1 there); all of them zero (-inf): the gates are zero.
-    if (total < 1e-280) {
+    // Scores near the end of fp64's range or below it: e^l instead, from the largest chosen logit (1 + e^l
+    // is 1 there); all of them zero (-inf): the gates are zero.  From 1e-200 on, what the range takes of
+    // a smaller score reaches no gate: exp_clamped's floor (1e-304) and denormal numbers (below 1e-307)
+    // are 1e-104 of the sum at most, which times the largest scale (3.4e38) is nothing in fp32; and
+    // scale / total stays finite.
+    if (total < 1e-200) {
       m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
