@@ -888,14 +888,16 @@ class AdamWTensors:
     fp32, or int8 and uint8 with m_steps and v_steps ([ceil(n / 256)] fp32 each); copies, bf16, are
     written after each step; weight_decay is a number or one per tensor.  Their addresses are taken
     here and in set_grads: a tensor whose storage is exchanged afterwards (`t.data = ...`) has to be
-    handed over again."""
+    handed over again.  grads may be None until set_grads: moe_adamw_moments needs none."""
 
     def __init__(self, params, grads, m, v, m_steps=None, v_steps=None, copies=None,
                  weight_decay=0.0):
         n = len(params)
         quantized = m_steps is not None or v_steps is not None
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
-        lists = {"params": params, "grads": grads, "m": m, "v": v, "weight_decay": decay}
+        lists = {"params": params, "m": m, "v": v, "weight_decay": decay}
+        if grads is not None:
+            lists["grads"] = grads
         for name, x in (("m_steps", m_steps), ("v_steps", v_steps)):
             if quantized:
                 lists[name] = x
@@ -925,7 +927,9 @@ class AdamWTensors:
                 a.copy = self._at(copies[i], f"copies[{i}]", torch.bfloat16, k)
             a.n = k
             a.weight_decay = float(decay[i])
-        self.set_grads(grads)
+        self.grads, self.grad_dtype = None, f32
+        if grads is not None:
+            self.set_grads(grads)
 
     def _one_dtype(self, tensors, name):
         kinds = {t.dtype for t in tensors}

@@ -524,9 +524,7 @@ class AdamW:
         where = lambda ts: [0 if t is None else t.data_ptr() for t in ts]
         here, grads_at = where(self.params) + where(self.copies or []), where(grads)
         if self.tensors is None or here != self.here:
-            self.tensors = B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
-                                          v_steps=self.v_steps, copies=self.copies,
-                                          weight_decay=self.weight_decay)
+            self.tensors = self._list(grads)
         elif grads_at != self.grads_at or any(g is not old for g, old in zip(grads, self.tensors.grads)):
             self.tensors.set_grads(grads)
         self.here, self.grads_at = here, grads_at
@@ -535,9 +533,12 @@ class AdamW:
         self.steps += 1
 
     def moments(self) -> tuple:
-        """The fp32 moments, two lists."""
+        """The fp32 moments that m, v and the steps stand for, two lists."""
         m, v = ([torch.empty(p.numel(), device=p.device) for p in self.params] for _ in range(2))
-        if self.tensors is None:
-            return [x.zero_() for x in m], [x.zero_() for x in v]
-        B.moe_adamw_moments(self.tensors, m, v)
+        B.moe_adamw_moments(self._list(None) if self.tensors is None else self.tensors, m, v)
         return m, v
+
+    def _list(self, grads):
+        return B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,
+                              v_steps=self.v_steps, copies=self.copies,
+                              weight_decay=self.weight_decay)

@@ -1,0 +1,80 @@
+"""The AdamW class of layer.py: what a program does with it between steps."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import scored_ref as S
+from capacity_routing_expert_amd import binding as B
+from capacity_routing_expert_amd import layer as L
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    B.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def stepped(bits, lengths=(300, 1, 0, 1024), steps=3):
+    """An optimiser after some steps, and a fresh one with its state copied in."""
+    g = torch.Generator(device=DEV).manual_seed(bits)
+    make = lambda: L.AdamW([torch.zeros(n, device=DEV) for n in lengths], state_bits=bits)
+    old, new = make(), make()
+    for _ in range(steps):
+        old.step([torch.randn(n, generator=g, device=DEV) for n in lengths])
+    for name in ("params", "m", "v") + (("m_steps", "v_steps") if bits == 8 else ()):
+        for a, b in zip(getattr(new, name), getattr(old, name)):
+            a.copy_(b)
+    new.steps = old.steps
+    return old, new, g
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_of_a_restored_state(bits):
+    """Before the first step, too, moments are those of the state."""
+    old, new, g = stepped(bits)
+    for a, b in zip(old.moments(), new.moments()):
+        assert any(bool(t.any()) for t in a)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    m, v = new.moments()
+    for i, p in enumerate(new.params):
+        if bits == 32:
+            want = new.m[i], new.v[i]
+        else:
+            d = lambda c, s: S.decode(c.cpu().numpy(), s.cpu().numpy())
+            r = d(new.v[i], new.v_steps[i])
+            want = (torch.from_numpy(x).to(DEV) for x in (d(new.m[i], new.m_steps[i]), r * r))
+        assert all(torch.equal(x, y) for x, y in zip((m[i], v[i]), want))
+    assert new.steps == 3  # reading them is no step
+    grads = [torch.randn(p.numel(), generator=g, device=DEV) for p in new.params]
+    old.step(grads)
+    new.step(grads)
+    for name in ("params", "m", "v"):
+        assert all(torch.equal(x, y) for x, y in zip(getattr(old, name), getattr(new, name)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_before_any_state(bits):
+    opt = L.AdamW([torch.ones(300, device=DEV), torch.ones(0, device=DEV)], state_bits=bits)
+    m, v = opt.moments()
+    assert [t.numel() for t in m] == [300, 0] and not any(bool(t.any()) for t in m + v)
+    assert L.AdamW([]).moments() == ([], [])
+
+
+def test_a_list_without_gradients_takes_no_step():
+    z = lambda: torch.zeros(256, device=DEV)
+    t = B.AdamWTensors([z()], None, [z()], [z()])
+    with pytest.raises(B.MoeError, match="grad is NULL"):
+        B.moe_adamw_step(t, 0.1, 0.9, 0.99, 1e-8, 1)
+    g = torch.ones(256, device=DEV)
+    t.set_grads([g])
+    B.moe_adamw_step(t, 0.1, 0.0, 0.0, 1e-8, 1)
+    assert torch.equal(t.m[0], g) and bool((t.params[0] + 0.1).abs().max() < 1e-6)
