@@ -1,0 +1,92 @@
+"""Which tensors a step of the AdamW class of layer.py takes, and what it refuses (no GPU: the addresses
+are host tensors', and the step itself is recorded instead of launched)."""
+import os
+
+import pytest
+import torch
+
+from capacity_routing_expert_amd import binding as B
+from capacity_routing_expert_amd import layer as L
+
+
+@pytest.fixture
+def steps(monkeypatch):
+    """The entries that each step was called with; host tensors pass for the GPU's."""
+    if not os.path.exists(B.LIB_PATH):
+        from capacity_routing_expert_amd import build
+        build.build()
+    real, taken = B._ptr, []
+
+    def ptr(t, name, dtype=None, device=None, numel=None):
+        try:
+            return real(t, name, dtype, device, numel)
+        except ValueError as e:
+            if "must be on the GPU" not in str(e):
+                raise
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def step(tensors, *args, **kw):
+        taken.append([dict(param=a.param, grad=a.grad, m=a.m, v=a.v, copy=a.copy, n=a.n, wd=a.weight_decay,
+                           params=tensors.param_dtype, grads=tensors.grad_dtype)
+                      for a in tensors.array[:tensors.n]])
+
+    monkeypatch.setattr(B, "_ptr", ptr)
+    monkeypatch.setattr(B, "moe_adamw_step", step)
+    return taken
+
+
+def make(copies=False, **kw):
+    params = [torch.zeros(16, 16), torch.zeros(300)]
+    return L.AdamW(params, copies=[torch.zeros(16, 16, dtype=torch.bfloat16), None] if copies else None,
+                   **kw), [torch.ones(16, 16), torch.ones(300)]
+
+
+# ways to look at a tensor's storage from the same address that a step must not take as before
+VIEWS = {"transposed": lambda t: t.t(), "shorter": lambda t: t.flatten()[:100],
+         "strided": lambda t: t.flatten()[::2],
+         "retyped": lambda t: t.view(torch.int32 if t.element_size() == 4 else torch.int16)}
+
+
+@pytest.mark.parametrize("view", sorted(VIEWS))
+@pytest.mark.parametrize("which", ["param", "grad", "copy"])
+def test_another_view_at_the_same_address(steps, view, which):
+    opt, grads = make(copies=True)
+    opt.step(grads)
+    t = {"param": opt.params, "grad": grads, "copy": opt.copies}[which][0]
+    before, at = t.data, t.data_ptr()
+    t.data = VIEWS[view](before)
+    assert t.data_ptr() == at
+    with pytest.raises((ValueError, TypeError)):
+        opt.step(grads)
+    assert len(steps) == 1 and opt.steps == 1
+    t.data = before
+    opt.step(grads)
+    assert steps[1] == steps[0] and opt.steps == 2
+
+
+def test_gradients_of_another_type_at_the_same_address(steps):
+    """As many bf16 gradients in the storage of the fp32 ones are taken as what they are."""
+    opt, grads = make()
+    opt.step(grads)
+    for g in grads:
+        g.data = g.data.flatten().view(torch.bfloat16)[:g.numel()]
+    opt.step(grads)
+    assert all(s["grads"] is torch.float32 for s in steps[0])
+    assert all(s["grads"] is torch.bfloat16 for s in steps[1])
+    assert [s["grad"] for s in steps[0]] == [s["grad"] for s in steps[1]]
+
+
+def test_storage_that_was_exchanged(steps):
+    opt, grads = make(copies=True)
+    opt.step(grads)
+    for t in (opt.params[1], grads[0], opt.copies[0]):
+        t.data = t.data.clone()
+    opt.step(grads)
+    assert [s["param"] for s in steps[1]] == [p.data_ptr() for p in opt.params]
+    assert [s["grad"] for s in steps[1]] == [g.data_ptr() for g in grads]
+    assert [s["copy"] for s in steps[1]] == [opt.copies[0].data_ptr(), None]
+    new = [g.clone() for g in grads]
+    opt.step(new)
+    assert [s["grad"] for s in steps[2]] == [g.data_ptr() for g in new]

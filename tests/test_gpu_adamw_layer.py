@@ -78,3 +78,27 @@ def test_a_list_without_gradients_takes_no_step():
     t.set_grads([g])
     B.moe_adamw_step(t, 0.1, 0.0, 0.0, 1e-8, 1)
     assert torch.equal(t.m[0], g) and bool((t.params[0] + 0.1).abs().max() < 1e-6)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_another_view_at_the_same_address(bits):
+    """A transposed, shorter or retyped tensor is refused or read as what it is."""
+    p, c = torch.zeros(16, 16, device=DEV), torch.zeros(16, 16, dtype=torch.bfloat16, device=DEV)
+    g = torch.ones(16, 16, device=DEV)
+    opt = L.AdamW([p], lr=0.5, betas=(0.0, 0.0), weight_decay=0.0, state_bits=bits, copies=[c])
+    opt.step([g])
+    for t in (p, g, c):
+        whole = t.data
+        for view in (whole.t(), whole.flatten()[:100]):
+            t.data = view
+            with pytest.raises(ValueError):
+                opt.step([g])
+        t.data = whole
+    assert bool((p + 0.5).abs().max() < 1e-6) and torch.equal(c.float(), p) and opt.steps == 1
+    half = torch.full((16, 32), -1.0, dtype=torch.bfloat16, device=DEV)
+    g.data = half.view(torch.float32)
+    opt.step([g])  # garbage, but its own 256 numbers
+    p.zero_()
+    g.data = half[:8]
+    opt.step([g])
+    assert bool((p - 0.5).abs().max() < 1e-6)
