@@ -944,15 +944,24 @@ class AdamWTensors:
         return p
 
     def set_grads(self, grads):
-        """Other gradients for the steps to come; checks that all tensors are apart."""
+        """Other gradients for the steps to come; checks that all tensors are apart.  Those that are
+        refused leave the list as it was."""
         if len(grads) != self.n:
             raise ValueError(f"grads has {len(grads)} entries, params {self.n}")
-        self.grad_dtype = self._one_dtype(grads, "grads")
-        self.grads = list(grads)
-        for i, g in enumerate(grads):
-            self.array[i].grad = self._at(g, f"grads[{i}]", self.grad_dtype, self.params[i].numel())
+        dtype = self._one_dtype(grads, "grads")
+        at = [self._at(g, f"grads[{i}]", dtype, self.params[i].numel()) for i, g in enumerate(grads)]
+        old = self.grads, self.grad_dtype, [a.grad for a in self.array]
+        self.grads, self.grad_dtype = list(grads), dtype
+        for a, p in zip(self.array, at):
+            a.grad = p
         c = self.config(0.0, 0.0, 0.0, 1.0, 1, 1.0, None)
-        _check(lib().moe_adamw_check(ctypes.byref(c), self.array, self.n), "moe_adamw_check")
+        try:
+            _check(lib().moe_adamw_check(ctypes.byref(c), self.array, self.n), "moe_adamw_check")
+        except MoeError:
+            self.grads, self.grad_dtype = old[:2]
+            for a, p in zip(self.array, old[2]):
+                a.grad = p
+            raise
 
     def config(self, lr, beta1, beta2, eps, step, grad_scale, dynamic):
         code = lambda t: MOE_BF16 if t is torch.bfloat16 else MOE_F32

@@ -90,3 +90,32 @@ def test_storage_that_was_exchanged(steps):
     new = [g.clone() for g in grads]
     opt.step(new)
     assert [s["grad"] for s in steps[2]] == [g.data_ptr() for g in new]
+
+
+def test_a_refused_step_leaves_no_address_behind(steps):
+    """Gradients in a param's storage are refused; the next step takes those that are there then."""
+    opt, grads = make()
+    opt.step(grads)
+    before = grads[0].data
+    grads[0].data = opt.params[0].data
+    with pytest.raises(B.MoeError, match="overlaps"):
+        opt.step(grads)
+    grads[0].data = before
+    opt.step(grads)
+    assert len(steps) == 2 and steps[1] == steps[0]
+
+
+def test_refused_gradients_leave_the_list_as_it_was(steps):
+    p, m, v = torch.zeros(300), torch.zeros(300), torch.zeros(300)
+    g = torch.ones(300, dtype=torch.bfloat16)
+    t = B.AdamWTensors([p, torch.zeros(4)], [g, torch.ones(4, dtype=torch.bfloat16)], [m, torch.zeros(4)],
+                       [v, torch.zeros(4)])
+    held = list(t.grads)
+    for bad, error in (([v, torch.ones(4)], B.MoeError), ([torch.ones(300), torch.ones(3)], ValueError),
+                       ([torch.ones(300), torch.ones(4).bfloat16()], TypeError), ([g], ValueError)):
+        with pytest.raises(error):
+            t.set_grads(bad)
+        B.moe_adamw_step(t)
+        assert [e["grad"] for e in steps[-1]] == [x.data_ptr() for x in held]
+        assert steps[-1][0]["grads"] is torch.bfloat16
+        assert all(x is y for x, y in zip(t.grads, held))
