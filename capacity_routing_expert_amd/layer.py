@@ -530,7 +530,9 @@ class AdamW:
     def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
         """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
         takes their places, for a captured step."""
-        here, grads_at = (_as_they_lie(self.params), _as_they_lie(self.copies or [])), _as_they_lie(grads)
+        decay = list(self.weight_decay) if isinstance(self.weight_decay, (list, tuple)) else self.weight_decay
+        here = _as_they_lie(self.params), _as_they_lie(self.copies or []), decay
+        grads_at = _as_they_lie(grads)
         if self.tensors is None or here != self.here:
             self.tensors = self._list(grads)
         elif grads_at != self.grads_at or any(g is not old for g, old in zip(grads, self.tensors.grads)):

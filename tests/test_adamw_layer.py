@@ -119,3 +119,16 @@ def test_refused_gradients_leave_the_list_as_it_was(steps):
         assert [e["grad"] for e in steps[-1]] == [x.data_ptr() for x in held]
         assert steps[-1][0]["grads"] is torch.bfloat16
         assert all(x is y for x, y in zip(t.grads, held))
+
+
+def test_weight_decay_that_was_changed(steps):
+    """It takes effect at the next step, as lr, betas and eps do: a number, a list, an entry of it."""
+    opt, grads = make(weight_decay=0.5)
+    opt.step(grads)
+    opt.weight_decay = 0.25
+    opt.step(grads)
+    opt.weight_decay = [0.125, 0.0]
+    opt.step(grads)
+    opt.weight_decay[1] = 1.0
+    opt.step(grads)
+    assert [[e["wd"] for e in s] for s in steps] == [[0.5, 0.5], [0.25, 0.25], [0.125, 0.0], [0.125, 1.0]]
