@@ -512,7 +512,7 @@ class AdamW:
     """AdamW over a list of tensors, all fp32 or all bf16, with moments of 32 or 8 bits that start at
     zero.  copies: bf16 tensors (or None entries) that receive the new fp32 params, for the forward
     pass.  Params, gradients and copies are taken as they lie at each step; a saved state is copied
-    into m, v and the steps."""
+    into m, v and the steps (m, v, m_steps, v_steps) or its tensors are put into these lists."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, copies=None):
@@ -525,19 +525,19 @@ class AdamW:
         self.m, self.v = like(torch.int8 if q else torch.float32), like(torch.uint8 if q else torch.float32)
         self.m_steps, self.v_steps = (steps(), steps()) if q else (None, None)
         self.params, self.copies, self.weight_decay = list(params), copies, weight_decay
-        self.tensors = self.here = self.grads_at = None
+        self.tensors = self.here = self.grads_at = self.state_held = None
 
     def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
         """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
         takes their places, for a captured step."""
         decay = list(self.weight_decay) if isinstance(self.weight_decay, (list, tuple)) else self.weight_decay
         here = _as_they_lie(self.params), _as_they_lie(self.copies or []), decay
-        grads_at = _as_they_lie(grads)
-        if self.tensors is None or here != self.here:
+        grads_at, state = _as_they_lie(grads), self._state()
+        if self.tensors is None or here != self.here or state != self.state_held:
             self.tensors = self._list(grads)
         elif grads_at != self.grads_at or any(g is not old for g, old in zip(grads, self.tensors.grads)):
             self.tensors.set_grads(grads)
-        self.here, self.grads_at = here, grads_at
+        self.here, self.grads_at, self.state_held = here, grads_at, state
         B.moe_adamw_step(self.tensors, self.lr, *self.betas, self.eps, self.steps + 1,
                          grad_scale=grad_scale, dynamic=dynamic)
         self.steps += 1
@@ -545,8 +545,13 @@ class AdamW:
     def moments(self) -> tuple:
         """The fp32 moments that m, v and the steps stand for, two lists."""
         m, v = ([torch.empty(p.numel(), device=p.device) for p in self.params] for _ in range(2))
-        B.moe_adamw_moments(self._list(None) if self.tensors is None else self.tensors, m, v)
+        held = self.tensors is not None and self._state() == self.state_held
+        B.moe_adamw_moments(self.tensors if held else self._list(None), m, v)
         return m, v
+
+    def _state(self):
+        """Which tensors the state is; self.tensors keeps those that it was made of."""
+        return [list(map(id, x or ())) for x in (self.m, self.v, self.m_steps, self.v_steps)]
 
     def _list(self, grads):
         return B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,

@@ -132,3 +132,28 @@ def test_weight_decay_that_was_changed(steps):
     opt.weight_decay[1] = 1.0
     opt.step(grads)
     assert [[e["wd"] for e in s] for s in steps] == [[0.5, 0.5], [0.25, 0.25], [0.125, 0.0], [0.125, 1.0]]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_that_was_put_in_place(steps, monkeypatch, bits):
+    """Tensors put into m, v or the steps, one or all, are the state from then on, as before the first
+    step; so are copies that are given later."""
+    read = []
+    monkeypatch.setattr(B, "moe_adamw_moments", lambda t, m, v: read.append([(a.m, a.v) for a in t.array[:t.n]]))
+    opt, grads = make(state_bits=bits)
+    opt.step(grads)
+    opt.m[0] = opt.m[0].clone()
+    opt.v = [t.clone() for t in opt.v]
+    if bits == 8:
+        opt.m_steps[1] = opt.m_steps[1].clone()
+    opt.moments()
+    opt.step(grads)
+    want = [(m.data_ptr(), v.data_ptr()) for m, v in zip(opt.m, opt.v)]
+    assert read == [want] and [(e["m"], e["v"]) for e in steps[1]] == want
+    if bits == 8:
+        assert opt.tensors.array[1].m_steps == opt.m_steps[1].data_ptr()
+    opt.copies = [torch.zeros(16, 16, dtype=torch.bfloat16), None]
+    opt.step(grads)
+    opt.copies = None
+    opt.step(grads)
+    assert [steps[i][0]["copy"] is None for i in range(4)] == [True, True, False, True]
