@@ -511,8 +511,8 @@ def _as_they_lie(tensors) -> tuple:
 class AdamW:
     """AdamW over a list of tensors, all fp32 or all bf16, with moments of 32 or 8 bits that start at
     zero.  copies: bf16 tensors (or None entries) that receive the new fp32 params, for the forward
-    pass.  Params, gradients and copies are taken as they lie at each step; a saved state is copied
-    into m, v and the steps (m, v, m_steps, v_steps) or its tensors are put into these lists."""
+    pass.  All are taken as they lie at each step; a saved state is copied into m, v and the steps (m_steps,
+    v_steps), or its tensors are put into these lists."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, copies=None):
@@ -550,8 +550,8 @@ class AdamW:
         return m, v
 
     def _state(self):
-        """Which tensors the state is; self.tensors keeps those that it was made of."""
-        return [list(map(id, x or ())) for x in (self.m, self.v, self.m_steps, self.v_steps)]
+        """Where the state lies."""
+        return [list(map(torch.Tensor.data_ptr, x or ())) for x in (self.m, self.v, self.m_steps, self.v_steps)]
 
     def _list(self, grads):
         return B.AdamWTensors(self.params, grads, self.m, self.v, m_steps=self.m_steps,

@@ -144,6 +144,7 @@ def test_a_state_that_was_put_in_place(steps, monkeypatch, bits):
     opt.step(grads)
     opt.m[0] = opt.m[0].clone()
     opt.v = [t.clone() for t in opt.v]
+    opt.m[1].data = opt.m[1].data.clone()
     if bits == 8:
         opt.m_steps[1] = opt.m_steps[1].clone()
     opt.moments()
