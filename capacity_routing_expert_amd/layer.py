@@ -519,17 +519,19 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits is {state_bits}, not 8 or 32")
         self.lr, self.betas, self.eps, self.steps = lr, betas, eps, 0
+        params = list(params)
         like = lambda dt: [torch.zeros(p.numel(), dtype=dt, device=p.device) for p in params]
         steps = lambda: [torch.zeros((p.numel() + 255) // 256, device=p.device) for p in params]
         q = state_bits == 8
         self.m, self.v = like(torch.int8 if q else torch.float32), like(torch.uint8 if q else torch.float32)
         self.m_steps, self.v_steps = (steps(), steps()) if q else (None, None)
-        self.params, self.copies, self.weight_decay = list(params), copies, weight_decay
+        self.params, self.copies, self.weight_decay = params, copies, weight_decay
         self.tensors = self.here = self.grads_at = self.state_held = None
 
     def step(self, grads, grad_scale: float = 1.0, dynamic: torch.Tensor | None = None):
         """One step with `grads`, one per param.  dynamic [4] on the device (lr, grad_scale, step, skip)
         takes their places, for a captured step."""
+        grads = list(grads)
         decay = list(self.weight_decay) if isinstance(self.weight_decay, (list, tuple)) else self.weight_decay
         here = _as_they_lie(self.params), _as_they_lie(self.copies or []), decay
         grads_at, state = _as_they_lie(grads), self._state()

@@ -158,3 +158,12 @@ def test_a_state_that_was_put_in_place(steps, monkeypatch, bits):
     opt.copies = None
     opt.step(grads)
     assert [steps[i][0]["copy"] is None for i in range(4)] == [True, True, False, True]
+
+
+def test_params_and_gradients_of_an_iterator(steps):
+    params = [torch.zeros(4), torch.zeros(300)]
+    opt = L.AdamW(iter(params), state_bits=8)
+    assert [t.numel() for t in opt.v] == [4, 300] and [t.numel() for t in opt.v_steps] == [1, 2]
+    for _ in range(2):
+        opt.step(torch.ones_like(p) for p in params)
+    assert [e["param"] for e in steps[1]] == [p.data_ptr() for p in params]
