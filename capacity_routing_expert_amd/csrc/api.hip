@@ -394,6 +394,41 @@ moe_status check_adamw(const moe_adamw_config* config, const moe_adamw_tensor* t
   return MOE_OK;
 }
 
+// Slots from bound on count as dropped; the row arrays are held apart over their n_rows rows.
+moe_status combine_backward(const moe_shape& s, const void* dout, const float* topk_gates,
+                            const int32_t* slot_of, const void* y_rows, int64_t n_rows,
+                            int64_t bound, float* dgates, void* dy_rows, hipStream_t st) {
+  if (!dgates && !dy_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dgates and dy_rows are both NULL");
+  if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or enqueue
+  MOE_TRY(check_data_ptr(s, dout, "dout"));
+  MOE_TRY(check_ptr(slot_of, 4, "slot_of"));
+  const size_t row = (size_t)s.d_model * elem_bytes(s), rows = (size_t)n_rows * row;
+  const size_t choices = (size_t)s.T * s.top_k * 4;
+  if (dgates) {
+    MOE_TRY(check_ptr(dgates, 4, "dgates"));
+    if (rows > 0 || y_rows) MOE_TRY(check_data_ptr(s, y_rows, "y_rows"));
+    if (overlap(dgates, choices, topk_gates, choices) || overlap(dgates, choices, slot_of, choices))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps topk_gates or slot_of");
+    if (overlap(dgates, choices, dout, (size_t)s.T * row) || overlap(dgates, choices, y_rows, rows))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps dout or y_rows");
+  }
+  if (dy_rows) {
+    MOE_TRY(check_data_ptr(s, dy_rows, "dy_rows"));
+    MOE_TRY(check_ptr(topk_gates, 4, "topk_gates"));
+    if (overlap(dy_rows, rows, dout, (size_t)s.T * row))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps dout");
+    if (overlap(dy_rows, rows, topk_gates, choices) || overlap(dy_rows, rows, slot_of, choices) ||
+        overlap(dy_rows, rows, dgates, choices))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps topk_gates, slot_of or dgates");
+    if (dgates && dy_rows != y_rows && overlap(dy_rows, rows, y_rows, rows))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps y_rows without being it");
+  }
+  hipError_t err =
+      launch_combine_backward(s, dout, topk_gates, slot_of, y_rows, bound, dgates, dy_rows, st);
+  return err == hipSuccess ? MOE_OK : device_error(err, "combine backward");
+}
+
 moe_status check_forward_args(const moe_shape* shape, const void* x, const void* w_router,
                               const float* b_router, const void* w1, const void* b1,
                               const void* w2, const void* b2, void* out, void* ws,
@@ -1433,36 +1468,9 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const 
                                 const int32_t* slot_of, const void* y_rows, float* dgates,
                                 void* dy_rows, moe_stream_t stream) {
   MOE_TRY(check_shape(shape));
-  const moe_shape& s = *shape;
-  if (!dgates && !dy_rows)
-    return fail(MOE_ERR_INVALID_ARGUMENT, "dgates and dy_rows are both NULL");
-  if (s.T == 0) return MOE_OK;  // empty batch: nothing to check or enqueue
-  MOE_TRY(check_data_ptr(s, dout, "dout"));
-  MOE_TRY(check_ptr(slot_of, 4, "slot_of"));
-  const size_t row = (size_t)s.d_model * elem_bytes(s), rows = (size_t)max_rows(s) * row;
-  const size_t choices = (size_t)s.T * s.top_k * 4;
-  if (dgates) {
-    MOE_TRY(check_ptr(dgates, 4, "dgates"));
-    if (rows > 0) MOE_TRY(check_data_ptr(s, y_rows, "y_rows"));
-    if (overlap(dgates, choices, topk_gates, choices) || overlap(dgates, choices, slot_of, choices))
-      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps topk_gates or slot_of");
-    if (overlap(dgates, choices, dout, (size_t)s.T * row) || overlap(dgates, choices, y_rows, rows))
-      return fail(MOE_ERR_INVALID_ARGUMENT, "dgates overlaps dout or y_rows");
-  }
-  if (dy_rows) {
-    MOE_TRY(check_data_ptr(s, dy_rows, "dy_rows"));
-    MOE_TRY(check_ptr(topk_gates, 4, "topk_gates"));
-    if (overlap(dy_rows, rows, dout, (size_t)s.T * row))
-      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps dout");
-    if (overlap(dy_rows, rows, topk_gates, choices) || overlap(dy_rows, rows, slot_of, choices) ||
-        overlap(dy_rows, rows, dgates, choices))
-      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps topk_gates, slot_of or dgates");
-    if (dgates && dy_rows != y_rows && overlap(dy_rows, rows, y_rows, rows))
-      return fail(MOE_ERR_INVALID_ARGUMENT, "dy_rows overlaps y_rows without being it");
-  }
-  hipError_t err = launch_combine_backward(s, dout, topk_gates, slot_of, y_rows, dgates, dy_rows,
-                                           (hipStream_t)stream);
-  return err == hipSuccess ? MOE_OK : device_error(err, "combine backward");
+  return combine_backward(*shape, dout, topk_gates, slot_of, y_rows, max_rows(*shape),
+                          (int64_t)shape->n_experts * shape->capacity, dgates, dy_rows,
+                          (hipStream_t)stream);
 }
 
 size_t moe_workspace_bytes_balance_bias(const moe_shape* shape) {

@@ -24,6 +24,7 @@ struct CombineBackArgs {
   void* dy;       // may be NULL
   int64_t T;
   int d, k;
+  uint32_t rows;  // of y and dy; a slot past them is a dropped choice's, as -1 is
 };
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -98,6 +99,7 @@ __global__ __launch_bounds__(256) void k_combine_back(const CombineBackArgs a) {
 #pragma unroll
     for (int j = 0; j < kB; ++j) {
       slot[j] = c0 + j < a.k ? a.slot_of[t * a.k + c0 + j] : -1;
+      if ((uint32_t)slot[j] >= a.rows) slot[j] = -1;
       gate[j] = DY && slot[j] >= 0 ? a.gates[t * a.k + c0 + j] : 0.0f;
       acc[j] = 0.0f;
       // the row of a dropped choice has no bytes: it reads as zeros
@@ -151,15 +153,15 @@ hipError_t launch(const CombineBackArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_combine_backward(const moe_shape& s, const void* dout, const float* gates,
-                                   const int32_t* slot_of, const void* y, float* dgates, void* dy,
-                                   hipStream_t st) {
+                                   const int32_t* slot_of, const void* y, int64_t rows,
+                                   float* dgates, void* dy, hipStream_t st) {
   const size_t size = s.dtype == MOE_BF16 ? 2 : 4, row = (size_t)s.d_model * size;
   constexpr int64_t kTokens = 1 << 25;  // a launch: 64 threads each, and 2^32 are too many
   for (int64_t t = 0; t < s.T; t += kTokens) {
     const int64_t n = s.T - t < kTokens ? s.T - t : kTokens;
     const CombineBackArgs a{(const char*)dout + t * row, gates ? gates + t * s.top_k : nullptr,
                             slot_of + t * s.top_k, y, dgates ? dgates + t * s.top_k : nullptr, dy, n,
-                            s.d_model, s.top_k};
+                            s.d_model, s.top_k, (uint32_t)(rows < INT32_MAX ? rows : INT32_MAX)};
     const uintptr_t all = (uintptr_t)dout | (uintptr_t)y | (uintptr_t)dy;
     hipError_t err;
     if (s.dtype == MOE_BF16)

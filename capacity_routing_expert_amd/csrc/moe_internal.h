@@ -278,10 +278,11 @@ size_t balance_bias_ws_bytes(const moe_shape& s);
 hipError_t launch_balance_bias(const moe_shape& s, const int32_t* ids, const uint8_t* mask,
                                float rate, float* bias, int32_t* counts, void* ws, hipStream_t st);
 
-// ---- backward pass of the combine (combine_backward.hip): dgates with y, dy with gates; T > 0
+// ---- backward pass of the combine (combine_backward.hip): dgates with y, dy with gates; T > 0; slots
+// that are not in [0, rows) are dropped ones
 hipError_t launch_combine_backward(const moe_shape& s, const void* dout, const float* gates,
-                                   const int32_t* slot_of, const void* y, float* dgates, void* dy,
-                                   hipStream_t st);
+                                   const int32_t* slot_of, const void* y, int64_t rows,
+                                   float* dgates, void* dy, hipStream_t st);
 
 // ---- AdamW (adamw.hip); m_out, v_out or their entries may be NULL
 hipError_t launch_adamw(const moe_adamw_config& c, const moe_adamw_tensor* ts, int n,

@@ -617,11 +617,12 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* 
  *   topk_gates [T, k] fp32 in; NULL without dy_rows
  *   slot_of    [T, k] int32 in, as moe_combine takes it (either layout), -1 for dropped; no two
  *              assignments share a slot
- *   y_rows     [rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates
+ *   y_rows     [rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates, or without rows
  *   dgates     [T, k] fp32 out or NULL
  *   dy_rows    [rows, d_model] dtype out or NULL; rows that no slot names are left as they are.  May be
  *              y_rows itself, must not overlap it otherwise; outputs overlap nothing else
- * At least one output is given.  Products are summed in fp32 in a fixed order: equal calls give equal
+ * At least one output is given.  A slot of n_experts * capacity or more counts as dropped, so with
+ * capacity 0 no row is looked at.  Products are summed in fp32 in a fixed order: equal calls give equal
  * bits.  T == 0 enqueues nothing. */
 moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const float* topk_gates,
                                 const int32_t* slot_of, const void* y_rows, float* dgates,
