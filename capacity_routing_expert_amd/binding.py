@@ -37,7 +37,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_bytes", "moe_max_kept_rows", "moe_stat
            "moe_quantized_scales_bytes", "moe_quantize_weights", "moe_dequantize_weights",
            "moe_expert_ffn_quantized", "moe_layer_forward_quantized",
            "moe_workspace_bytes_route_scored", "moe_route_scored", "moe_route_scored_backward",
-           "moe_combine_backward", "moe_workspace_bytes_balance_bias", "moe_balance_bias", "moe_adamw_check",
+           "moe_combine_backward", "moe_combine_backward_rows", "moe_workspace_bytes_balance_bias", "moe_balance_bias", "moe_adamw_check",
            "moe_adamw_step", "moe_adamw_moments")
 
 
@@ -182,6 +182,8 @@ def lib() -> ctypes.CDLL:
         L.moe_route_scored_backward.argtypes = [SP, RP] + [P] * 7
         # shape, dout, gates, slot_of, y_rows, dgates, dy_rows, stream
         L.moe_combine_backward.argtypes = [SP] + [P] * 7
+        # shape, dout, gates, slot_of, y_rows, n_rows, dgates, dy_rows, stream
+        L.moe_combine_backward_rows.argtypes = [SP] + [P] * 4 + [I64] + [P] * 3
         # shape, topk_ids, token_mask, rate, score_bias, counts, ws, ws_bytes, stream
         L.moe_balance_bias.argtypes = [SP, P, P, ctypes.c_float, P, P, P, SZ, P]
         CP, TP = ctypes.POINTER(MoeAdamWConfig), ctypes.POINTER(MoeAdamWTensor)
@@ -190,7 +192,7 @@ def lib() -> ctypes.CDLL:
         # config, tensors, n, m_out, v_out, stream
         L.moe_adamw_moments.argtypes = [CP, TP, I32, P, P, P]
         for name in ("moe_route_scored", "moe_route_scored_backward", "moe_combine_backward",
-                     "moe_balance_bias", "moe_adamw_check", "moe_adamw_step", "moe_adamw_moments",
+                     "moe_combine_backward_rows", "moe_balance_bias", "moe_adamw_check", "moe_adamw_step", "moe_adamw_moments",
                      "moe_quantize_weights", "moe_dequantize_weights", "moe_expert_ffn_quantized",
                      "moe_layer_forward_quantized", "moe_balance_loss", "moe_route_backward", "moe_route", "moe_dispatch", "moe_expert_ffn", "moe_combine",
                      "moe_layer_forward", "moe_layer_forward_profiled", "moe_layer_forward_padded",
@@ -848,16 +850,22 @@ def moe_route_scored_backward(shape, routing, logits, topk_ids, dgates, dlogits,
 def moe_combine_backward(shape, dout, topk_gates, slot_of, y_rows, dgates=None, dy_rows=None,
                          stream=None):
     """Gradients of moe_combine: dgates [T, k] fp32 (needs y_rows) and dy_rows (needs topk_gates),
-    each optional; y_rows and dy_rows hold every row that a slot names."""
+    each optional.  slot_of in either layout: y_rows and dy_rows hold moe_max_kept_rows rows, or the
+    padded layout's n_experts * capacity; a slot past what they hold counts as dropped."""
     dt, T, d, k = _dtype_of(shape), shape.T, shape.d_model, shape.top_k
-    rows = min(T * k, shape.n_experts * shape.capacity)  # moe_max_kept_rows
+    padded = shape.n_experts * shape.capacity
+    rows = min(T * k, padded)  # moe_max_kept_rows
     dev = _device()
-    _check(lib().moe_combine_backward(
+    y, dy = _cur(dev, y_rows, "y_rows", dt, rows * d), _cur(dev, dy_rows, "dy_rows", dt, rows * d)
+    held = [t.numel() // d for t in (None if dgates is None else y_rows, dy_rows) if t is not None]
+    if held:
+        rows = min(*held, max(T * k, padded), 2 ** 31 - 1)
+    _check(lib().moe_combine_backward_rows(
         ctypes.byref(shape), _cur(dev, dout, "dout", dt, T * d),
         _cur(dev, topk_gates, "topk_gates", torch.float32, T * k),
-        _cur(dev, slot_of, "slot_of", torch.int32, T * k), _cur(dev, y_rows, "y_rows", dt, rows * d),
-        _cur(dev, dgates, "dgates", torch.float32, T * k),
-        _cur(dev, dy_rows, "dy_rows", dt, rows * d), _stream(stream, dev)), "moe_combine_backward")
+        _cur(dev, slot_of, "slot_of", torch.int32, T * k), y, rows,
+        _cur(dev, dgates, "dgates", torch.float32, T * k), dy, _stream(stream, dev)),
+        "moe_combine_backward")
 
 
 def workspace_bytes_balance_bias(shape: MoeShape) -> int:

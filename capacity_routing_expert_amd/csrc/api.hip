@@ -1473,6 +1473,18 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const 
                           (hipStream_t)stream);
 }
 
+moe_status moe_combine_backward_rows(const moe_shape* shape, const void* dout,
+                                     const float* topk_gates, const int32_t* slot_of,
+                                     const void* y_rows, int64_t n_rows, float* dgates,
+                                     void* dy_rows, moe_stream_t stream) {
+  MOE_TRY(check_shape(shape));
+  if (n_rows < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "n_rows = %lld < 0", (long long)n_rows);
+  if (n_rows >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "n_rows = %lld >= 2^31", (long long)n_rows);
+  return combine_backward(*shape, dout, topk_gates, slot_of, y_rows, n_rows, n_rows, dgates,
+                          dy_rows, (hipStream_t)stream);
+}
+
 size_t moe_workspace_bytes_balance_bias(const moe_shape* shape) {
   if (check_shape(shape) != MOE_OK) return 0;
   return balance_bias_ws_bytes(*shape);

@@ -615,18 +615,28 @@ moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* 
  * (the residual's part of dx is dout itself).
  *   dout       [T, d_model] dtype in: gradient on moe_combine's out
  *   topk_gates [T, k] fp32 in; NULL without dy_rows
- *   slot_of    [T, k] int32 in, as moe_combine takes it (either layout), -1 for dropped; no two
- *              assignments share a slot
- *   y_rows     [rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates, or without rows
+ *   slot_of    [T, k] int32 in, moe_dispatch's, -1 for dropped; no two assignments share a slot
+ *   y_rows     [moe_max_kept_rows, d_model] dtype in, moe_expert_ffn's; NULL without dgates, or without
+ *              rows
  *   dgates     [T, k] fp32 out or NULL
- *   dy_rows    [rows, d_model] dtype out or NULL; rows that no slot names are left as they are.  May be
- *              y_rows itself, must not overlap it otherwise; outputs overlap nothing else
+ *   dy_rows    [moe_max_kept_rows, d_model] dtype out or NULL; rows that no slot names are left as they
+ *              are.  May be y_rows itself, must not overlap it otherwise; outputs overlap nothing else
  * At least one output is given.  A slot of n_experts * capacity or more counts as dropped, so with
  * capacity 0 no row is looked at.  Products are summed in fp32 in a fixed order: equal calls give equal
  * bits.  T == 0 enqueues nothing. */
 moe_status moe_combine_backward(const moe_shape* shape, const void* dout, const float* topk_gates,
                                 const int32_t* slot_of, const void* y_rows, float* dgates,
                                 void* dy_rows, moe_stream_t stream);
+
+/* The same over y_rows and dy_rows of n_rows rows each, whatever the layout: the padded one's
+ * n_experts * capacity (moe_layer_forward_padded's slot_of and y_rows), or as many as the buffers hold.
+ * A slot that is not in [0, n_rows) counts as dropped, and no other row is read or written.
+ * shape->capacity is not looked at.  MOE_ERR_INVALID_ARGUMENT also for n_rows < 0, MOE_ERR_UNSUPPORTED
+ * for n_rows >= 2^31. */
+moe_status moe_combine_backward_rows(const moe_shape* shape, const void* dout,
+                                     const float* topk_gates, const int32_t* slot_of,
+                                     const void* y_rows, int64_t n_rows, float* dgates,
+                                     void* dy_rows, moe_stream_t stream);
 
 /* Workspace bytes for moe_balance_bias (no less for a larger T); 0 for an invalid shape, and where it
  * needs none. */
