@@ -512,7 +512,8 @@ class AdamW:
     """AdamW over a list of tensors, all fp32 or all bf16, with moments of 32 or 8 bits that start at
     zero.  copies: bf16 tensors (or None entries) that receive the new fp32 params, for the forward
     pass.  All are taken as they lie at each step; a saved state is copied into m, v and the steps (m_steps,
-    v_steps), or its tensors are put into these lists."""
+    v_steps), or its tensors are put into these lists.  8 bits suit tensors whose gradients go on: an
+    element whose gradient ends while others of its 256 go on keeps a small m, and moves (moe.h)."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, copies=None):
