@@ -601,8 +601,9 @@ moe_status moe_route_scored(const moe_shape* shape, const moe_routing* routing, 
  *   token_mask  [T] uint8 or NULL: 0 marks a token that is not there; nothing of its rows is read, its
  *               dlogits row is zero
  *   dlogits     [T, E] fp32 out; must not overlap logits
- * fp32 throughout.  Reads shape->T, n_experts and top_k, routing->score, renormalize and scale.  Equal
- * calls give equal bits.  T == 0 enqueues nothing. */
+ * fp32 throughout.  Computes with shape->T, n_experts and top_k, routing->score, renormalize and scale;
+ * the routing is refused as by moe_route_scored, fields of its groups included, so that it is the one
+ * that made the gates.  Equal calls give equal bits.  T == 0 enqueues nothing. */
 moe_status moe_route_scored_backward(const moe_shape* shape, const moe_routing* routing,
                                      const float* logits, const int32_t* topk_ids,
                                      const float* dgates, const float* dlogits_add,
