@@ -402,10 +402,6 @@ struct Lanes {
     }
     return m;
   }
-  static __device__ __forceinline__ uint32_t from(uint32_t v, int lane) {
-    if constexpr (LPT == 64) return __builtin_amdgcn_readlane(v, __builtin_amdgcn_readfirstlane(lane));
-    return (uint32_t)__shfl((int)v, lane, LPT);
-  }
 };
 
 // The two largest keys of two pairs (best >= second).
