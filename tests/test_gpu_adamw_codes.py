@@ -1,6 +1,7 @@
 """8-bit moments over many steps, codes to the code: gradients that end, in a block where others go on."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -24,3 +25,23 @@ def test_gradients_that_end(lengths):
         B.moe_adamw_step(c.tensors, step=step, **HYPER)
         c.check(want)
     assert all(bool((m[::3] != 0).any()) for m in c.m)  # small codes stay
+
+
+@pytest.mark.parametrize("dynamic", [False, True])
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_params_with_fp32_moments(grad, dynamic):
+    """Seven half steps of the update, two fewer than the reference's bound, which holds for 8 bits' hardware
+    roots and reciprocals too: rate, its product with m, the root, its factor, their sum, the quotient,
+    one for the second order."""
+    c = Case([100003, 257], 32, grad=grad, seed=13)
+    for step in (1, 5):
+        before = [c.host(i)[0].astype(np.float64) for i in range(2)]
+        want = c.expect(step)
+        dyn = torch.tensor([HYPER["lr"], 1.0, step, 0.0], device=DEV) if dynamic else None
+        B.moe_adamw_step(c.tensors, step=step, dynamic=dyn, **HYPER)
+        c.check(want)
+        lr = float(np.float32(HYPER["lr"]))
+        for i, (p, bound, _, _) in enumerate(want):
+            up = before[i] - lr * float(np.float32(c.wd[i])) * before[i] - p
+            got = c.p[i].double().cpu().numpy()
+            assert np.all(np.abs(got - p) <= bound - 2 * 2.0 ** -24 * np.abs(up)), i
