@@ -853,18 +853,21 @@ def moe_combine_backward(shape, dout, topk_gates, slot_of, y_rows, dgates=None, 
     each optional.  slot_of in either layout: y_rows and dy_rows hold moe_max_kept_rows rows, or the
     padded layout's n_experts * capacity; a slot past what they hold counts as dropped."""
     dt, T, d, k = _dtype_of(shape), shape.T, shape.d_model, shape.top_k
-    padded = shape.n_experts * shape.capacity
-    rows = min(T * k, padded)  # moe_max_kept_rows
+    n, padded = T * k, shape.n_experts * shape.capacity
+    rows, most = (n, padded) if n < padded else (padded, n)  # moe_max_kept_rows, and of any layout
     dev = _device()
     y, dy = _cur(dev, y_rows, "y_rows", dt, rows * d), _cur(dev, dy_rows, "dy_rows", dt, rows * d)
-    held = [t.numel() // d for t in (None if dgates is None else y_rows, dy_rows) if t is not None]
-    if held:
-        rows = min(*held, max(T * k, padded), 2 ** 31 - 1)
+    if y is not None and dgates is not None:
+        rows = min(most, y_rows.numel() // d, 0x7FFFFFFF)
+        if dy is not None:
+            rows = min(rows, dy_rows.numel() // d)
+    elif dy is not None:
+        rows = min(most, dy_rows.numel() // d, 0x7FFFFFFF)
     _check(lib().moe_combine_backward_rows(
         ctypes.byref(shape), _cur(dev, dout, "dout", dt, T * d),
-        _cur(dev, topk_gates, "topk_gates", torch.float32, T * k),
-        _cur(dev, slot_of, "slot_of", torch.int32, T * k), y, rows,
-        _cur(dev, dgates, "dgates", torch.float32, T * k), dy, _stream(stream, dev)),
+        _cur(dev, topk_gates, "topk_gates", torch.float32, n),
+        _cur(dev, slot_of, "slot_of", torch.int32, n), y, rows,
+        _cur(dev, dgates, "dgates", torch.float32, n), dy, _stream(stream, dev)),
         "moe_combine_backward")
 
 
