@@ -478,7 +478,7 @@ def route_scored_backward(logits: torch.Tensor, ids: torch.Tensor, dgates: torch
                           token_mask: torch.Tensor | None = None) -> torch.Tensor:
     """dlogits [T, E], which route_backward takes on (its dgates then being None)."""
     T, E = logits.shape
-    shape = B.make_shape(T, 8, 8, E, ids.shape[1], 0, B.MOE_F32)
+    shape = B.make_shape(T, 1, 1, E, ids.shape[1], 0, B.MOE_F32)
     dlogits = torch.empty_like(logits)
     B.moe_route_scored_backward(shape, routing, logits, ids, dgates, dlogits,
                                 dlogits_add=dlogits_add, token_mask=token_mask)
@@ -491,7 +491,7 @@ def balance_bias(ids: torch.Tensor, score_bias: torch.Tensor, rate: float,
     """Moves score_bias [E] towards even counts of ids [T, k], in place; returns the counts [E]."""
     T, k = ids.shape
     E = score_bias.numel()
-    shape = B.make_shape(T, 8, 8, E, k, 0, B.MOE_F32)
+    shape = B.make_shape(T, 1, 1, E, k, 0, B.MOE_F32)
     if ws is None:
         ws = torch.empty(max(B.workspace_bytes_balance_bias(shape), 256), dtype=torch.uint8,
                          device=score_bias.device)
