@@ -22,10 +22,10 @@
 // fp32 moments.  A block whose gradients end together decays as it should, by its steps.
 //
 // Bound: memory, 28 bytes an element for fp32 moments and gradients, 14 to 18 for 8 bits: 268 million
-// elements with bf16 gradients 1148 us (6.1 TB/s), 37.8 million at 8 bits with copies 105 us (5.7 TB/s; with
-// each load behind the branch for odd tensors 115).  The tensors'
-// addresses go along as kernel arguments, 64 or 48 to a launch; a block takes 1024 elements of one
-// tensor, a thread 4 neighbours, so that a wave has exactly the 256 that share a step.
+// elements with bf16 gradients 1145 to 1220 us (5.7 to 6.1 TB/s), 37.8 million at 8 bits with copies 105
+// us (5.7 TB/s; with each load behind the branch for odd tensors 115).  The tensors' addresses go along
+// as kernel arguments, 64 or 48 to a launch; a block takes 1024 elements of one tensor, a thread 4
+// neighbours, so that a wave has exactly the 256 that share a step.
 #include <math.h>
 
 #include <type_traits>
